@@ -285,6 +285,131 @@ fsdp_status fsdp_unflatten(const fsdp_unit* unit, fsdp_dtype src_dtype, fsdp_dty
                            const void* const* shards, void* const* tensors,
                            hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The sharded Muon step, and the RMS norm of a unit's blocks.
+ *
+ * Muon updates a matrix with the orthogonalised momentum instead of the
+ * momentum itself. Sharded over F ranks a step is: every rank folds the
+ * gradient rows into its window of the momentum and emits the window of the
+ * bf16 update (fsdp_reduce_momentum_shard); the windows are gathered into whole
+ * matrices (fsdp_cast_unflatten); the matrices are orthogonalised
+ * (fsdp_orthogonalize); every rank applies its window of the result to its
+ * master weights (fsdp_muon_apply_shard). Persistent state is fp32 master and
+ * momentum: 8 bytes a parameter of the window beside the bf16 parameter and
+ * gradient, against AdamW's 12.
+ * ------------------------------------------------------------------------- */
+
+typedef struct {
+  double lr;            /* finite, >= 0 */
+  double momentum;      /* in [0, 1) */
+  double weight_decay;  /* finite; decoupled, scaled by lr */
+  double grad_scale;    /* finite; multiplies the fp32 sum (1/n_grads = mean) */
+  int32_t nesterov;     /* 0 or 1 */
+  int32_t reserved;
+} fsdp_muon_hparams;
+
+/* The ranks' gradients reduced as by fsdp_reduce_shard (same fold, same
+ * grad_scale), into this rank's window of the momentum. For i < shard_valid, one
+ * binary32 operation per step:
+ *   g = reduced gradient;  m' = momentum*m + g;
+ *   update[i] = bf16_rne(nesterov ? g + momentum*m' : m').
+ * `momentum`: fp32, in place. `update_bf16_out`: shard_valid bf16 outputs. lr and
+ * weight_decay are checked and not used. */
+fsdp_status fsdp_reduce_momentum_shard(const fsdp_unit* unit, int32_t n_grads,
+                                       const void* const* grads, float* momentum,
+                                       void* update_bf16_out, const fsdp_muon_hparams* hp,
+                                       hipStream_t stream);
+
+/* This rank's window of whole bf16 update tensors, applied to its master
+ * weights in place. For window element i, which is element j of tensor t:
+ *   p' = p - lr*(fp32(scales[t])*widen(tensors[t][j]) + wd*p);
+ *   param[i] = bf16_rne(p').
+ * `tensors_bf16`, `scales`: host arrays of T entries; entries of tensors that do
+ * not reach into the window are not looked at. `param_bf16_out`: NULL, or
+ * shard_valid bf16 outputs. One launch per 64 tensors of the window; if the
+ * runtime refuses a launch, the launches before it stay enqueued. */
+fsdp_status fsdp_muon_apply_shard(const fsdp_unit* unit, const void* const* tensors_bf16,
+                                  const double* scales, float* master, void* param_bf16_out,
+                                  const fsdp_muon_hparams* hp, hipStream_t stream);
+
+/* Orthogonalises n_mats matrices by Newton-Schulz products. With X the matrix or
+ * its transpose, whichever has no more rows than columns:
+ *   X_0 = X / (|X|_F + eps);  S = X X^T;  X <- (a I + b S + c S S) X, `steps` times,
+ * (a, b, c) = coeffs; out is X in the input's orientation, in bf16.
+ * `mats` (of `dtype`) and `outs` (bf16): host arrays of device pointers to
+ * row-major rows[i] x cols[i] matrices with row pitches mat_ld[i] and out_ld[i]
+ * in elements; any element alignment. Matrices with no elements are skipped.
+ * Products are of fp16 operands with fp32 sums: an element of X is held to 2^-11
+ * relative (2^-36 absolute), so the result of the usual 5 steps is within about
+ * 1.5e-3 (2-norm) of the exact polynomial's before its rounding to bf16; X, its
+ * powers of 2 scaled away, has to stay below 16 and S below 64, which holds for
+ * any matrix with coefficients whose polynomial keeps [0, 1.3] below 4. A matrix
+ * with a NaN or an infinity gives NaN. The same inputs give the same bits.
+ * `workspace`: device memory, 256-byte aligned, of fsdp_orthogonalize_workspace
+ * bytes for the same sizes; its contents need not be kept from call to call.
+ * 1 <= steps <= 64; sides up to 2^20. The call enqueues 3 launches a step and 2
+ * more per 24 matrices; if the runtime refuses one, those before it stay. */
+fsdp_status fsdp_orthogonalize_workspace(int32_t n_mats, const int64_t* rows, const int64_t* cols,
+                                         int64_t* bytes);
+fsdp_status fsdp_orthogonalize(int32_t n_mats, fsdp_dtype dtype, const void* const* mats,
+                               const int64_t* rows, const int64_t* cols, const int64_t* mat_ld,
+                               void* const* outs, const int64_t* out_ld, void* workspace,
+                               int64_t workspace_bytes, int32_t steps, const double* coeffs,
+                               double eps, hipStream_t stream);
+
+/* RMS norm of `rows` rows of `dim` elements, with the residual's addition:
+ *   h = x, or with a residual h = x + residual rounded to dtype, written to residual_out;
+ *   rstd = 1/sqrt(mean(h*h) + eps);  y = h*rstd*weight   (fp32);
+ *   out = y rounded to dtype; with `scales` instead
+ *   scale = max(max|y| / 448, 2^-126),  out = e4m3_rne(clamp(y / scale, -448, 448)).
+ * A NaN in a row gives a NaN scale and a row of NaN. Every row argument has its
+ * own pitch in elements (>= dim); rows and pointers may have any element
+ * alignment. rows < 2^22, dim <= 2^24. rows == 0 is a no-op. */
+typedef struct {
+  const void* x;
+  const void* residual;       /* NULL: none */
+  const void* weight;         /* dim elements of dtype */
+  void* residual_out;         /* with residual */
+  void* out;                  /* dtype, or e4m3 bytes with scales */
+  float* rstd;                /* rows, or NULL */
+  float* scales;              /* rows, or NULL: out in dtype */
+  int64_t rows, dim;
+  int64_t x_pitch, residual_pitch, residual_out_pitch, out_pitch;
+  double eps;                 /* finite, >= 0 */
+  fsdp_dtype dtype;
+  int32_t reserved;
+} fsdp_rms_norm_args;
+fsdp_status fsdp_rms_norm(const fsdp_rms_norm_args* args, hipStream_t stream);
+
+/* Gradients of fsdp_rms_norm's y with respect to h (= x here) and weight. With
+ * xhat = x*rstd and g = dy*weight, in fp32:
+ *   dx = rstd*(g - xhat*mean(g*xhat)) [+ dresidual]   rounded to dtype;
+ *   dweight = sum over rows of dy*xhat                rounded to dtype.
+ * x is what was normed (residual_out where there was a residual), rstd the
+ * forward's. dresidual (or NULL) is the gradient that reaches residual_out from
+ * elsewhere; dx is then the gradient of both x and residual. dweight may be
+ * NULL; otherwise `workspace` (device memory, 16-byte aligned) has
+ * fsdp_rms_norm_backward_workspace bytes. Sums are joined in a fixed order: the
+ * same inputs give the same bits. rows == 0 gives a dweight of zeros. Two
+ * launches (three for dim > 2^14); if the runtime refuses one, those before stay. */
+typedef struct {
+  const void* dy;
+  const void* x;
+  const void* weight;
+  const float* rstd;
+  const void* dresidual;      /* NULL: none */
+  void* dx;
+  void* dweight;              /* dim elements of dtype, or NULL */
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t rows, dim;
+  int64_t dy_pitch, x_pitch, dresidual_pitch, dx_pitch;
+  fsdp_dtype dtype;
+  int32_t reserved;
+} fsdp_rms_norm_backward_args;
+fsdp_status fsdp_rms_norm_backward_workspace(int64_t rows, int64_t dim, int64_t* bytes);
+fsdp_status fsdp_rms_norm_backward(const fsdp_rms_norm_backward_args* args, hipStream_t stream);
+
 const char* fsdp_status_string(fsdp_status status);
 const char* fsdp_last_error(void);
 

@@ -19,6 +19,15 @@ Names follow the C ABI in include/fsdp_shard.h:
 * ``reduce_shard_bf16acc`` / ``reduce_adamw_shard_bf16acc`` -> bf16 partial sums
 * ``cast_unflatten(unit, shards, outs)``    -> fsdp_cast_unflatten (bf16 outputs)
 * ``unflatten(unit, shards, outs)``         -> fsdp_unflatten (dtypes from the tensors)
+* ``reduce_momentum_shard(unit, grads, momentum, update, hp)``
+                                            -> fsdp_reduce_momentum_shard
+* ``orthogonalize(mats, outs, workspace)`` / ``orthogonalize_workspace(mats)``
+                                            -> fsdp_orthogonalize
+* ``muon_apply_shard(unit, tensors, scales, master, param_out, hp)``
+                                            -> fsdp_muon_apply_shard
+* ``rms_norm(x, weight, out, ...)``         -> fsdp_rms_norm
+* ``rms_norm_backward(dy, x, weight, rstd, dx, dweight, workspace, ...)``
+                                            -> fsdp_rms_norm_backward
 """
 
 from __future__ import annotations
@@ -33,7 +42,9 @@ __all__ = [
     "FsdpError", "Unit", "AdamWHparams", "flatten_pad", "reduce_shard", "adamw_shard",
     "reduce_adamw_shard", "reduce_adamw_units", "UnitsStep", "cast_unflatten", "unflatten",
     "reduce_shard_hybrid", "reduce_adamw_shard_hybrid", "reduce_shard_bf16acc",
-    "reduce_adamw_shard_bf16acc", "abi_version", "library_path",
+    "reduce_adamw_shard_bf16acc", "MuonHparams", "reduce_momentum_shard", "muon_apply_shard",
+    "orthogonalize", "orthogonalize_workspace", "rms_norm", "rms_norm_backward",
+    "rms_norm_backward_workspace", "abi_version", "library_path",
     "F32", "BF16",
 ]
 
@@ -71,6 +82,33 @@ class _Hparams(ctypes.Structure):
                 ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
                 ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
                 ("step", ctypes.c_int64)]
+
+
+class _MuonHparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("nesterov", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _NormArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("residual_out", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("x_pitch", ctypes.c_int64), ("residual_pitch", ctypes.c_int64),
+                ("residual_out_pitch", ctypes.c_int64), ("out_pitch", ctypes.c_int64),
+                ("eps", ctypes.c_double), ("dtype", ctypes.c_int), ("reserved", ctypes.c_int32)]
+
+
+class _NormBackwardArgs(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("x", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("dresidual", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("dweight", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("dy_pitch", ctypes.c_int64), ("x_pitch", ctypes.c_int64),
+                ("dresidual_pitch", ctypes.c_int64), ("dx_pitch", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("reserved", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -111,6 +149,19 @@ def _load():
                                                  ctypes.POINTER(_Hparams), vp]),
         "fsdp_reduce_adamw_shard_hybrid": (st, [vp, i32, _c_void_p_p, vp, vp, vp, vp,
                                                 ctypes.POINTER(_Hparams), vp]),
+        "fsdp_reduce_momentum_shard": (st, [vp, i32, _c_void_p_p, vp, vp,
+                                            ctypes.POINTER(_MuonHparams), vp]),
+        "fsdp_muon_apply_shard": (st, [vp, _c_void_p_p, ctypes.POINTER(ctypes.c_double), vp, vp,
+                                       ctypes.POINTER(_MuonHparams), vp]),
+        "fsdp_orthogonalize_workspace": (st, [i32, ctypes.POINTER(i64), ctypes.POINTER(i64),
+                                              ctypes.POINTER(i64)]),
+        "fsdp_orthogonalize": (st, [i32, st, _c_void_p_p, ctypes.POINTER(i64),
+                                    ctypes.POINTER(i64), ctypes.POINTER(i64), _c_void_p_p,
+                                    ctypes.POINTER(i64), vp, i64, i32,
+                                    ctypes.POINTER(ctypes.c_double), ctypes.c_double, vp]),
+        "fsdp_rms_norm": (st, [ctypes.POINTER(_NormArgs), vp]),
+        "fsdp_rms_norm_backward_workspace": (st, [i64, i64, ctypes.POINTER(i64)]),
+        "fsdp_rms_norm_backward": (st, [ctypes.POINTER(_NormBackwardArgs), vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -382,3 +433,171 @@ def cast_unflatten(unit: Unit, shards, outs, stream=None):
     if outs and outs[0].dtype != torch.bfloat16:
         raise TypeError("cast_unflatten writes bf16 tensors; use unflatten for fp32 outputs")
     unflatten(unit, shards, outs, stream)
+
+
+# --- the sharded Muon step ------------------------------------------------------------------
+
+
+@dataclass
+class MuonHparams:
+    lr: float = 0.02
+    momentum: float = 0.95
+    nesterov: bool = True
+    weight_decay: float = 0.0
+
+    def _c(self, grad_scale: float = 0.0) -> _MuonHparams:
+        return _MuonHparams(self.lr, self.momentum, self.weight_decay, grad_scale,
+                            1 if self.nesterov else 0, 0)
+
+
+def reduce_momentum_shard(unit: Unit, grads, momentum: torch.Tensor, update: torch.Tensor,
+                          hp: MuonHparams, grad_scale: float | None = None, stream=None):
+    """The gradient rows reduced into this rank's momentum; ``update``: its bf16 update."""
+    ptrs = _grad_ptrs(unit, grads)
+    c = hp._c(1.0 / len(grads) if grad_scale is None else float(grad_scale))
+    m = _dev(momentum, torch.float32, "momentum", unit.shard_valid)
+    u = _dev(update, torch.bfloat16, "update", unit.shard_valid)
+    _check(_lib.fsdp_reduce_momentum_shard(unit.handle, len(ptrs), _ptr_array(ptrs), m, u,
+                                           ctypes.byref(c), _stream(stream, momentum.device)))
+
+
+def muon_apply_shard(unit: Unit, tensors, scales, master: torch.Tensor,
+                     param_out: torch.Tensor | None, hp: MuonHparams, stream=None):
+    """This rank's window of the whole update tensors, each times its scale, applied to its
+    master weights (and the bf16 parameter)."""
+    if len(tensors) != unit.n_tensors or len(scales) != unit.n_tensors:
+        raise ValueError(f"need {unit.n_tensors} tensors and scales, got {len(tensors)} and "
+                         f"{len(scales)}")
+    ptrs = [_dev(t, torch.bfloat16, f"tensors[{i}]", n) for i, (t, n) in
+            enumerate(zip(tensors, unit.numels))]
+    p = _dev(master, torch.float32, "master", unit.shard_valid)
+    w = None if param_out is None else _dev(param_out, torch.bfloat16, "param_out",
+                                            unit.shard_valid)
+    c = hp._c()
+    _check(_lib.fsdp_muon_apply_shard(unit.handle, _ptr_array(ptrs),
+                                      (ctypes.c_double * len(scales))(*scales), p, w,
+                                      ctypes.byref(c), _stream(stream, master.device)))
+
+
+def _dev_rows(t: torch.Tensor, dtype: torch.dtype, name: str, shape=None):
+    """A 2-d device tensor with contiguous rows: pointer and row pitch in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        want = "2-d" if shape is None else f"of shape {tuple(shape)}"
+        raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+
+
+def _i64_array(values):
+    return (ctypes.c_int64 * max(1, len(values)))(*values)
+
+
+def orthogonalize_workspace(mats) -> int:
+    """Bytes of device workspace that ``orthogonalize`` needs for matrices of these shapes."""
+    need = ctypes.c_int64()
+    _check(_lib.fsdp_orthogonalize_workspace(
+        len(mats), _i64_array([m.shape[0] for m in mats]),
+        _i64_array([m.shape[1] for m in mats]), ctypes.byref(need)))
+    return need.value
+
+
+def orthogonalize(mats, outs, workspace: torch.Tensor, steps: int = 5,
+                  coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, stream=None):
+    """Newton-Schulz orthogonalisation of 2-d matrices (all bf16 or all fp32) into bf16 ``outs``.
+
+    ``workspace``: a device byte tensor of ``orthogonalize_workspace(mats)`` bytes."""
+    if len(outs) != len(mats):
+        raise ValueError(f"need {len(mats)} outputs, got {len(outs)}")
+    if len(coeffs) != 3:
+        raise ValueError("coeffs must be three numbers")
+    if not mats:
+        return
+    dtype = mats[0].dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("matrices must be float32 or bfloat16")
+    src = [_dev_rows(m, dtype, f"mats[{i}]") for i, m in enumerate(mats)]
+    dst = [_dev_rows(o, torch.bfloat16, f"outs[{i}]", m.shape)
+           for i, (o, m) in enumerate(zip(outs, mats))]
+    ws = _dev(workspace, torch.uint8, "workspace")
+    _check(_lib.fsdp_orthogonalize(
+        len(mats), F32 if dtype == torch.float32 else BF16, _ptr_array([p for p, _ in src]),
+        _i64_array([m.shape[0] for m in mats]), _i64_array([m.shape[1] for m in mats]),
+        _i64_array([ld for _, ld in src]), _ptr_array([p for p, _ in dst]),
+        _i64_array([ld for _, ld in dst]), ws, workspace.numel(), int(steps),
+        (ctypes.c_double * 3)(*coeffs), float(eps), _stream(stream, mats[0].device)))
+
+
+# --- RMS norm -------------------------------------------------------------------------------
+
+
+def _norm_type(x: torch.Tensor):
+    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("x must be a float32 or bfloat16 tensor")
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-d (rows, dim), got {tuple(x.shape)}")
+    return F32 if x.dtype == torch.float32 else BF16
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, eps: float = 1e-6,
+             residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+             rstd: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """``out`` = the RMS norm of x's rows (of x + residual, which goes to ``residual_out``)
+    times weight: in x's type, or in e4m3 (torch.float8_e4m3fn) with a scale a row in ``scales``.
+    ``rstd`` (fp32, a value a row) is kept for the backward pass."""
+    code = _norm_type(x)
+    rows, dim = x.shape
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out go together")
+    a = _NormArgs(rows=rows, dim=dim, eps=float(eps), dtype=code)
+    a.x, a.x_pitch = _dev_rows(x, x.dtype, "x")
+    a.weight = _dev(weight, x.dtype, "weight", dim)
+    a.out, a.out_pitch = _dev_rows(out, x.dtype if scales is None else torch.float8_e4m3fn,
+                                   "out", x.shape)
+    if residual is not None:
+        a.residual, a.residual_pitch = _dev_rows(residual, x.dtype, "residual", x.shape)
+        a.residual_out, a.residual_out_pitch = _dev_rows(residual_out, x.dtype, "residual_out",
+                                                         x.shape)
+    if rstd is not None:
+        a.rstd = _dev(rstd, torch.float32, "rstd", rows)
+    if scales is not None:
+        a.scales = _dev(scales, torch.float32, "scales", rows)
+    _check(_lib.fsdp_rms_norm(ctypes.byref(a), _stream(stream, x.device)))
+
+
+def rms_norm_backward_workspace(rows: int, dim: int) -> int:
+    """Bytes of device workspace that ``rms_norm_backward`` needs."""
+    need = ctypes.c_int64()
+    _check(_lib.fsdp_rms_norm_backward_workspace(int(rows), int(dim), ctypes.byref(need)))
+    return need.value
+
+
+def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                      rstd: torch.Tensor, dx: torch.Tensor, dweight: torch.Tensor | None,
+                      workspace: torch.Tensor | None, dresidual: torch.Tensor | None = None,
+                      stream=None):
+    """Gradients of ``rms_norm``: dx (plus dresidual, the gradient that reaches the summed
+    residual from elsewhere) and dweight (None: not computed, and no workspace needed)."""
+    code = _norm_type(x)
+    rows, dim = x.shape
+    a = _NormBackwardArgs(rows=rows, dim=dim, dtype=code)
+    a.dy, a.dy_pitch = _dev_rows(dy, x.dtype, "dy", x.shape)
+    a.x, a.x_pitch = _dev_rows(x, x.dtype, "x")
+    a.weight = _dev(weight, x.dtype, "weight", dim)
+    a.rstd = _dev(rstd, torch.float32, "rstd", rows)
+    a.dx, a.dx_pitch = _dev_rows(dx, x.dtype, "dx", x.shape)
+    if dresidual is not None:
+        a.dresidual, a.dresidual_pitch = _dev_rows(dresidual, x.dtype, "dresidual", x.shape)
+    if dweight is not None:
+        a.dweight = _dev(dweight, x.dtype, "dweight", dim)
+        if workspace is not None:
+            a.workspace = _dev(workspace, torch.uint8, "workspace")
+            a.workspace_bytes = workspace.numel()
+    _check(_lib.fsdp_rms_norm_backward(ctypes.byref(a), _stream(stream, x.device)))

@@ -1,7 +1,8 @@
 """Builds libfsdpshard.so in-tree with hipcc for gfx950.
 
-The host indexer (csrc/unit.cpp) is plain C++; the kernels and the device
-entry points (csrc/kernels.hip) are HIP. Flags that fix the numerics:
+The host indexer (csrc/unit.cpp) is plain C++; the kernels and their entry
+points are HIP: csrc/kernels.hip (the shard step), csrc/muon_step.hip,
+csrc/orthogonalize.hip and csrc/rms_norm.hip, compiled side by side. Flags that fix the numerics:
 -ffp-contract=off (no fused multiply-add anywhere on the path), the default
 correctly rounded fp32 division and square root (never -ffast-math), and
 packed-fp32 instructions disabled for device code.
@@ -13,12 +14,14 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfsdpshard.so"
+SOURCES = ["unit.cpp", "kernels.hip", "muon_step.hip", "orthogonalize.hip", "rms_norm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -47,14 +50,17 @@ def build(out_dir: str | None = None, defines=(), verbose: bool = False) -> str:
     obj_dir = os.path.join(out_dir, "_build")
     os.makedirs(obj_dir, exist_ok=True)
     dflags = [f"-D{d}" for d in defines]
-    unit_o = os.path.join(obj_dir, "unit.o")
-    kern_o = os.path.join(obj_dir, "kernels.o")
-    _run([HIPCC, "-x", "c++", *COMMON, *dflags, "-c", os.path.join(CSRC, "unit.cpp"),
-          "-o", unit_o], verbose)
-    _run([HIPCC, "-x", "hip", *DEVICE, *COMMON, *dflags, "-c",
-          os.path.join(CSRC, "kernels.hip"), "-o", kern_o], verbose)
+
+    def compile_one(source):
+        obj = os.path.join(obj_dir, os.path.splitext(source)[0] + ".o")
+        lang = ["-x", "hip", *DEVICE] if source.endswith(".hip") else ["-x", "c++"]
+        _run([HIPCC, *lang, *COMMON, *dflags, "-c", os.path.join(CSRC, source), "-o", obj], verbose)
+        return obj
+
+    with ThreadPoolExecutor(4) as pool:
+        objects = list(pool.map(compile_one, SOURCES))
     tmp = os.path.join(out_dir, LIB_NAME + ".tmp")
-    _run([HIPCC, *DEVICE, "-shared", "-fPIC", "-o", tmp, unit_o, kern_o], verbose)
+    _run([HIPCC, *DEVICE, "-shared", "-fPIC", "-o", tmp, *objects], verbose)
     final = os.path.join(out_dir, LIB_NAME)
     os.replace(tmp, final)
     shutil.rmtree(obj_dir, ignore_errors=True)

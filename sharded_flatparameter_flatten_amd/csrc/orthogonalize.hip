@@ -1,0 +1,639 @@
+// Orthogonalisation of a list of matrices by Newton-Schulz products (the
+// update of the Muon step) on gfx950, and its entry points.
+//
+// For a matrix G with m = min(rows, cols) and n = max(rows, cols), X is the
+// m x n one of G and its transpose, and
+//   X_0 = X / (|X|_F + eps)
+//   S = X X^T,  P = a I + b S + c S S,  X <- P X          (`steps` times).
+// All the work is in the three products, which are run as one kind of tiled
+// product C = A B^T with both operands stored along the contracted axis:
+//   S = X X^T                 rows of X with rows of X;
+//   S S = S S^T               (S is symmetric);
+//   (P X)^T = X^T P^T         rows of X^T with rows of P.
+// X is therefore kept in both orientations; the epilogue of the third product
+// writes both. S and P are symmetric: only the tiles on and below the diagonal
+// are computed, and each is stored with its mirror image. The additions of
+// a I and b S are in the second product's epilogue.
+//
+// Numerics: the operands of the matrix instructions are fp16 and every sum is
+// held in fp32. fp16 rather than bf16, at the same rate, because each rounding
+// of X is amplified: the polynomial raises the small singular values (up to
+// 3.4 times a step) over rounding errors that are relative to the large ones.
+// With bf16 operands the result is about 1.1e-2 from the exact polynomial,
+// with fp16 ones 1.4e-3 (2-norm, matrices with a few strong directions). The
+// values are scaled by powers of two to sit in fp16's normal range: X by
+// 2^12, S and P by 2^10, so |X| < 16, |S| < 64 and |P| < 64 are representable;
+// singular values start at 1 or less and stay below 1.3 with the usual
+// coefficients. A matrix whose norm is far below eps loses precision (its X
+// has elements near fp16's subnormals once norm / eps < 1e-4).
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "device_util.h"
+
+#pragma clang fp contract(off)
+
+using fsdp::fail;
+using namespace fsdp::dev;
+
+namespace {
+
+typedef _Float16 f16;
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kScaleX = 4096.f;     // stored X is X * 2^12
+constexpr float kScaleS = 1024.f;     // stored S and P are times 2^10
+constexpr int kBK = 64;               // contracted elements per stage: one 128-byte line a row
+constexpr int kMaxMats = 24;          // matrices per launch (kernel arguments < 4 KB)
+constexpr int kSumBlocks = 256;       // partial sums of squares per matrix, at most
+constexpr int kSumRow = 8192;         // a contiguous matrix is summed as rows of this length
+
+// ---------------------------------------------------------------------------
+// the tiled product
+// ---------------------------------------------------------------------------
+
+// One matrix's product in a launch: C[i][j] = sum_k A[i][k] B[j][k]. Every
+// buffer is padded with zeros to whole tiles on both axes, so the kernel has
+// no bounds to check except those of the final output.
+struct Prod {
+  const f16* a;
+  const f16* b;
+  f16* c;            // [i][j], or null
+  f16* ct;           // [j][i], or null
+  const f16* d;      // symmetric addend, or null
+  uint16_t* out;     // final bf16 output [j][i], bounded by out_j and out_i
+  int64_t out_ld;
+  int32_t lda, ldb, ldc, ldct;
+  int32_t kt;        // stages
+  int32_t ti, tj;    // tiles on each axis
+  int32_t out_i, out_j;
+  int32_t tile_end;  // exclusive prefix of tiles over the launch
+};
+struct ProdArgs {
+  Prod p[kMaxMats];
+  int32_t np;
+  int32_t tiles;
+  float alpha, beta, delta;   // result = alpha * sum + beta * D + delta * I
+};
+
+// Workgroup index -> tile: consecutive tiles stay on one XCD (workgroup b runs
+// on XCD b % 8), whose L2 then holds the rows they share.
+__device__ __forceinline__ int xcd_tile(int b, int nb) {
+  const int per = nb / 8, extra = nb % 8, x = b % 8;
+  return x * per + (x < extra ? x : extra) + b / 8;
+}
+
+// Tile t of a ti x tj grid, walked in bands of 8 tile rows.
+__device__ __forceinline__ void tile_of(int t, int ti, int tj, int& i, int& j) {
+  const int band = t / (8 * tj), r0 = band * 8, h = ti - r0 < 8 ? ti - r0 : 8, in = t - r0 * tj;
+  i = r0 + in % h;
+  j = in / h;
+}
+// Tile t of the lower triangle, row by row: t = i (i + 1) / 2 + j, j <= i.
+__device__ __forceinline__ void tri_of(int t, int& i, int& j) {
+  int r = int((sqrtf(8.f * float(t) + 1.f) - 1.f) * 0.5f);
+  while (r * (r + 1) / 2 > t) --r;
+  while ((r + 1) * (r + 2) / 2 <= t) ++r;
+  i = r;
+  j = t - r * (r + 1) / 2;
+}
+
+enum class Kind { Sym, Update, Final };
+
+// BM x BN tile by WM x WN waves. LDS holds two stages of both operands; a
+// stage row is 128 bytes, 8 chunks of 16. Global loads go straight to LDS:
+// lane l of a load fills chunk l % 8 of row l / 8, and takes it from global
+// chunk (l % 8) ^ (l / 8), so that chunk c of row r sits at c ^ (r % 8) and
+// the fragment reads (16 rows, one chunk each) touch every bank evenly.
+template <int BM, int BN, int WM, int WN, Kind KIND>
+__global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
+  constexpr int kWaves = WM * WN;
+  constexpr int kLoads = (BM + BN) / 8;           // 1 KB loads a stage
+  static_assert(BM == BN && kWaves % 2 == 0 && kLoads % kWaves == 0, "whole loads per wave");
+  constexpr int kPer = kLoads / kWaves;
+  constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
+  constexpr int kStage = (BM + BN) * kBK * 2;
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
+
+  const int t = xcd_tile(blockIdx.x, gridDim.x);
+  int s = 0;
+  while (t >= args.p[s].tile_end) ++s;            // tiles == the grid: ends at the last entry
+  const Prod& p = args.p[s];
+  const int local = t - (s ? args.p[s - 1].tile_end : 0);
+  int ti, tj;
+  if constexpr (KIND == Kind::Sym) tri_of(local, ti, tj);
+  else tile_of(local, p.ti, p.tj, ti, tj);
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  // The first half of the waves load A's rows, the other half B's.
+  const bool of_b = wave >= kWaves / 2;
+  const int ld = of_b ? p.ldb : p.lda;
+  const f16* base = of_b ? p.b + int64_t(tj) * BN * ld : p.a + int64_t(ti) * BM * ld;
+  const __amdgpu_buffer_rsrc_t r = rsrc(base, int64_t(BM) * ld * 2);
+  const int first = (wave % (kWaves / 2)) * kPer;
+  const int vo = (lane >> 3) * ld * 2 + ((lane & 7) ^ (lane >> 3)) * 16;
+
+  auto load = [&](int buf, int k) {
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)                // 8 rows each
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          r, (__attribute__((address_space(3))) void*)(lds + buf * kStage + (wave * kPer + q) * 1024),
+          16, vo, (first + q) * 8 * ld * 2 + k * (kBK * 2), 0, 0);
+  };
+
+  f32x4 acc[MI][NI];
+#pragma unroll
+  for (int x = 0; x < MI; ++x)
+#pragma unroll
+    for (int y = 0; y < NI; ++y) acc[x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int frag = (lane & 15) * 128;
+  const int c0 = ((lane >> 4) ^ (lane & 7)) * 16;  // the second half of a stage flips bit 2
+  const int kt = p.kt;
+  load(0, 0);
+  for (int k = 0; k < kt; ++k) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (k + 1 < kt) load((k + 1) & 1, k + 1);
+    const char* sa = lds + (k & 1) * kStage + wm * (BM / WM) * 128 + frag;
+    const char* sb = lds + (k & 1) * kStage + (BM + wn * (BN / WN)) * 128 + frag;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = c0 ^ (h * 64);
+      f16x8 fa[MI], fb[NI];
+#pragma unroll
+      for (int x = 0; x < MI; ++x) fa[x] = *reinterpret_cast<const f16x8*>(sa + x * 2048 + c);
+#pragma unroll
+      for (int y = 0; y < NI; ++y) fb[y] = *reinterpret_cast<const f16x8*>(sb + y * 2048 + c);
+#pragma unroll
+      for (int x = 0; x < MI; ++x)
+#pragma unroll
+        for (int y = 0; y < NI; ++y)
+          acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fa[x], fb[y], acc[x][y], 0, 0, 0);
+    }
+  }
+
+  // A lane's acc[x][y] holds 4 consecutive i of one j.
+  const int i0 = ti * BM + wm * (BM / WM) + (lane >> 4) * 4, j0 = tj * BN + wn * (BN / WN) + (lane & 15);
+#pragma unroll
+  for (int x = 0; x < MI; ++x)
+#pragma unroll
+    for (int y = 0; y < NI; ++y) {
+      const int i = i0 + x * 16, j = j0 + y * 16;
+      f32x4 v = acc[x][y] * args.alpha;
+      if constexpr (KIND == Kind::Final) {
+        if (j < p.out_j) {
+          uint16_t* o = p.out + int64_t(j) * p.out_ld + i;
+          if (i + 4 <= p.out_i) {
+            st_loose<u32x2, 2>(o, u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)});
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (i + e < p.out_i) o[e] = uint16_t(to_bf16(v[e]));
+          }
+        }
+      } else {
+        if constexpr (KIND == Kind::Sym) {
+          if (p.d) {
+            const f16x4 d = *reinterpret_cast<const f16x4*>(p.d + int64_t(j) * p.ldct + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = v[e] + args.beta * float(d[e]) + (i + e == j ? args.delta : 0.f);
+          }
+        }
+        const f16x4 q = {f16(v.x), f16(v.y), f16(v.z), f16(v.w)};
+        *reinterpret_cast<f16x4*>(p.ct + int64_t(j) * p.ldct + i) = q;
+        if (KIND == Kind::Update || ti != tj) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p.c[int64_t(i + e) * p.ldc + j] = q[e];
+        }
+      }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the norm, and X_0 in both orientations
+// ---------------------------------------------------------------------------
+
+struct Source {
+  const void* g;      // the caller's matrix: rows x cols, `ld` elements a row
+  int64_t ld;
+  int32_t rows, cols;
+  f16* x;             // m x n, padded to mp x np
+  f16* xt;            // n x m, padded to np x mp
+  double* partial;    // sums of squares
+  int32_t mp, np;
+  int32_t parts;      // partial sums
+  int32_t end;        // exclusive prefix of workgroups over the launch
+};
+struct SourceArgs {
+  Source s[kMaxMats];
+  int32_t ns;
+  float eps;
+};
+
+// 8 consecutive elements as fp32, from element alignment.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const f32x4 a = ld_loose<f32x4, 4>(p), b = ld_loose<f32x4, 4>(p + 4);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) { x[e] = a[e]; x[4 + e] = b[e]; }
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
+  const u32x4 q = ld_loose<u32x4, 2>(p);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) { x[2 * e] = lo_bf16(q[e]); x[2 * e + 1] = hi_bf16(q[e]); }
+}
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t* p) { return widen(*p); }
+
+__device__ __forceinline__ double block_sum_256(double v, double* lds4) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) lds4[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (lds4[0] + lds4[1]) + (lds4[2] + lds4[3]);
+}
+
+// Sums of squares in fp64 (an fp32 element's square can leave fp32's range),
+// one partial a workgroup, joined in a fixed order by k_ortho_start.
+template <typename T>
+__global__ __launch_bounds__(256) void k_ortho_sumsq(SourceArgs args) {
+  int s = 0;
+  while (int(blockIdx.x) >= args.s[s].end) ++s;
+  const Source& src = args.s[s];
+  const int part = int(blockIdx.x) - (s ? args.s[s - 1].end : 0);
+  const T* g = static_cast<const T*>(src.g);
+  const bool flat = src.ld == src.cols;
+  const int64_t total = int64_t(src.rows) * src.cols;
+  const int64_t len = flat ? kSumRow : src.cols, ld = flat ? kSumRow : src.ld;
+  const int64_t rows = flat ? (total + kSumRow - 1) / kSumRow : src.rows;
+  double sum = 0.0;
+  for (int64_t r = part; r < rows; r += src.parts) {
+    const T* row = g + r * ld;
+    const int64_t n = flat && total - r * len < len ? total - r * len : len;
+    for (int64_t c = int64_t(threadIdx.x) * 8; c < n; c += 2048) {
+      if (c + 8 <= n) {
+        float x[8];
+        load8(row + c, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += double(x[e]) * double(x[e]);
+      } else {
+        for (int64_t e = c; e < n; ++e) sum += double(load1(row + e)) * double(load1(row + e));
+      }
+    }
+  }
+  __shared__ double lds4[4];
+  sum = block_sum_256(sum, lds4);
+  if (threadIdx.x == 0) src.partial[part] = sum;
+}
+
+// X_0 from a 64 x 64 block of G: scaled, rounded to fp16, written as it lies
+// and transposed; what lies past G's edge is zero.
+template <typename T>
+__global__ __launch_bounds__(256) void k_ortho_start(SourceArgs args) {
+  int s = 0;
+  while (int(blockIdx.x) >= args.s[s].end) ++s;
+  const Source& src = args.s[s];
+  const int local = int(blockIdx.x) - (s ? args.s[s - 1].end : 0);
+  __shared__ double lds4[4];
+  __shared__ f16 tile[64][64 + 8];
+  const double sq = block_sum_256(int(threadIdx.x) < src.parts ? src.partial[threadIdx.x] : 0.0, lds4);
+  const float scale = float(double(kScaleX) / (sqrt(sq) + double(args.eps)));
+
+  const bool tall = src.rows > src.cols;
+  const int pr = tall ? src.np : src.mp, pc = tall ? src.mp : src.np;   // G's padded sides
+  f16* as_is = tall ? src.xt : src.x;
+  f16* turned = tall ? src.x : src.xt;
+  const int bc = pc / 64, r0 = local / bc * 64, c0 = local % bc * 64;
+  const T* g = static_cast<const T*>(src.g);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = (threadIdx.x >> 3) + 32 * k, c = (threadIdx.x & 7) * 8;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (r0 + r < src.rows) {
+      const T* p = g + int64_t(r0 + r) * src.ld + c0 + c;
+      if (c0 + c + 8 <= src.cols) {
+        load8(p, x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c0 + c + e < src.cols) x[e] = load1(p + e);
+      }
+    }
+    f16x8 q;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = f16(x[e] * scale);
+    *reinterpret_cast<f16x8*>(as_is + int64_t(r0 + r) * pc + c0 + c) = q;
+    *reinterpret_cast<f16x8*>(&tile[r][c]) = q;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = (threadIdx.x >> 3) + 32 * k, c = (threadIdx.x & 7) * 8;
+    f16x8 q;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = tile[c + e][r];
+    *reinterpret_cast<f16x8*>(turned + int64_t(c0 + r) * pr + r0 + c) = q;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+struct Plan {
+  int32_t rows, cols, m, n;   // m <= n
+  int64_t mp, np;             // padded
+  int64_t x, xt0, xt1, s, p, partial;   // workspace offsets
+  int32_t parts;
+};
+
+int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// The tile side of a call: 256 or 128. A larger tile reads less from LDS for
+// each matrix instruction; a smaller one pads less and gives more workgroups.
+// Estimated cost: padded multiply-adds of a step over the share of the 256 CUs
+// that its tiles keep busy.
+int choose_tile(int32_t count, const int64_t* rows, const int64_t* cols) {
+  int best = 128;
+  double least = 0;
+  for (int t : {256, 128}) {
+    double cost = 0;
+    double tiles[3] = {0, 0, 0}, depth[3] = {0, 0, 0};
+    for (int32_t i = 0; i < count; ++i) {
+      const double m = double(round_up(std::min(rows[i], cols[i]), t)) / t;
+      const double n = double(round_up(std::max(rows[i], cols[i]), t)) / t;
+      const double tri = m * (m + 1) / 2, tl[3] = {tri, tri, m * n}, dp[3] = {n, m, m};
+      for (int k = 0; k < 3; ++k) {
+        tiles[k] += tl[k];
+        depth[k] += tl[k] * dp[k];
+      }
+    }
+    const double slots = t == 256 ? 256 : 512;
+    for (int k = 0; k < 3; ++k)
+      if (tiles[k] > 0)
+        cost += depth[k] / tiles[k] * std::ceil(tiles[k] / slots) * double(t) * t * t * (t == 256 ? 1.0 : 2 * 1.3);
+    if (t == 256 || cost < least) {
+      best = t;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+constexpr int64_t kMaxSide = int64_t(1) << 20;
+
+fsdp_status check_shapes(int32_t count, const int64_t* rows, const int64_t* cols) {
+  if (count < 0 || count > FSDP_MAX_TENSORS)
+    return fail(FSDP_ERR_INVALID_ARG, "n_mats must be in [0, %d] (got %d)", FSDP_MAX_TENSORS, count);
+  if (count > 0 && (!rows || !cols)) return fail(FSDP_ERR_INVALID_ARG, "rows or cols is NULL");
+  for (int32_t i = 0; i < count; ++i) {
+    if (rows[i] < 0 || cols[i] < 0)
+      return fail(FSDP_ERR_INVALID_ARG, "matrix %d: negative size", i);
+    if (rows[i] > kMaxSide || cols[i] > kMaxSide)
+      return fail(FSDP_ERR_RANGE, "matrix %d: %lld x %lld is over %lld a side", i,
+                  static_cast<long long>(rows[i]), static_cast<long long>(cols[i]),
+                  static_cast<long long>(kMaxSide));
+  }
+  return FSDP_OK;
+}
+
+// Lays the buffers of every matrix that has elements out in the workspace.
+int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int tile,
+                  std::vector<Plan>* plans) {
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += round_up(bytes, 1024);
+    return here;
+  };
+  for (int32_t i = 0; i < count; ++i) {
+    Plan q{};
+    q.rows = int32_t(rows[i]);
+    q.cols = int32_t(cols[i]);
+    q.m = std::min(q.rows, q.cols);
+    q.n = std::max(q.rows, q.cols);
+    if (q.m > 0) {
+      q.mp = round_up(q.m, tile);
+      q.np = round_up(q.n, tile);
+      q.x = take(q.mp * q.np * 2);
+      q.xt0 = take(q.mp * q.np * 2);
+      q.xt1 = take(q.mp * q.np * 2);
+      q.s = take(q.mp * q.mp * 2);
+      q.p = take(q.mp * q.mp * 2);
+      q.parts = int32_t(std::min<int64_t>(kSumBlocks, (int64_t(q.m) * q.n + kSumRow - 1) / kSumRow));
+      q.partial = take(q.parts * 8);
+    }
+    if (plans) plans->push_back(q);
+  }
+  return at;
+}
+
+template <Kind KIND>
+void launch_product(const ProdArgs& a, int tile, hipStream_t stream) {
+  if (tile == 256) k_ortho_product<256, 256, 2, 4, KIND><<<a.tiles, 512, 0, stream>>>(a);
+  else k_ortho_product<128, 128, 2, 2, KIND><<<a.tiles, 256, 0, stream>>>(a);
+}
+
+template <typename T>
+fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const int64_t* mat_ld,
+                void* const* outs, const int64_t* out_ld, char* ws, int tile, int steps,
+                const double* coeffs, double eps, hipStream_t stream) {
+  const char* what = "fsdp_orthogonalize";
+  std::vector<int> live;
+  for (size_t i = 0; i < plans.size(); ++i)
+    if (plans[i].m > 0) live.push_back(int(i));
+  for (size_t b = 0; b < live.size(); b += kMaxMats) {
+    const int nb = int(std::min<size_t>(kMaxMats, live.size() - b));
+    SourceArgs src{};
+    src.ns = nb;
+    src.eps = float(eps);
+    int blocks = 0;
+    for (int k = 0; k < nb; ++k) {
+      const int i = live[b + k];
+      const Plan& q = plans[i];
+      Source& d = src.s[k];
+      d.g = mats[i];
+      d.ld = mat_ld[i];
+      d.rows = q.rows;
+      d.cols = q.cols;
+      d.x = reinterpret_cast<f16*>(ws + q.x);
+      d.xt = reinterpret_cast<f16*>(ws + q.xt0);
+      d.partial = reinterpret_cast<double*>(ws + q.partial);
+      d.mp = int32_t(q.mp);
+      d.np = int32_t(q.np);
+      d.parts = q.parts;
+      blocks += q.parts;
+      d.end = blocks;
+    }
+    k_ortho_sumsq<T><<<blocks, 256, 0, stream>>>(src);
+    if (fsdp_status st = fsdp::after_launch(what)) return st;
+    blocks = 0;
+    for (int k = 0; k < nb; ++k) {
+      blocks += int(plans[live[b + k]].mp / 64 * (plans[live[b + k]].np / 64));
+      src.s[k].end = blocks;
+    }
+    k_ortho_start<T><<<blocks, 256, 0, stream>>>(src);
+    if (fsdp_status st = fsdp::after_launch(what)) return st;
+
+    for (int step = 0; step < steps; ++step) {
+      const bool last = step + 1 == steps;
+      ProdArgs gram{}, poly{}, up[2] = {};        // up[1]: the last step of tall matrices
+      gram.np = poly.np = nb;
+      gram.alpha = kScaleS / (kScaleX * kScaleX);
+      poly.alpha = float(coeffs[2] / kScaleS);
+      poly.beta = float(coeffs[1]);
+      poly.delta = float(coeffs[0]) * kScaleS;
+      up[0].alpha = up[1].alpha = last ? 1.f / (kScaleS * kScaleX) : 1.f / kScaleS;
+      for (int k = 0; k < nb; ++k) {
+        const int i = live[b + k];
+        const Plan& q = plans[i];
+        f16* x = reinterpret_cast<f16*>(ws + q.x);
+        f16* xt = reinterpret_cast<f16*>(ws + (step & 1 ? q.xt1 : q.xt0));
+        f16* xt_next = reinterpret_cast<f16*>(ws + (step & 1 ? q.xt0 : q.xt1));
+        f16* sm = reinterpret_cast<f16*>(ws + q.s);
+        f16* pm = reinterpret_cast<f16*>(ws + q.p);
+        const int mt = int(q.mp / tile), nt = int(q.np / tile), tri = mt * (mt + 1) / 2;
+        Prod& g = gram.p[k];
+        g.a = g.b = x;
+        g.c = g.ct = sm;
+        g.lda = g.ldb = int32_t(q.np);
+        g.ldc = g.ldct = int32_t(q.mp);
+        g.kt = int32_t(q.np / kBK);
+        gram.tiles += tri;
+        g.tile_end = gram.tiles;
+        Prod& o = poly.p[k];
+        o.a = o.b = o.d = sm;
+        o.c = o.ct = pm;
+        o.lda = o.ldb = o.ldc = o.ldct = int32_t(q.mp);
+        o.kt = int32_t(q.mp / kBK);
+        poly.tiles += tri;
+        o.tile_end = poly.tiles;
+        const bool tall = q.rows > q.cols;
+        ProdArgs& ua = up[last && tall ? 1 : 0];
+        Prod& u = ua.p[ua.np++];
+        u.lda = u.ldb = int32_t(q.mp);
+        u.kt = int32_t(q.mp / kBK);
+        u.out = static_cast<uint16_t*>(outs[i]);
+        u.out_ld = out_ld[i];
+        if (last && tall) {                       // i along m: the output's rows are X^T's
+          u.a = pm;
+          u.b = xt;
+          u.ti = mt;
+          u.tj = nt;
+          u.out_i = q.m;
+          u.out_j = q.n;
+        } else {
+          u.a = xt;
+          u.b = pm;
+          u.ti = nt;
+          u.tj = mt;
+          u.c = xt_next;
+          u.ldc = int32_t(q.mp);
+          u.ct = x;
+          u.ldct = int32_t(q.np);
+          u.out_i = q.n;
+          u.out_j = q.m;
+        }
+        ua.tiles += mt * nt;
+        u.tile_end = ua.tiles;
+      }
+      launch_product<Kind::Sym>(gram, tile, stream);
+      if (fsdp_status st = fsdp::after_launch(what)) return st;
+      launch_product<Kind::Sym>(poly, tile, stream);
+      if (fsdp_status st = fsdp::after_launch(what)) return st;
+      for (const ProdArgs& u : up) {
+        if (u.tiles == 0) continue;
+        if (last) launch_product<Kind::Final>(u, tile, stream);
+        else launch_product<Kind::Update>(u, tile, stream);
+        if (fsdp_status st = fsdp::after_launch(what)) return st;
+      }
+    }
+  }
+  return FSDP_OK;
+}
+
+fsdp_status orthogonalize(int32_t count, fsdp_dtype dtype, const void* const* mats,
+                          const int64_t* rows, const int64_t* cols, const int64_t* mat_ld,
+                          void* const* outs, const int64_t* out_ld, void* workspace,
+                          int64_t workspace_bytes, int32_t steps, const double* coeffs, double eps,
+                          hipStream_t stream) {
+  const char* what = "fsdp_orthogonalize";
+  if (fsdp_status st = check_shapes(count, rows, cols)) return st;
+  if (dtype != FSDP_F32 && dtype != FSDP_BF16)
+    return fail(FSDP_ERR_UNSUPPORTED, "dtype %d not supported", static_cast<int>(dtype));
+  if (steps < 1 || steps > 64)
+    return fail(FSDP_ERR_INVALID_ARG, "steps must be in [1, 64] (got %d)", steps);
+  if (!coeffs) return fail(FSDP_ERR_INVALID_ARG, "coeffs is NULL");
+  for (int k = 0; k < 3; ++k)
+    if (!std::isfinite(coeffs[k])) return fail(FSDP_ERR_INVALID_ARG, "coeffs must be finite");
+  if (!std::isfinite(eps) || !(eps >= 0.0))
+    return fail(FSDP_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (count == 0) return FSDP_OK;
+  const int64_t es = dtype == FSDP_F32 ? 4 : 2;
+  const int tile = choose_tile(count, rows, cols);
+  std::vector<Plan> plans;
+  const int64_t need = make_plan(count, rows, cols, tile, &plans);
+  if (need == 0) return FSDP_OK;               // only empty matrices
+  if (!mats || !mat_ld || !outs || !out_ld)
+    return fail(FSDP_ERR_INVALID_ARG, "a matrix array is NULL");
+  std::vector<fsdp::ByteRange> ranges;
+  for (int32_t i = 0; i < count; ++i) {
+    if (plans[i].m == 0) continue;
+    if (!mats[i] || !outs[i]) return fail(FSDP_ERR_INVALID_ARG, "%s[%d] is NULL", mats[i] ? "outs" : "mats", i);
+    if (reinterpret_cast<uintptr_t>(mats[i]) % es)
+      return fail(FSDP_ERR_INVALID_ARG, "mats[%d] is not element aligned", i);
+    if (reinterpret_cast<uintptr_t>(outs[i]) % 2)
+      return fail(FSDP_ERR_INVALID_ARG, "outs[%d] is not 2-byte aligned", i);
+    if (mat_ld[i] < cols[i] || out_ld[i] < cols[i])
+      return fail(FSDP_ERR_RANGE, "matrix %d: a row pitch is below its %lld columns", i,
+                  static_cast<long long>(cols[i]));
+    if (mat_ld[i] > (int64_t(1) << 40) || out_ld[i] > (int64_t(1) << 40))
+      return fail(FSDP_ERR_RANGE, "matrix %d: row pitch too large", i);
+    ranges.push_back(fsdp::range_of(mats[i], (rows[i] - 1) * mat_ld[i] + cols[i], es, false, "mats", i));
+    ranges.push_back(fsdp::range_of(outs[i], (rows[i] - 1) * out_ld[i] + cols[i], 2, true, "outs", i));
+  }
+  if (fsdp_status st = fsdp::check_ptr(workspace, "workspace", 256)) return st;
+  if (workspace_bytes < need)
+    return fail(FSDP_ERR_RANGE, "workspace has %lld bytes, needs %lld",
+                static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+  ranges.push_back(fsdp::range_of(workspace, need, 1, true, "workspace"));
+  if (fsdp_status st = fsdp::check_alias(ranges)) return st;
+  if (fsdp_status st = fsdp::check_no_pending_error(what)) return st;
+  char* ws = static_cast<char*>(workspace);
+  if (dtype == FSDP_F32)
+    return run<float>(plans, mats, mat_ld, outs, out_ld, ws, tile, steps, coeffs, eps, stream);
+  return run<uint16_t>(plans, mats, mat_ld, outs, out_ld, ws, tile, steps, coeffs, eps, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+fsdp_status fsdp_orthogonalize_workspace(int32_t n_mats, const int64_t* rows, const int64_t* cols,
+                                         int64_t* bytes) {
+  fsdp::clear_error();
+  if (!bytes) return fail(FSDP_ERR_INVALID_ARG, "bytes pointer is NULL");
+  if (fsdp_status st = check_shapes(n_mats, rows, cols)) return st;
+  *bytes = make_plan(n_mats, rows, cols, choose_tile(n_mats, rows, cols), nullptr);
+  return FSDP_OK;
+}
+
+fsdp_status fsdp_orthogonalize(int32_t n_mats, fsdp_dtype dtype, const void* const* mats,
+                               const int64_t* rows, const int64_t* cols, const int64_t* mat_ld,
+                               void* const* outs, const int64_t* out_ld, void* workspace,
+                               int64_t workspace_bytes, int32_t steps, const double* coeffs,
+                               double eps, hipStream_t stream) {
+  fsdp::clear_error();
+  try {
+    return orthogonalize(n_mats, dtype, mats, rows, cols, mat_ld, outs, out_ld, workspace,
+                         workspace_bytes, steps, coeffs, eps, stream);
+  } catch (const std::bad_alloc&) {
+    return fail(FSDP_ERR_INVALID_ARG, "out of host memory");
+  }
+}
+
+}  // extern "C"
