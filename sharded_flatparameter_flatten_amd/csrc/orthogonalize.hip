@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <cmath>
 #include <new>
+#include <type_traits>
 
 #include "device_util.h"
 
@@ -43,6 +44,7 @@ namespace {
 typedef _Float16 f16;
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kScaleX = 4096.f;     // stored X is X * 2^12
 constexpr float kScaleS = 1024.f;     // stored S and P are times 2^10
@@ -70,21 +72,15 @@ struct Prod {
   int32_t kt;        // stages
   int32_t ti, tj;    // tiles on each axis
   int32_t out_i, out_j;
-  int32_t tile_end;  // exclusive prefix of tiles over the launch
+  int32_t per_xcd;   // tiles on one XCD
+  int32_t slot_end;  // exclusive prefix of per_xcd over the launch
 };
 struct ProdArgs {
   Prod p[kMaxMats];
   int32_t np;
-  int32_t tiles;
+  int32_t slots;     // workgroups on one XCD
   float alpha, beta, delta;   // result = alpha * sum + beta * D + delta * I
 };
-
-// Workgroup index -> tile: consecutive tiles stay on one XCD (workgroup b runs
-// on XCD b % 8), whose L2 then holds the rows they share.
-__device__ __forceinline__ int xcd_tile(int b, int nb) {
-  const int per = nb / 8, extra = nb % 8, x = b % 8;
-  return x * per + (x < extra ? x : extra) + b / 8;
-}
 
 // Tile t of a ti x tj grid, walked in bands of 8 tile rows.
 __device__ __forceinline__ void tile_of(int t, int ti, int tj, int& i, int& j) {
@@ -103,116 +99,182 @@ __device__ __forceinline__ void tri_of(int t, int& i, int& j) {
 
 enum class Kind { Sym, Update, Final };
 
-// BM x BN tile by WM x WN waves. LDS holds two stages of both operands; a
-// stage row is 128 bytes, 8 chunks of 16. Global loads go straight to LDS:
-// lane l of a load fills chunk l % 8 of row l / 8, and takes it from global
-// chunk (l % 8) ^ (l / 8), so that chunk c of row r sits at c ^ (r % 8) and
-// the fragment reads (16 rows, one chunk each) touch every bank evenly.
-template <int BM, int BN, int WM, int WN, Kind KIND>
+// Every load of this wave has landed, in registers or in LDS.
+__device__ __forceinline__ void wait_all() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+
+// T x T tile by WM x WN waves, on 32 x 32 x 16 matrix instructions.
+//
+// LDS holds two stages of both operands; a stage row is 128 bytes, 8 chunks of
+// 16. Global loads go straight to LDS, 8 rows each: lane l of a load fills chunk
+// l % 8 of row l / 8. Chunk c of row r sits at c ^ (r / 2 % 8), so that the
+// fragment reads (32 rows, one chunk each), which LDS serves 16 lanes, 256
+// bytes, at a time, touch each of its 64 banks once.
+//
+// A stage is worked off in two halves, and the fragments of the next half are
+// read while the matrix instructions of this one run. The stage's one barrier
+// stands between the halves: by then every wave holds the second half's
+// fragments in registers, so the next stage but one may be loaded over this
+// one, and has a whole stage's time to arrive.
+template <int T, int WM, int WN, Kind KIND>
 __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   constexpr int kWaves = WM * WN;
-  constexpr int kLoads = (BM + BN) / 8;           // 1 KB loads a stage
-  static_assert(BM == BN && kWaves % 2 == 0 && kLoads % kWaves == 0, "whole loads per wave");
+  constexpr int kLoads = 2 * T / 8;               // 1 KB loads a stage
+  static_assert(kWaves % 2 == 0 && kLoads % kWaves == 0, "whole loads per wave");
   constexpr int kPer = kLoads / kWaves;
-  constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
-  constexpr int kStage = (BM + BN) * kBK * 2;
+  static_assert(kPer % 2 == 0, "a wave's first load is of an even q");
+  constexpr int MI = T / WM / 32, NI = T / WN / 32;
+  constexpr int kStage = 2 * T * kBK * 2;
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
 
-  const int t = xcd_tile(blockIdx.x, gridDim.x);
+  // Workgroup b runs on XCD b % 8. Every XCD takes an eighth of each matrix, in
+  // one run of tiles, whose shared rows then stay in its L2; the matrix of the
+  // longest contraction comes first, so that no XCD ends on a long tile.
+  const int xcd = blockIdx.x % 8, slot = blockIdx.x / 8;
   int s = 0;
-  while (t >= args.p[s].tile_end) ++s;            // tiles == the grid: ends at the last entry
+  while (slot >= args.p[s].slot_end) ++s;         // slot < slots: ends at the last entry
   const Prod& p = args.p[s];
-  const int local = t - (s ? args.p[s - 1].tile_end : 0);
+  const int local = xcd * p.per_xcd + slot - (s ? args.p[s - 1].slot_end : 0);
   int ti, tj;
-  if constexpr (KIND == Kind::Sym) tri_of(local, ti, tj);
-  else tile_of(local, p.ti, p.tj, ti, tj);
+  if constexpr (KIND == Kind::Sym) {
+    if (local >= p.ti * (p.ti + 1) / 2) return;
+    tri_of(local, ti, tj);
+  } else {
+    if (local >= p.ti * p.tj) return;
+    tile_of(local, p.ti, p.tj, ti, tj);
+  }
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   // The first half of the waves load A's rows, the other half B's.
   const bool of_b = wave >= kWaves / 2;
   const int ld = of_b ? p.ldb : p.lda;
-  const f16* base = of_b ? p.b + int64_t(tj) * BN * ld : p.a + int64_t(ti) * BM * ld;
-  const __amdgpu_buffer_rsrc_t r = rsrc(base, int64_t(BM) * ld * 2);
+  const f16* base = of_b ? p.b + int64_t(tj) * T * ld : p.a + int64_t(ti) * T * ld;
+  const __amdgpu_buffer_rsrc_t r = rsrc(base, int64_t(T) * ld * 2);
   const int first = (wave % (kWaves / 2)) * kPer;
-  const int vo = (lane >> 3) * ld * 2 + ((lane & 7) ^ (lane >> 3)) * 16;
+  // row 8 q + lane / 8: its r / 2 % 8 is lane / 16, plus 4 for odd q
+  const int v0 = (lane >> 3) * ld * 2 + ((lane & 7) ^ (lane >> 4)) * 16, v1 = v0 ^ 64;
 
-  auto load = [&](int buf, int k) {
+  auto load = [&](int k) {
+    char* to = lds + (k & 1) * kStage + wave * (kPer * 1024);
 #pragma unroll
     for (int q = 0; q < kPer; ++q)                // 8 rows each
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          r, (__attribute__((address_space(3))) void*)(lds + buf * kStage + (wave * kPer + q) * 1024),
-          16, vo, (first + q) * 8 * ld * 2 + k * (kBK * 2), 0, 0);
+          r, (__attribute__((address_space(3))) void*)(to + q * 1024), 16, q & 1 ? v1 : v0,
+          (first + q) * 8 * ld * 2 + k * (kBK * 2), 0, 0);
   };
 
-  f32x4 acc[MI][NI];
+  f32x16 acc[MI][NI];
 #pragma unroll
   for (int x = 0; x < MI; ++x)
 #pragma unroll
-    for (int y = 0; y < NI; ++y) acc[x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int y = 0; y < NI; ++y)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.f;
 
-  const int frag = (lane & 15) * 128;
-  const int c0 = ((lane >> 4) ^ (lane & 7)) * 16;  // the second half of a stage flips bit 2
-  const int kt = p.kt;
-  load(0, 0);
-  for (int k = 0; k < kt; ++k) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (k + 1 < kt) load((k + 1) & 1, k + 1);
-    const char* sa = lds + (k & 1) * kStage + wm * (BM / WM) * 128 + frag;
-    const char* sb = lds + (k & 1) * kStage + (BM + wn * (BN / WN)) * 128 + frag;
+  // A lane's fragment: row lane % 32, 8 elements at chunk 2 q + lane / 32 of the stage row.
+  const int frag = (lane & 31) * 128, c0 = ((lane >> 5) ^ ((lane >> 1) & 7)) * 16;
+  const int oa = wm * (T / WM) * 128 + frag, ob = (T + wn * (T / WN)) * 128 + frag;
+  f16x8 fa[2][2][MI], fb[2][2][NI];               // [half][q][fragment]
+  auto read = [&](int k, int h) {
+    const char* st = lds + (k & 1) * kStage;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = c0 ^ (h * 64);
-      f16x8 fa[MI], fb[NI];
+    for (int q = 0; q < 2; ++q) {
+      const int c = c0 ^ (h * 64 + q * 32);
 #pragma unroll
-      for (int x = 0; x < MI; ++x) fa[x] = *reinterpret_cast<const f16x8*>(sa + x * 2048 + c);
+      for (int x = 0; x < MI; ++x) fa[h][q][x] = *reinterpret_cast<const f16x8*>(st + oa + x * 4096 + c);
 #pragma unroll
-      for (int y = 0; y < NI; ++y) fb[y] = *reinterpret_cast<const f16x8*>(sb + y * 2048 + c);
+      for (int y = 0; y < NI; ++y) fb[h][q][y] = *reinterpret_cast<const f16x8*>(st + ob + y * 4096 + c);
+    }
+  };
+  auto multiply = [&](int h) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
       for (int x = 0; x < MI; ++x)
 #pragma unroll
         for (int y = 0; y < NI; ++y)
-          acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fa[x], fb[y], acc[x][y], 0, 0, 0);
+          acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[h][q][x], fb[h][q][y], acc[x][y], 0, 0, 0);
+  };
+  // Matrix instructions of one half with the fragment reads of the next between them.
+  auto interleave = [&] {
+    constexpr int kReads = 2 * (MI + NI), kMul = 2 * MI * NI;
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                     // a read
+      if ((i + 1) * kMul / kReads > i * kMul / kReads)
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                   // a multiply
     }
-  }
+  };
 
-  // A lane's acc[x][y] holds 4 consecutive i of one j.
-  const int i0 = ti * BM + wm * (BM / WM) + (lane >> 4) * 4, j0 = tj * BN + wn * (BN / WN) + (lane & 15);
+  // Stage k; LOAD: stage k + 2 exists, READ: stage k + 1 does.
+  auto stage = [&](int k, auto load_next, auto read_next) {
+    read(k, 1);
+    multiply(0);
+    interleave();
+    __builtin_amdgcn_sched_barrier(0);
+    wait_all();                                   // fragments read; the next stage has landed
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if constexpr (load_next.value) load(k + 2);
+    if constexpr (read_next.value) read(k + 1, 0);
+    multiply(1);
+    if constexpr (read_next.value) interleave();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using std::false_type;
+  using std::true_type;
+
+  const int kt = p.kt;
+  load(0);
+  wait_all();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  if (kt > 1) load(1);
+  read(0, 0);
+  for (int k = 0; k + 2 < kt; ++k) stage(k, true_type{}, true_type{});
+  if (kt > 1) stage(kt - 2, false_type{}, true_type{});
+  stage(kt - 1, false_type{}, false_type{});
+
+  // A lane's acc[x][y][4 g + e] holds i = 8 g + 4 (lane / 32) + e of one j = lane % 32.
+  const int i0 = ti * T + wm * (T / WM) + (lane >> 5) * 4, j0 = tj * T + wn * (T / WN) + (lane & 31);
 #pragma unroll
   for (int x = 0; x < MI; ++x)
 #pragma unroll
-    for (int y = 0; y < NI; ++y) {
-      const int i = i0 + x * 16, j = j0 + y * 16;
-      f32x4 v = acc[x][y] * args.alpha;
-      if constexpr (KIND == Kind::Final) {
-        if (j < p.out_j) {
-          uint16_t* o = p.out + int64_t(j) * p.out_ld + i;
-          if (i + 4 <= p.out_i) {
-            st_loose<u32x2, 2>(o, u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)});
-          } else {
+    for (int y = 0; y < NI; ++y)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (i + e < p.out_i) o[e] = uint16_t(to_bf16(v[e]));
+      for (int g = 0; g < 4; ++g) {
+        const int i = i0 + x * 32 + g * 8, j = j0 + y * 32;
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[x][y][4 * g + e] * args.alpha;
+        if constexpr (KIND == Kind::Final) {
+          if (j < p.out_j) {
+            uint16_t* o = p.out + int64_t(j) * p.out_ld + i;
+            if (i + 4 <= p.out_i) {
+              st_loose<u32x2, 2>(o, u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)});
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (i + e < p.out_i) o[e] = uint16_t(to_bf16(v[e]));
+            }
           }
-        }
-      } else {
-        if constexpr (KIND == Kind::Sym) {
-          if (p.d) {
-            const f16x4 d = *reinterpret_cast<const f16x4*>(p.d + int64_t(j) * p.ldct + i);
+        } else {
+          if constexpr (KIND == Kind::Sym) {
+            if (p.d) {
+              const f16x4 d = *reinterpret_cast<const f16x4*>(p.d + int64_t(j) * p.ldct + i);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = v[e] + args.beta * float(d[e]) + (i + e == j ? args.delta : 0.f);
+              for (int e = 0; e < 4; ++e)
+                v[e] = v[e] + args.beta * float(d[e]) + (i + e == j ? args.delta : 0.f);
+            }
           }
-        }
-        const f16x4 q = {f16(v.x), f16(v.y), f16(v.z), f16(v.w)};
-        *reinterpret_cast<f16x4*>(p.ct + int64_t(j) * p.ldct + i) = q;
-        if (KIND == Kind::Update || ti != tj) {
+          const f16x4 q = {f16(v.x), f16(v.y), f16(v.z), f16(v.w)};
+          *reinterpret_cast<f16x4*>(p.ct + int64_t(j) * p.ldct + i) = q;
+          if (KIND == Kind::Update || ti != tj) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p.c[int64_t(i + e) * p.ldc + j] = q[e];
+            for (int e = 0; e < 4; ++e) p.c[int64_t(i + e) * p.ldc + j] = q[e];
+          }
         }
       }
-    }
 }
 
 // ---------------------------------------------------------------------------
@@ -432,10 +494,19 @@ int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int t
   return at;
 }
 
+// Adds a product of `tiles` tiles to a launch.
+Prod& add_product(ProdArgs& a, int tiles) {
+  Prod& p = a.p[a.np++];
+  p.per_xcd = (tiles + 7) / 8;
+  a.slots += p.per_xcd;
+  p.slot_end = a.slots;
+  return p;
+}
+
 template <Kind KIND>
 void launch_product(const ProdArgs& a, int tile, hipStream_t stream) {
-  if (tile == 256) k_ortho_product<256, 256, 2, 4, KIND><<<a.tiles, 512, 0, stream>>>(a);
-  else k_ortho_product<128, 128, 2, 2, KIND><<<a.tiles, 256, 0, stream>>>(a);
+  if (tile == 256) k_ortho_product<256, 2, 4, KIND><<<8 * a.slots, 512, 0, stream>>>(a);
+  else k_ortho_product<128, 2, 2, KIND><<<8 * a.slots, 256, 0, stream>>>(a);
 }
 
 template <typename T>
@@ -446,6 +517,10 @@ fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const i
   std::vector<int> live;
   for (size_t i = 0; i < plans.size(); ++i)
     if (plans[i].m > 0) live.push_back(int(i));
+  // longest contractions first, in S = X X^T and in the others
+  std::stable_sort(live.begin(), live.end(), [&](int a, int b) {
+    return plans[a].np != plans[b].np ? plans[a].np > plans[b].np : plans[a].mp > plans[b].mp;
+  });
   for (size_t b = 0; b < live.size(); b += kMaxMats) {
     const int nb = int(std::min<size_t>(kMaxMats, live.size() - b));
     SourceArgs src{};
@@ -482,7 +557,6 @@ fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const i
     for (int step = 0; step < steps; ++step) {
       const bool last = step + 1 == steps;
       ProdArgs gram{}, poly{}, up[2] = {};        // up[1]: the last step of tall matrices
-      gram.np = poly.np = nb;
       gram.alpha = kScaleS / (kScaleX * kScaleX);
       poly.alpha = float(coeffs[2] / kScaleS);
       poly.beta = float(coeffs[1]);
@@ -497,24 +571,22 @@ fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const i
         f16* sm = reinterpret_cast<f16*>(ws + q.s);
         f16* pm = reinterpret_cast<f16*>(ws + q.p);
         const int mt = int(q.mp / tile), nt = int(q.np / tile), tri = mt * (mt + 1) / 2;
-        Prod& g = gram.p[k];
+        Prod& g = add_product(gram, tri);
         g.a = g.b = x;
         g.c = g.ct = sm;
         g.lda = g.ldb = int32_t(q.np);
         g.ldc = g.ldct = int32_t(q.mp);
         g.kt = int32_t(q.np / kBK);
-        gram.tiles += tri;
-        g.tile_end = gram.tiles;
-        Prod& o = poly.p[k];
+        g.ti = mt;
+        Prod& o = add_product(poly, tri);
         o.a = o.b = o.d = sm;
         o.c = o.ct = pm;
         o.lda = o.ldb = o.ldc = o.ldct = int32_t(q.mp);
         o.kt = int32_t(q.mp / kBK);
-        poly.tiles += tri;
-        o.tile_end = poly.tiles;
+        o.ti = mt;
         const bool tall = q.rows > q.cols;
         ProdArgs& ua = up[last && tall ? 1 : 0];
-        Prod& u = ua.p[ua.np++];
+        Prod& u = add_product(ua, mt * nt);
         u.lda = u.ldb = int32_t(q.mp);
         u.kt = int32_t(q.mp / kBK);
         u.out = static_cast<uint16_t*>(outs[i]);
@@ -538,15 +610,13 @@ fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const i
           u.out_i = q.n;
           u.out_j = q.m;
         }
-        ua.tiles += mt * nt;
-        u.tile_end = ua.tiles;
       }
       launch_product<Kind::Sym>(gram, tile, stream);
       if (fsdp_status st = fsdp::after_launch(what)) return st;
       launch_product<Kind::Sym>(poly, tile, stream);
       if (fsdp_status st = fsdp::after_launch(what)) return st;
       for (const ProdArgs& u : up) {
-        if (u.tiles == 0) continue;
+        if (u.slots == 0) continue;
         if (last) launch_product<Kind::Final>(u, tile, stream);
         else launch_product<Kind::Update>(u, tile, stream);
         if (fsdp_status st = fsdp::after_launch(what)) return st;
