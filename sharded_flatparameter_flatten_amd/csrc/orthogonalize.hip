@@ -63,9 +63,8 @@ constexpr int kSumRow = 8192;         // a contiguous matrix is summed as rows o
 struct Prod {
   const f16* a;
   const f16* b;
-  f16* c;            // [i][j], or null
-  f16* ct;           // [j][i], or null
-  const f16* d;      // symmetric addend, or null
+  f16* c;            // [i][j]
+  f16* ct;           // [j][i]
   uint16_t* out;     // final bf16 output [j][i], bounded by out_j and out_i
   int64_t out_ld;
   int32_t lda, ldb, ldc, ldct;
@@ -79,7 +78,7 @@ struct ProdArgs {
   Prod p[kMaxMats];
   int32_t np;
   int32_t slots;     // workgroups on one XCD
-  float alpha, beta, delta;   // result = alpha * sum + beta * D + delta * I
+  float alpha, beta, delta;   // Poly: alpha * sum + beta * A + delta * I; else alpha * sum
 };
 
 // Tile t of a ti x tj grid, walked in bands of 8 tile rows.
@@ -97,7 +96,7 @@ __device__ __forceinline__ void tri_of(int t, int& i, int& j) {
   j = t - r * (r + 1) / 2;
 }
 
-enum class Kind { Sym, Update, Final };
+enum class Kind { Gram, Poly, Update, Final };
 
 // Every load of this wave has landed, in registers or in LDS.
 __device__ __forceinline__ void wait_all() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
@@ -124,7 +123,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   static_assert(kPer % 2 == 0, "a wave's first load is of an even q");
   constexpr int MI = T / WM / 32, NI = T / WN / 32;
   constexpr int kStage = 2 * T * kBK * 2;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
+  constexpr int kLds = std::max(2 * kStage, T * (2 * T + 16));   // two stages, or the result
+  __shared__ __attribute__((aligned(1024))) char lds[kLds];
 
   // Workgroup b runs on XCD b % 8. Every XCD takes an eighth of each matrix, in
   // one run of tiles, whose shared rows then stay in its L2; the matrix of the
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   const Prod& p = args.p[s];
   const int local = xcd * p.per_xcd + slot - (s ? args.p[s - 1].slot_end : 0);
   int ti, tj;
-  if constexpr (KIND == Kind::Sym) {
+  if constexpr (KIND == Kind::Gram || KIND == Kind::Poly) {
     if (local >= p.ti * (p.ti + 1) / 2) return;
     tri_of(local, ti, tj);
   } else {
@@ -235,46 +235,91 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   if (kt > 1) stage(kt - 2, false_type{}, true_type{});
   stage(kt - 1, false_type{}, false_type{});
 
-  // A lane's acc[x][y][4 g + e] holds i = 8 g + 4 (lane / 32) + e of one j = lane % 32.
-  const int i0 = ti * T + wm * (T / WM) + (lane >> 5) * 4, j0 = tj * T + wn * (T / WN) + (lane & 31);
+  // The result goes through LDS, so that global memory is written in whole
+  // lines: as it lies in the registers, a lane holds 4 values of each of 64
+  // lines, and writing those directly took as long as a third of the main loop
+  // at 4096. acc[x][y][4 g + e] is i = 8 g + 4 (lane / 32) + e of one j = lane % 32.
+  // A row of LDS is T values and 16 bytes more, which spreads a column over all banks.
+  constexpr int kRow = 2 * T + 16, kChunks = T / 8, kThreads = 64 * kWaves;
+  const int64_t i0 = int64_t(ti) * T, j0 = int64_t(tj) * T;
+  const int il = wm * (T / WM) + (lane >> 5) * 4, jl = wn * (T / WN) + (lane & 31);
+  auto each_chunk = [&](auto f) {                 // 8 values of one row a lane
+#pragma unroll
+    for (int q = 0; q < T * kChunks / kThreads; ++q) {
+      const int at = q * kThreads + threadIdx.x;
+      f(at / kChunks, at % kChunks * 8);
+    }
+  };
+  auto row_at = [&](int row, int col) { return lds + row * kRow + col * 2; };
+
+  if constexpr (KIND == Kind::Poly) {             // S, in the order of its mirror image
+    each_chunk([&](int row, int col) {
+      *reinterpret_cast<f16x8*>(row_at(row, col)) =
+          *reinterpret_cast<const f16x8*>(p.a + (j0 + row) * p.lda + i0 + col);
+    });
+    __syncthreads();
+  }
+  f16x4 result[MI][NI][4];
 #pragma unroll
   for (int x = 0; x < MI; ++x)
 #pragma unroll
     for (int y = 0; y < NI; ++y)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int i = i0 + x * 32 + g * 8, j = j0 + y * 32;
+        const int i = il + x * 32 + g * 8, j = jl + y * 32;
+        u32x2* at = reinterpret_cast<u32x2*>(row_at(j, i));
         f32x4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = acc[x][y][4 * g + e] * args.alpha;
         if constexpr (KIND == Kind::Final) {
-          if (j < p.out_j) {
-            uint16_t* o = p.out + int64_t(j) * p.out_ld + i;
-            if (i + 4 <= p.out_i) {
-              st_loose<u32x2, 2>(o, u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)});
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (i + e < p.out_i) o[e] = uint16_t(to_bf16(v[e]));
-            }
-          }
-        } else {
-          if constexpr (KIND == Kind::Sym) {
-            if (p.d) {
-              const f16x4 d = *reinterpret_cast<const f16x4*>(p.d + int64_t(j) * p.ldct + i);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[e] = v[e] + args.beta * float(d[e]) + (i + e == j ? args.delta : 0.f);
-            }
-          }
-          const f16x4 q = {f16(v.x), f16(v.y), f16(v.z), f16(v.w)};
-          *reinterpret_cast<f16x4*>(p.ct + int64_t(j) * p.ldct + i) = q;
-          if (KIND == Kind::Update || ti != tj) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p.c[int64_t(i + e) * p.ldc + j] = q[e];
-          }
+          *at = u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)};
+          continue;
         }
+        if constexpr (KIND == Kind::Poly) {
+          const f16x4 d = __builtin_bit_cast(f16x4, *at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = v[e] + args.beta * float(d[e]) + (i0 + i + e == j0 + j ? args.delta : 0.f);
+        }
+        result[x][y][g] = f16x4{f16(v.x), f16(v.y), f16(v.z), f16(v.w)};
+        *at = __builtin_bit_cast(u32x2, result[x][y][g]);
       }
+  __syncthreads();
+  if constexpr (KIND == Kind::Final) {
+    each_chunk([&](int row, int col) {
+      if (j0 + row >= p.out_j || i0 + col >= p.out_i) return;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(row_at(row, col));
+      uint16_t* o = p.out + (j0 + row) * p.out_ld + i0 + col;
+      if (i0 + col + 8 <= p.out_i) {
+        st_loose<u32x4, 2>(o, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (i0 + col + e < p.out_i) o[e] = uint16_t(v[e / 2] >> (16 * (e & 1)));
+      }
+    });
+    return;
+  }
+  each_chunk([&](int row, int col) {
+    *reinterpret_cast<f16x8*>(p.ct + (j0 + row) * p.ldct + i0 + col) =
+        *reinterpret_cast<const f16x8*>(row_at(row, col));
+  });
+  if (KIND != Kind::Update && ti == tj) return;
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < MI; ++x)
+#pragma unroll
+    for (int y = 0; y < NI; ++y)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<f16*>(row_at(il + x * 32 + g * 8 + e, jl + y * 32)) = result[x][y][g][e];
+  __syncthreads();
+  each_chunk([&](int row, int col) {
+    *reinterpret_cast<f16x8*>(p.c + (i0 + row) * p.ldc + j0 + col) =
+        *reinterpret_cast<const f16x8*>(row_at(row, col));
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -579,7 +624,7 @@ fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const i
         g.kt = int32_t(q.np / kBK);
         g.ti = mt;
         Prod& o = add_product(poly, tri);
-        o.a = o.b = o.d = sm;
+        o.a = o.b = sm;
         o.c = o.ct = pm;
         o.lda = o.ldb = o.ldc = o.ldct = int32_t(q.mp);
         o.kt = int32_t(q.mp / kBK);
@@ -611,9 +656,9 @@ fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const i
           u.out_j = q.m;
         }
       }
-      launch_product<Kind::Sym>(gram, tile, stream);
+      launch_product<Kind::Gram>(gram, tile, stream);
       if (fsdp_status st = fsdp::after_launch(what)) return st;
-      launch_product<Kind::Sym>(poly, tile, stream);
+      launch_product<Kind::Poly>(poly, tile, stream);
       if (fsdp_status st = fsdp::after_launch(what)) return st;
       for (const ProdArgs& u : up) {
         if (u.slots == 0) continue;
