@@ -15,6 +15,14 @@
 // are computed, and each is stored with its mirror image. The additions of
 // a I and b S are in the second product's epilogue.
 //
+// Two steps at once: with S_2 = P_1 P_1 S_1 and P_2 its polynomial, X <- (P_2 P_1) X.
+// Everything but the first S and the last product is then m x m and symmetric
+// (polynomials of S commute), which is less work where n is well over m. The
+// diagonal stays inside P: kept apart, as a I + P', the products cancel against
+// it once S is near I. Pairs of steps and single ones alternate: two pairs in a
+// row lose half as much again to rounding (3e-3 against 2.1e-3 after 5 steps),
+// three steps at once up to six times as much.
+//
 // Numerics: the operands of the matrix instructions are fp16 and every sum is
 // held in fp32. fp16 rather than bf16, at the same rate, because each rounding
 // of X is amplified: the polynomial raises the small singular values (up to
@@ -60,6 +68,12 @@ constexpr int kSumRow = 8192;         // a contiguous matrix is summed as rows o
 // One matrix's product in a launch: C[i][j] = sum_k A[i][k] B[j][k]. Every
 // buffer is padded with zeros to whole tiles on both axes, so the kernel has
 // no bounds to check except those of the final output.
+enum Kind : int32_t {
+  kSym,      // a symmetric result: alpha * sum
+  kPoly,     // the same: alpha * sum + beta * A + delta * I
+  kUpdate,   // any result: alpha * sum
+  kFinal     // bf16 output: alpha * sum
+};
 struct Prod {
   const f16* a;
   const f16* b;
@@ -69,6 +83,8 @@ struct Prod {
   int64_t out_ld;
   int32_t lda, ldb, ldc, ldct;
   int32_t kt;        // stages
+  int32_t kind;
+  float alpha, beta, delta;
   int32_t ti, tj;    // tiles on each axis
   int32_t out_i, out_j;
   int32_t per_xcd;   // tiles on one XCD
@@ -78,7 +94,6 @@ struct ProdArgs {
   Prod p[kMaxMats];
   int32_t np;
   int32_t slots;     // workgroups on one XCD
-  float alpha, beta, delta;   // Poly: alpha * sum + beta * A + delta * I; else alpha * sum
 };
 
 // Tile t of a ti x tj grid, walked in bands of 8 tile rows.
@@ -96,8 +111,6 @@ __device__ __forceinline__ void tri_of(int t, int& i, int& j) {
   j = t - r * (r + 1) / 2;
 }
 
-enum class Kind { Gram, Poly, Update, Final };
-
 // Every load of this wave has landed, in registers or in LDS.
 __device__ __forceinline__ void wait_all() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 
@@ -114,7 +127,7 @@ __device__ __forceinline__ void wait_all() { asm volatile("s_waitcnt vmcnt(0) lg
 // stands between the halves: by then every wave holds the second half's
 // fragments in registers, so the next stage but one may be loaded over this
 // one, and has a whole stage's time to arrive.
-template <int T, int WM, int WN, Kind KIND>
+template <int T, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   constexpr int kWaves = WM * WN;
   constexpr int kLoads = 2 * T / 8;               // 1 KB loads a stage
@@ -135,7 +148,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   const Prod& p = args.p[s];
   const int local = xcd * p.per_xcd + slot - (s ? args.p[s - 1].slot_end : 0);
   int ti, tj;
-  if constexpr (KIND == Kind::Gram || KIND == Kind::Poly) {
+  const int kind = p.kind;
+  if (kind == kSym || kind == kPoly) {
     if (local >= p.ti * (p.ti + 1) / 2) return;
     tri_of(local, ti, tj);
   } else {
@@ -252,13 +266,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   };
   auto row_at = [&](int row, int col) { return lds + row * kRow + col * 2; };
 
-  if constexpr (KIND == Kind::Poly) {             // S, in the order of its mirror image
+  if (kind == kPoly) {                            // A, in the order of its mirror image
     each_chunk([&](int row, int col) {
       *reinterpret_cast<f16x8*>(row_at(row, col)) =
           *reinterpret_cast<const f16x8*>(p.a + (j0 + row) * p.lda + i0 + col);
     });
     __syncthreads();
   }
+  const float alpha = p.alpha, beta = p.beta, delta = p.delta;
   f16x4 result[MI][NI][4];
 #pragma unroll
   for (int x = 0; x < MI; ++x)
@@ -270,22 +285,22 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
         u32x2* at = reinterpret_cast<u32x2*>(row_at(j, i));
         f32x4 v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[x][y][4 * g + e] * args.alpha;
-        if constexpr (KIND == Kind::Final) {
+        for (int e = 0; e < 4; ++e) v[e] = acc[x][y][4 * g + e] * alpha;
+        if (kind == kFinal) {
           *at = u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)};
           continue;
         }
-        if constexpr (KIND == Kind::Poly) {
+        if (kind == kPoly) {
           const f16x4 d = __builtin_bit_cast(f16x4, *at);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            v[e] = v[e] + args.beta * float(d[e]) + (i0 + i + e == j0 + j ? args.delta : 0.f);
+            v[e] = v[e] + beta * float(d[e]) + (i0 + i + e == j0 + j ? delta : 0.f);
         }
         result[x][y][g] = f16x4{f16(v.x), f16(v.y), f16(v.z), f16(v.w)};
         *at = __builtin_bit_cast(u32x2, result[x][y][g]);
       }
   __syncthreads();
-  if constexpr (KIND == Kind::Final) {
+  if (kind == kFinal) {
     each_chunk([&](int row, int col) {
       if (j0 + row >= p.out_j || i0 + col >= p.out_i) return;
       const u32x4 v = *reinterpret_cast<const u32x4*>(row_at(row, col));
@@ -300,11 +315,20 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
     });
     return;
   }
+  // A tile on the diagonal is made exactly symmetric, like the mirrored ones: a
+  // product of two matrices that commute only up to rounding is not, and later
+  // products would amplify the difference (four times the error after 5 steps).
+  const bool diagonal = kind != kUpdate && ti == tj;
   each_chunk([&](int row, int col) {
-    *reinterpret_cast<f16x8*>(p.ct + (j0 + row) * p.ldct + i0 + col) =
-        *reinterpret_cast<const f16x8*>(row_at(row, col));
+    f16x8 v = *reinterpret_cast<const f16x8*>(row_at(row, col));
+    if (diagonal && col < row) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (col + e < row) v[e] = *reinterpret_cast<const f16*>(row_at(col + e, row));
+    }
+    *reinterpret_cast<f16x8*>(p.ct + (j0 + row) * p.ldct + i0 + col) = v;
   });
-  if (KIND != Kind::Update && ti == tj) return;
+  if (diagonal) return;
   __syncthreads();
 #pragma unroll
   for (int x = 0; x < MI; ++x)
@@ -454,7 +478,7 @@ __global__ __launch_bounds__(256) void k_ortho_start(SourceArgs args) {
 struct Plan {
   int32_t rows, cols, m, n;   // m <= n
   int64_t mp, np;             // padded
-  int64_t x, xt0, xt1, s, p, partial;   // workspace offsets
+  int64_t x, xt0, xt1, sym0, sym1, sym2, partial;   // workspace offsets
   int32_t parts;
 };
 
@@ -490,6 +514,13 @@ int choose_tile(int32_t count, const int64_t* rows, const int64_t* cols) {
   }
   return best;
 }
+
+// Whether a matrix takes its steps in pairs (see the head of this file): the
+// products of a pair cost 3 m^2 n + 5 m^3 multiply-adds against 6 m^2 n + 2 m^3
+// and one launch more, so they pay from some n / m above 1 on. Nearly square
+// matrices, whose least singular values are tiny, also lose more that way
+// (2.9e-3 against 2.3e-3 after 5 steps at n = m; alike from n = 1.25 m on).
+bool pair_steps(const Plan& q) { return 4 * int64_t(q.n) >= 5 * int64_t(q.m) && 4 * q.np >= 5 * q.mp; }
 
 constexpr int64_t kMaxSide = int64_t(1) << 20;
 
@@ -529,8 +560,9 @@ int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int t
       q.x = take(q.mp * q.np * 2);
       q.xt0 = take(q.mp * q.np * 2);
       q.xt1 = take(q.mp * q.np * 2);
-      q.s = take(q.mp * q.mp * 2);
-      q.p = take(q.mp * q.mp * 2);
+      q.sym0 = take(q.mp * q.mp * 2);
+      q.sym1 = take(q.mp * q.mp * 2);
+      q.sym2 = pair_steps(q) ? take(q.mp * q.mp * 2) : 0;
       q.parts = int32_t(std::min<int64_t>(kSumBlocks, (int64_t(q.m) * q.n + kSumRow - 1) / kSumRow));
       q.partial = take(q.parts * 8);
     }
@@ -539,19 +571,81 @@ int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int t
   return at;
 }
 
-// Adds a product of `tiles` tiles to a launch.
-Prod& add_product(ProdArgs& a, int tiles) {
-  Prod& p = a.p[a.np++];
-  p.per_xcd = (tiles + 7) / 8;
-  a.slots += p.per_xcd;
-  p.slot_end = a.slots;
-  return p;
+void launch_products(const ProdArgs& a, int tile, hipStream_t stream) {
+  if (tile == 256) k_ortho_product<256, 2, 4><<<8 * a.slots, 512, 0, stream>>>(a);
+  else k_ortho_product<128, 2, 2><<<8 * a.slots, 256, 0, stream>>>(a);
 }
 
-template <Kind KIND>
-void launch_product(const ProdArgs& a, int tile, hipStream_t stream) {
-  if (tile == 256) k_ortho_product<256, 2, 4, KIND><<<8 * a.slots, 512, 0, stream>>>(a);
-  else k_ortho_product<128, 2, 2, KIND><<<8 * a.slots, 256, 0, stream>>>(a);
+// The products of one matrix, in order; the n-th of every matrix go into one launch.
+void list_products(const Plan& q, char* ws, int tile, int steps, const double* coeffs,
+                   void* out, int64_t out_ld, std::vector<Prod>* list) {
+  auto at = [&](int64_t offset) { return reinterpret_cast<f16*>(ws + offset); };
+  f16 *x = at(q.x), *xt = at(q.xt0), *xt_next = at(q.xt1);
+  f16 *s0 = at(q.sym0), *s1 = at(q.sym1), *s2 = at(q.sym2);
+  const int mt = int(q.mp / tile), nt = int(q.np / tile);
+  auto add = [&](Kind kind, const f16* a, const f16* b, int64_t ld, double alpha) -> Prod& {
+    list->emplace_back();
+    Prod& p = list->back();
+    p = Prod{};
+    p.kind = kind;
+    p.a = a;
+    p.b = b;
+    p.lda = p.ldb = int32_t(ld);
+    p.kt = int32_t(ld / kBK);
+    p.alpha = float(alpha);
+    p.ti = p.tj = mt;
+    return p;
+  };
+  auto symmetric = [&](Kind kind, const f16* a, const f16* b, f16* to, int64_t ld, double alpha) -> Prod& {
+    Prod& p = add(kind, a, b, ld, alpha);
+    p.c = p.ct = to;
+    p.ldc = p.ldct = int32_t(q.mp);
+    return p;
+  };
+  auto poly = [&](const f16* a, f16* to) {
+    Prod& p = symmetric(kPoly, a, a, to, q.mp, coeffs[2] / kScaleS);
+    p.beta = float(coeffs[1]);
+    p.delta = float(coeffs[0]) * kScaleS;
+  };
+  auto multiply = [&](const f16* a, const f16* b, f16* to) {
+    symmetric(kSym, a, b, to, q.mp, 1.0 / kScaleS);
+  };
+  const bool pairs = pair_steps(q);
+  for (int step = 0, group = 0; step < steps; ++group) {
+    const int n = pairs && group % 2 == 0 && step + 2 <= steps ? 2 : 1;
+    step += n;
+    symmetric(kSym, x, x, s0, q.np, double(kScaleS) / (double(kScaleX) * kScaleX));
+    poly(s0, s1);                               // P_1
+    f16* p = s1;
+    if (n == 2) {
+      multiply(s1, s0, s2);                     // P_1 S_1
+      multiply(s1, s2, s0);                     // S_2 = P_1 P_1 S_1
+      poly(s0, s2);                             // P_2
+      multiply(s2, s1, s0);                     // P_2 P_1
+      p = s0;
+    }
+    const bool last = step == steps;
+    Prod& u = add(last ? kFinal : kUpdate, xt, p, q.mp,
+                  last ? 1.0 / (double(kScaleS) * kScaleX) : 1.0 / kScaleS);
+    u.ti = nt;
+    u.out_i = q.n;
+    u.out_j = q.m;
+    if (!last) {
+      u.c = xt_next;
+      u.ldc = int32_t(q.mp);
+      u.ct = x;
+      u.ldct = int32_t(q.np);
+      std::swap(xt, xt_next);
+    } else {
+      u.out = static_cast<uint16_t*>(out);
+      u.out_ld = out_ld;
+      if (q.rows > q.cols) {                    // the output's rows are X^T's
+        std::swap(u.a, u.b);
+        std::swap(u.ti, u.tj);
+        std::swap(u.out_i, u.out_j);
+      }
+    }
+  }
 }
 
 template <typename T>
@@ -562,10 +656,6 @@ fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const i
   std::vector<int> live;
   for (size_t i = 0; i < plans.size(); ++i)
     if (plans[i].m > 0) live.push_back(int(i));
-  // longest contractions first, in S = X X^T and in the others
-  std::stable_sort(live.begin(), live.end(), [&](int a, int b) {
-    return plans[a].np != plans[b].np ? plans[a].np > plans[b].np : plans[a].mp > plans[b].mp;
-  });
   for (size_t b = 0; b < live.size(); b += kMaxMats) {
     const int nb = int(std::min<size_t>(kMaxMats, live.size() - b));
     SourceArgs src{};
@@ -599,73 +689,29 @@ fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const i
     k_ortho_start<T><<<blocks, 256, 0, stream>>>(src);
     if (fsdp_status st = fsdp::after_launch(what)) return st;
 
-    for (int step = 0; step < steps; ++step) {
-      const bool last = step + 1 == steps;
-      ProdArgs gram{}, poly{}, up[2] = {};        // up[1]: the last step of tall matrices
-      gram.alpha = kScaleS / (kScaleX * kScaleX);
-      poly.alpha = float(coeffs[2] / kScaleS);
-      poly.beta = float(coeffs[1]);
-      poly.delta = float(coeffs[0]) * kScaleS;
-      up[0].alpha = up[1].alpha = last ? 1.f / (kScaleS * kScaleX) : 1.f / kScaleS;
-      for (int k = 0; k < nb; ++k) {
-        const int i = live[b + k];
-        const Plan& q = plans[i];
-        f16* x = reinterpret_cast<f16*>(ws + q.x);
-        f16* xt = reinterpret_cast<f16*>(ws + (step & 1 ? q.xt1 : q.xt0));
-        f16* xt_next = reinterpret_cast<f16*>(ws + (step & 1 ? q.xt0 : q.xt1));
-        f16* sm = reinterpret_cast<f16*>(ws + q.s);
-        f16* pm = reinterpret_cast<f16*>(ws + q.p);
-        const int mt = int(q.mp / tile), nt = int(q.np / tile), tri = mt * (mt + 1) / 2;
-        Prod& g = add_product(gram, tri);
-        g.a = g.b = x;
-        g.c = g.ct = sm;
-        g.lda = g.ldb = int32_t(q.np);
-        g.ldc = g.ldct = int32_t(q.mp);
-        g.kt = int32_t(q.np / kBK);
-        g.ti = mt;
-        Prod& o = add_product(poly, tri);
-        o.a = o.b = sm;
-        o.c = o.ct = pm;
-        o.lda = o.ldb = o.ldc = o.ldct = int32_t(q.mp);
-        o.kt = int32_t(q.mp / kBK);
-        o.ti = mt;
-        const bool tall = q.rows > q.cols;
-        ProdArgs& ua = up[last && tall ? 1 : 0];
-        Prod& u = add_product(ua, mt * nt);
-        u.lda = u.ldb = int32_t(q.mp);
-        u.kt = int32_t(q.mp / kBK);
-        u.out = static_cast<uint16_t*>(outs[i]);
-        u.out_ld = out_ld[i];
-        if (last && tall) {                       // i along m: the output's rows are X^T's
-          u.a = pm;
-          u.b = xt;
-          u.ti = mt;
-          u.tj = nt;
-          u.out_i = q.m;
-          u.out_j = q.n;
-        } else {
-          u.a = xt;
-          u.b = pm;
-          u.ti = nt;
-          u.tj = mt;
-          u.c = xt_next;
-          u.ldc = int32_t(q.mp);
-          u.ct = x;
-          u.ldct = int32_t(q.np);
-          u.out_i = q.n;
-          u.out_j = q.m;
-        }
+    std::vector<std::vector<Prod>> lists(nb);
+    size_t longest = 0;
+    for (int k = 0; k < nb; ++k) {
+      const int i = live[b + k];
+      list_products(plans[i], ws, tile, steps, coeffs, outs[i], out_ld[i], &lists[k]);
+      longest = std::max(longest, lists[k].size());
+    }
+    for (size_t n = 0; n < longest; ++n) {
+      std::vector<const Prod*> now;
+      for (const std::vector<Prod>& list : lists)
+        if (n < list.size()) now.push_back(&list[n]);
+      std::stable_sort(now.begin(), now.end(), [](const Prod* a, const Prod* b) { return a->kt > b->kt; });
+      ProdArgs args{};
+      for (const Prod* p : now) {
+        Prod& to = args.p[args.np++] = *p;
+        const bool sym = p->kind == kSym || p->kind == kPoly;
+        const int tiles = sym ? p->ti * (p->ti + 1) / 2 : p->ti * p->tj;
+        to.per_xcd = (tiles + 7) / 8;
+        args.slots += to.per_xcd;
+        to.slot_end = args.slots;
       }
-      launch_product<Kind::Gram>(gram, tile, stream);
+      launch_products(args, tile, stream);
       if (fsdp_status st = fsdp::after_launch(what)) return st;
-      launch_product<Kind::Poly>(poly, tile, stream);
-      if (fsdp_status st = fsdp::after_launch(what)) return st;
-      for (const ProdArgs& u : up) {
-        if (u.slots == 0) continue;
-        if (last) launch_product<Kind::Final>(u, tile, stream);
-        else launch_product<Kind::Update>(u, tile, stream);
-        if (fsdp_status st = fsdp::after_launch(what)) return st;
-      }
     }
   }
   return FSDP_OK;
