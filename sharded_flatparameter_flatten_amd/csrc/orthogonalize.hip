@@ -85,15 +85,15 @@ struct Prod {
   int32_t kt;        // stages
   int32_t kind;
   float alpha, beta, delta;
+  int32_t side_i, side_j;   // padded lengths
   int32_t ti, tj;    // tiles on each axis
   int32_t out_i, out_j;
   int32_t per_xcd;   // tiles on one XCD
-  int32_t slot_end;  // exclusive prefix of per_xcd over the launch
 };
 struct ProdArgs {
   Prod p[kMaxMats];
-  int32_t np;
-  int32_t slots;     // workgroups on one XCD
+  int32_t slot_end[kMaxMats];   // exclusive prefix of per_xcd; past the last: the largest int
+  int32_t slots;                // workgroups on one XCD
 };
 
 // Tile t of a ti x tj grid, walked in bands of 8 tile rows.
@@ -111,42 +111,56 @@ __device__ __forceinline__ void tri_of(int t, int& i, int& j) {
   j = t - r * (r + 1) / 2;
 }
 
-// Every load of this wave has landed, in registers or in LDS.
-__device__ __forceinline__ void wait_all() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+// At most N global loads of this wave are still under way, and no LDS read.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 // T x T tile by WM x WN waves, on 32 x 32 x 16 matrix instructions.
 //
-// LDS holds two stages of both operands; a stage row is 128 bytes, 8 chunks of
-// 16. Global loads go straight to LDS, 8 rows each: lane l of a load fills chunk
-// l % 8 of row l / 8. Chunk c of row r sits at c ^ (r / 2 % 8), so that the
-// fragment reads (32 rows, one chunk each), which LDS serves 16 lanes, 256
-// bytes, at a time, touch each of its 64 banks once.
+// LDS holds S stages (a power of two) of both operands; a stage row is 128
+// bytes, 8 chunks of 16. Global loads go straight to LDS, 8 rows each: lane l of
+// a load fills chunk l % 8 of row l / 8. Chunk c of row r sits at c ^ (r / 2 % 8),
+// so that the fragment reads (32 rows, one chunk each), which LDS serves 16
+// lanes, 256 bytes, at a time, touch each of its 64 banks once.
 //
 // A stage is worked off in two halves, and the fragments of the next half are
 // read while the matrix instructions of this one run. The stage's one barrier
 // stands between the halves: by then every wave holds the second half's
-// fragments in registers, so the next stage but one may be loaded over this
-// one, and has a whole stage's time to arrive.
-template <int T, int WM, int WN>
+// fragments in registers, so stage k + S may be loaded over stage k, and has
+// S - 1 stages' time to arrive.
+template <int T, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   constexpr int kWaves = WM * WN;
   constexpr int kLoads = 2 * T / 8;               // 1 KB loads a stage
   static_assert(kWaves % 2 == 0 && kLoads % kWaves == 0, "whole loads per wave");
   constexpr int kPer = kLoads / kWaves;
   static_assert(kPer % 2 == 0, "a wave's first load is of an even q");
+  static_assert(S >= 2 && (S & (S - 1)) == 0 && (S - 1) * kPer < 64, "stages");
   constexpr int MI = T / WM / 32, NI = T / WN / 32;
   constexpr int kStage = 2 * T * kBK * 2;
-  constexpr int kLds = std::max(2 * kStage, T * (2 * T + 16));   // two stages, or the result
+  constexpr int kLds = std::max(S * kStage, T * (2 * T + 16));   // the stages, or the result
   __shared__ __attribute__((aligned(1024))) char lds[kLds];
 
   // Workgroup b runs on XCD b % 8. Every XCD takes an eighth of each matrix, in
   // one run of tiles, whose shared rows then stay in its L2; the matrix of the
   // longest contraction comes first, so that no XCD ends on a long tile.
   const int xcd = blockIdx.x % 8, slot = blockIdx.x / 8;
-  int s = 0;
-  while (slot >= args.p[s].slot_end) ++s;         // slot < slots: ends at the last entry
+  int s = 0, before = 0;
+#pragma unroll
+  for (int q = 0; q < kMaxMats - 1; ++q) {        // slot < the last entry's end
+    const int end = args.slot_end[q];
+    s += slot >= end;
+    before = slot >= end ? end : before;
+  }
+  s = __builtin_amdgcn_readfirstlane(s);
   const Prod& p = args.p[s];
-  const int local = xcd * p.per_xcd + slot - (s ? args.p[s - 1].slot_end : 0);
+  const int local = xcd * p.per_xcd + slot - __builtin_amdgcn_readfirstlane(before);
   int ti, tj;
   const int kind = p.kind;
   if (kind == kSym || kind == kPoly) {
@@ -168,13 +182,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   // row 8 q + lane / 8: its r / 2 % 8 is lane / 16, plus 4 for odd q
   const int v0 = (lane >> 3) * ld * 2 + ((lane & 7) ^ (lane >> 4)) * 16, v1 = v0 ^ 64;
 
+  auto load_one = [&](int k, int q) {             // 8 rows of stage k
+    char* to = lds + (k & (S - 1)) * kStage + (wave * kPer + q) * 1024;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        r, (__attribute__((address_space(3))) void*)to, 16, q & 1 ? v1 : v0,
+        (first + q) * 8 * ld * 2 + k * (kBK * 2), 0, 0);
+  };
   auto load = [&](int k) {
-    char* to = lds + (k & 1) * kStage + wave * (kPer * 1024);
 #pragma unroll
-    for (int q = 0; q < kPer; ++q)                // 8 rows each
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          r, (__attribute__((address_space(3))) void*)(to + q * 1024), 16, q & 1 ? v1 : v0,
-          (first + q) * 8 * ld * 2 + k * (kBK * 2), 0, 0);
+    for (int q = 0; q < kPer; ++q) load_one(k, q);
   };
 
   f32x16 acc[MI][NI];
@@ -188,66 +204,75 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   // A lane's fragment: row lane % 32, 8 elements at chunk 2 q + lane / 32 of the stage row.
   const int frag = (lane & 31) * 128, c0 = ((lane >> 5) ^ ((lane >> 1) & 7)) * 16;
   const int oa = wm * (T / WM) * 128 + frag, ob = (T + wn * (T / WN)) * 128 + frag;
+  constexpr int kReads = 2 * (MI + NI), kMuls = 2 * MI * NI;
   f16x8 fa[2][2][MI], fb[2][2][NI];               // [half][q][fragment]
-  auto read = [&](int k, int h) {
-    const char* st = lds + (k & 1) * kStage;
+  auto read_one = [&](int k, int h, int n) {      // the n-th fragment of a half
+    const int q = n / (MI + NI), w = n % (MI + NI);
+    const char* st = lds + (k & (S - 1)) * kStage + (c0 ^ (h * 64 + q * 32));
+    if (w < NI) fb[h][q][w] = *reinterpret_cast<const f16x8*>(st + ob + w * 4096);
+    else fa[h][q][w - NI] = *reinterpret_cast<const f16x8*>(st + oa + (w - NI) * 4096);
+  };
+  // The multiplies of half h of stage k, each followed by a share of the next
+  // half's fragment reads and, in the second half, of the loads of stage k + S
+  // (reads and loads in this order: both are LDS accesses to the compiler).
+  auto half = [&](int k, int h, auto load_next, auto read_next) {
+    int reads = 0, loads = 0;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int c = c0 ^ (h * 64 + q * 32);
+    for (int i = 0; i < kMuls; ++i) {
+      if constexpr (read_next.value) {
 #pragma unroll
-      for (int x = 0; x < MI; ++x) fa[h][q][x] = *reinterpret_cast<const f16x8*>(st + oa + x * 4096 + c);
+        for (int z = 0; z < kReads; ++z)
+          if (reads < kReads && reads <= i + 1) {
+            read_one(h ? k + 1 : k, 1 - h, reads++);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          }
+      }
+      const int q = i / (MI * NI), x = i % (MI * NI) / NI, y = i % NI;
+      acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[h][q][x], fb[h][q][y], acc[x][y], 0, 0, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if constexpr (load_next.value) {
 #pragma unroll
-      for (int y = 0; y < NI; ++y) fb[h][q][y] = *reinterpret_cast<const f16x8*>(st + ob + y * 4096 + c);
+        for (int z = 0; z < kPer; ++z)
+          if (loads < kPer && loads * kMuls < (i + 1) * kPer * 2) {
+            load_one(k + S, loads++);
+            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+          }
+      }
     }
-  };
-  auto multiply = [&](int h) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int x = 0; x < MI; ++x)
-#pragma unroll
-        for (int y = 0; y < NI; ++y)
-          acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[h][q][x], fb[h][q][y], acc[x][y], 0, 0, 0);
-  };
-  // Matrix instructions of one half with the fragment reads of the next between them.
-  auto interleave = [&] {
-    constexpr int kReads = 2 * (MI + NI), kMul = 2 * MI * NI;
-#pragma unroll
-    for (int i = 0; i < kReads; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                     // a read
-      if ((i + 1) * kMul / kReads > i * kMul / kReads)
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                   // a multiply
-    }
-  };
-
-  // Stage k; LOAD: stage k + 2 exists, READ: stage k + 1 does.
-  auto stage = [&](int k, auto load_next, auto read_next) {
-    read(k, 1);
-    multiply(0);
-    interleave();
-    __builtin_amdgcn_sched_barrier(0);
-    wait_all();                                   // fragments read; the next stage has landed
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if constexpr (load_next.value) load(k + 2);
-    if constexpr (read_next.value) read(k + 1, 0);
-    multiply(1);
-    if constexpr (read_next.value) interleave();
     __builtin_amdgcn_sched_barrier(0);
   };
   using std::false_type;
   using std::true_type;
 
   const int kt = p.kt;
-  load(0);
-  wait_all();
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  if (kt > 1) load(1);
-  read(0, 0);
-  for (int k = 0; k + 2 < kt; ++k) stage(k, true_type{}, true_type{});
-  if (kt > 1) stage(kt - 2, false_type{}, true_type{});
-  stage(kt - 1, false_type{}, false_type{});
+  if (kt >= S) {
+#pragma unroll
+    for (int k = 0; k < S; ++k) load(k);
+    wait_loads<(S - 1) * kPer>();
+  } else {
+    for (int k = 0; k < kt; ++k) load(k);
+    wait_loads<0>();
+  }
+  meet();
+#pragma unroll
+  for (int n = 0; n < kReads; ++n) read_one(0, 0, n);
+  int k = 0;
+  for (; k + S < kt; ++k) {                       // stages k + 2 to k + S - 1 may be under way
+    half(k, 0, false_type{}, true_type{});
+    wait_loads<(S - 2) * kPer>();
+    meet();
+    half(k, 1, true_type{}, true_type{});
+  }
+  for (; k + 1 < kt; ++k) {
+    half(k, 0, false_type{}, true_type{});
+    wait_loads<0>();
+    meet();
+    half(k, 1, false_type{}, true_type{});
+  }
+  half(k, 0, false_type{}, true_type{});
+  wait_loads<0>();
+  meet();
+  half(k, 1, false_type{}, false_type{});
 
   // The result goes through LDS, so that global memory is written in whole
   // lines: as it lies in the registers, a lane holds 4 values of each of 64
@@ -484,32 +509,21 @@ struct Plan {
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// The tile side of a call: 256 or 128. A larger tile reads less from LDS for
-// each matrix instruction; a smaller one pads less and gives more workgroups.
-// Estimated cost: padded multiply-adds of a step over the share of the 256 CUs
-// that its tiles keep busy.
-int choose_tile(int32_t count, const int64_t* rows, const int64_t* cols) {
-  int best = 128;
+// What a call's matrices are padded to: the largest tile that grows no side's
+// share of the work much. Every launch then takes that tile or a smaller one.
+int choose_pad(int32_t count, const int64_t* rows, const int64_t* cols) {
   double least = 0;
-  for (int t : {256, 128}) {
-    double cost = 0;
-    double tiles[3] = {0, 0, 0}, depth[3] = {0, 0, 0};
+  int best = 64;
+  for (int t : {64, 128, 256}) {
+    double work = 0;
     for (int32_t i = 0; i < count; ++i) {
-      const double m = double(round_up(std::min(rows[i], cols[i]), t)) / t;
-      const double n = double(round_up(std::max(rows[i], cols[i]), t)) / t;
-      const double tri = m * (m + 1) / 2, tl[3] = {tri, tri, m * n}, dp[3] = {n, m, m};
-      for (int k = 0; k < 3; ++k) {
-        tiles[k] += tl[k];
-        depth[k] += tl[k] * dp[k];
-      }
+      const double m = double(round_up(std::min(rows[i], cols[i]), t)), n = double(round_up(std::max(rows[i], cols[i]), t));
+      work += 3 * m * m * n + m * m * m;
     }
-    const double slots = t == 256 ? 256 : 512;
-    for (int k = 0; k < 3; ++k)
-      if (tiles[k] > 0)
-        cost += depth[k] / tiles[k] * std::ceil(tiles[k] / slots) * double(t) * t * t * (t == 256 ? 1.0 : 2 * 1.3);
-    if (t == 256 || cost < least) {
+    work *= t == 256 ? 1.0 : t == 128 ? 1.2 : 1.6;       // measured at full size
+    if (t == 64 || work <= least) {
       best = t;
-      least = cost;
+      least = work;
     }
   }
   return best;
@@ -540,7 +554,7 @@ fsdp_status check_shapes(int32_t count, const int64_t* rows, const int64_t* cols
 }
 
 // Lays the buffers of every matrix that has elements out in the workspace.
-int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int tile,
+int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int pad,
                   std::vector<Plan>* plans) {
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -555,8 +569,8 @@ int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int t
     q.m = std::min(q.rows, q.cols);
     q.n = std::max(q.rows, q.cols);
     if (q.m > 0) {
-      q.mp = round_up(q.m, tile);
-      q.np = round_up(q.n, tile);
+      q.mp = round_up(q.m, pad);
+      q.np = round_up(q.n, pad);
       q.x = take(q.mp * q.np * 2);
       q.xt0 = take(q.mp * q.np * 2);
       q.xt1 = take(q.mp * q.np * 2);
@@ -571,18 +585,57 @@ int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int t
   return at;
 }
 
-void launch_products(const ProdArgs& a, int tile, hipStream_t stream) {
-  if (tile == 256) k_ortho_product<256, 2, 4><<<8 * a.slots, 512, 0, stream>>>(a);
-  else k_ortho_product<128, 2, 2><<<8 * a.slots, 256, 0, stream>>>(a);
+// Workgroups of a launch on tiles of t, and its estimated time in units of one
+// stage of a 256 tile.
+int64_t tiles_of(const Prod& p, int t) {
+  const int64_t i = p.side_i / t, j = p.side_j / t;
+  return p.kind == kSym || p.kind == kPoly ? i * (i + 1) / 2 : i * j;
+}
+
+int launch_tile(const std::vector<const Prod*>& now, int pad) {
+  int best = pad;
+  double least = 0;
+  for (int t = pad; t >= 64; t /= 2) {
+    // stage time of a workgroup and workgroups per CU, measured
+    const double stage = t == 256 ? 1.0 : t == 128 ? 0.42 : 0.2, per_cu = t == 256 ? 1 : 2;
+    double work = 0, longest = 0;
+    for (const Prod* p : now) {
+      work += double(tiles_of(*p, t)) * (p->kt + 6) * stage;
+      longest = std::max(longest, (p->kt + 6) * stage);
+    }
+    const double time = std::max(longest, work / (256 * per_cu) + longest / 2);
+    if (t == pad || time < least) {
+      best = t;
+      least = time;
+    }
+  }
+  return best;
+}
+
+void launch_products(const std::vector<const Prod*>& now, int pad, hipStream_t stream) {
+  const int tile = launch_tile(now, pad);
+  ProdArgs a{};
+  std::fill(a.slot_end, a.slot_end + kMaxMats, INT32_MAX);
+  int n = 0;
+  for (const Prod* p : now) {
+    Prod& to = a.p[n] = *p;
+    to.ti = p->side_i / tile;
+    to.tj = p->side_j / tile;
+    to.per_xcd = int32_t((tiles_of(*p, tile) + 7) / 8);
+    a.slots += to.per_xcd;
+    a.slot_end[n++] = a.slots;
+  }
+  if (tile == 256) k_ortho_product<256, 2, 4, 2><<<8 * a.slots, 512, 0, stream>>>(a);
+  else if (tile == 128) k_ortho_product<128, 2, 2, 2><<<8 * a.slots, 256, 0, stream>>>(a);
+  else k_ortho_product<64, 2, 2, 4><<<8 * a.slots, 256, 0, stream>>>(a);
 }
 
 // The products of one matrix, in order; the n-th of every matrix go into one launch.
-void list_products(const Plan& q, char* ws, int tile, int steps, const double* coeffs,
+void list_products(const Plan& q, char* ws, int steps, const double* coeffs,
                    void* out, int64_t out_ld, std::vector<Prod>* list) {
   auto at = [&](int64_t offset) { return reinterpret_cast<f16*>(ws + offset); };
   f16 *x = at(q.x), *xt = at(q.xt0), *xt_next = at(q.xt1);
   f16 *s0 = at(q.sym0), *s1 = at(q.sym1), *s2 = at(q.sym2);
-  const int mt = int(q.mp / tile), nt = int(q.np / tile);
   auto add = [&](Kind kind, const f16* a, const f16* b, int64_t ld, double alpha) -> Prod& {
     list->emplace_back();
     Prod& p = list->back();
@@ -593,7 +646,7 @@ void list_products(const Plan& q, char* ws, int tile, int steps, const double* c
     p.lda = p.ldb = int32_t(ld);
     p.kt = int32_t(ld / kBK);
     p.alpha = float(alpha);
-    p.ti = p.tj = mt;
+    p.side_i = p.side_j = int32_t(q.mp);
     return p;
   };
   auto symmetric = [&](Kind kind, const f16* a, const f16* b, f16* to, int64_t ld, double alpha) -> Prod& {
@@ -627,7 +680,7 @@ void list_products(const Plan& q, char* ws, int tile, int steps, const double* c
     const bool last = step == steps;
     Prod& u = add(last ? kFinal : kUpdate, xt, p, q.mp,
                   last ? 1.0 / (double(kScaleS) * kScaleX) : 1.0 / kScaleS);
-    u.ti = nt;
+    u.side_i = int32_t(q.np);
     u.out_i = q.n;
     u.out_j = q.m;
     if (!last) {
@@ -641,7 +694,7 @@ void list_products(const Plan& q, char* ws, int tile, int steps, const double* c
       u.out_ld = out_ld;
       if (q.rows > q.cols) {                    // the output's rows are X^T's
         std::swap(u.a, u.b);
-        std::swap(u.ti, u.tj);
+        std::swap(u.side_i, u.side_j);
         std::swap(u.out_i, u.out_j);
       }
     }
@@ -650,7 +703,7 @@ void list_products(const Plan& q, char* ws, int tile, int steps, const double* c
 
 template <typename T>
 fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const int64_t* mat_ld,
-                void* const* outs, const int64_t* out_ld, char* ws, int tile, int steps,
+                void* const* outs, const int64_t* out_ld, char* ws, int pad, int steps,
                 const double* coeffs, double eps, hipStream_t stream) {
   const char* what = "fsdp_orthogonalize";
   std::vector<int> live;
@@ -693,7 +746,7 @@ fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const i
     size_t longest = 0;
     for (int k = 0; k < nb; ++k) {
       const int i = live[b + k];
-      list_products(plans[i], ws, tile, steps, coeffs, outs[i], out_ld[i], &lists[k]);
+      list_products(plans[i], ws, steps, coeffs, outs[i], out_ld[i], &lists[k]);
       longest = std::max(longest, lists[k].size());
     }
     for (size_t n = 0; n < longest; ++n) {
@@ -701,16 +754,7 @@ fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const i
       for (const std::vector<Prod>& list : lists)
         if (n < list.size()) now.push_back(&list[n]);
       std::stable_sort(now.begin(), now.end(), [](const Prod* a, const Prod* b) { return a->kt > b->kt; });
-      ProdArgs args{};
-      for (const Prod* p : now) {
-        Prod& to = args.p[args.np++] = *p;
-        const bool sym = p->kind == kSym || p->kind == kPoly;
-        const int tiles = sym ? p->ti * (p->ti + 1) / 2 : p->ti * p->tj;
-        to.per_xcd = (tiles + 7) / 8;
-        args.slots += to.per_xcd;
-        to.slot_end = args.slots;
-      }
-      launch_products(args, tile, stream);
+      launch_products(now, pad, stream);
       if (fsdp_status st = fsdp::after_launch(what)) return st;
     }
   }
@@ -735,9 +779,9 @@ fsdp_status orthogonalize(int32_t count, fsdp_dtype dtype, const void* const* ma
     return fail(FSDP_ERR_INVALID_ARG, "eps must be finite and >= 0");
   if (count == 0) return FSDP_OK;
   const int64_t es = dtype == FSDP_F32 ? 4 : 2;
-  const int tile = choose_tile(count, rows, cols);
+  const int pad = choose_pad(count, rows, cols);
   std::vector<Plan> plans;
-  const int64_t need = make_plan(count, rows, cols, tile, &plans);
+  const int64_t need = make_plan(count, rows, cols, pad, &plans);
   if (need == 0) return FSDP_OK;               // only empty matrices
   if (!mats || !mat_ld || !outs || !out_ld)
     return fail(FSDP_ERR_INVALID_ARG, "a matrix array is NULL");
@@ -766,8 +810,8 @@ fsdp_status orthogonalize(int32_t count, fsdp_dtype dtype, const void* const* ma
   if (fsdp_status st = fsdp::check_no_pending_error(what)) return st;
   char* ws = static_cast<char*>(workspace);
   if (dtype == FSDP_F32)
-    return run<float>(plans, mats, mat_ld, outs, out_ld, ws, tile, steps, coeffs, eps, stream);
-  return run<uint16_t>(plans, mats, mat_ld, outs, out_ld, ws, tile, steps, coeffs, eps, stream);
+    return run<float>(plans, mats, mat_ld, outs, out_ld, ws, pad, steps, coeffs, eps, stream);
+  return run<uint16_t>(plans, mats, mat_ld, outs, out_ld, ws, pad, steps, coeffs, eps, stream);
 }
 
 }  // namespace
@@ -779,7 +823,7 @@ fsdp_status fsdp_orthogonalize_workspace(int32_t n_mats, const int64_t* rows, co
   fsdp::clear_error();
   if (!bytes) return fail(FSDP_ERR_INVALID_ARG, "bytes pointer is NULL");
   if (fsdp_status st = check_shapes(n_mats, rows, cols)) return st;
-  *bytes = make_plan(n_mats, rows, cols, choose_tile(n_mats, rows, cols), nullptr);
+  *bytes = make_plan(n_mats, rows, cols, choose_pad(n_mats, rows, cols), nullptr);
   return FSDP_OK;
 }
 
