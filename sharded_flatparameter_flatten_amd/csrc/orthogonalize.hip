@@ -205,6 +205,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   const int frag = (lane & 31) * 128, c0 = ((lane >> 5) ^ ((lane >> 1) & 7)) * 16;
   const int oa = wm * (T / WM) * 128 + frag, ob = (T + wn * (T / WN)) * 128 + frag;
   constexpr int kReads = 2 * (MI + NI), kMuls = 2 * MI * NI;
+  constexpr int kAhead = (kReads + kMuls - 1) / kMuls;   // reads before and after each multiply
   f16x8 fa[2][2][MI], fb[2][2][NI];               // [half][q][fragment]
   auto read_one = [&](int k, int h, int n) {      // the n-th fragment of a half
     const int q = n / (MI + NI), w = n % (MI + NI);
@@ -222,7 +223,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
       if constexpr (read_next.value) {
 #pragma unroll
         for (int z = 0; z < kReads; ++z)
-          if (reads < kReads && reads <= i + 1) {
+          if (reads < kReads && reads <= (i + 1) * kAhead) {
             read_one(h ? k + 1 : k, 1 - h, reads++);
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
           }
@@ -585,25 +586,29 @@ int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int p
   return at;
 }
 
-// Workgroups of a launch on tiles of t, and its estimated time in units of one
-// stage of a 256 tile.
+// Workgroups of a product on tiles of t.
 int64_t tiles_of(const Prod& p, int t) {
   const int64_t i = p.side_i / t, j = p.side_j / t;
   return p.kind == kSym || p.kind == kPoly ? i * (i + 1) / 2 : i * j;
 }
 
+// The tile of a launch: the one of the least estimated time. A launch takes at
+// least the chain of stages of its longest tile, and at least the work of all
+// tiles over the CUs. Units are one stage of a 256 tile (1.1 us), measured: a
+// workgroup that has its CU to itself needs 1, 0.5 or 0.37 of that a stage on a
+// tile of 256, 128 or 64, and a full CU gets through one in 1, 0.3 or 0.11; a
+// tile's start and end take about 6 stages.
 int launch_tile(const std::vector<const Prod*>& now, int pad) {
   int best = pad;
   double least = 0;
   for (int t = pad; t >= 64; t /= 2) {
-    // stage time of a workgroup and workgroups per CU, measured
-    const double stage = t == 256 ? 1.0 : t == 128 ? 0.42 : 0.2, per_cu = t == 256 ? 1 : 2;
+    const double alone = t == 256 ? 1.0 : t == 128 ? 0.5 : 0.37, full = t == 256 ? 1.0 : t == 128 ? 0.3 : 0.11;
     double work = 0, longest = 0;
     for (const Prod* p : now) {
-      work += double(tiles_of(*p, t)) * (p->kt + 6) * stage;
-      longest = std::max(longest, (p->kt + 6) * stage);
+      work += double(tiles_of(*p, t)) * (p->kt + 6) * full / 256;
+      longest = std::max(longest, double(p->kt + 6));
     }
-    const double time = std::max(longest, work / (256 * per_cu) + longest / 2);
+    const double time = std::max(longest * alone, work + longest * full / 2);
     if (t == pad || time < least) {
       best = t;
       least = time;
