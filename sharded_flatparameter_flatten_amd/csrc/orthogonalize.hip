@@ -102,13 +102,24 @@ __device__ __forceinline__ void tile_of(int t, int ti, int tj, int& i, int& j) {
   i = r0 + in % h;
   j = in / h;
 }
-// Tile t of the lower triangle, row by row: t = i (i + 1) / 2 + j, j <= i.
-__device__ __forceinline__ void tri_of(int t, int& i, int& j) {
-  int r = int((sqrtf(8.f * float(t) + 1.f) - 1.f) * 0.5f);
-  while (r * (r + 1) / 2 > t) --r;
-  while ((r + 1) * (r + 2) / 2 <= t) ++r;
-  i = r;
-  j = t - r * (r + 1) / 2;
+// Tile t of the lower triangle of n rows, in bands of 4 rows walked by columns:
+// neighbours in this order share rows of both operands.
+__device__ __forceinline__ void tri_of(int t, int n, int& i, int& j) {
+  int r = int((sqrtf(8.f * float(t) + 1.f) - 1.f) * 0.5f) & ~3;
+  while (r * (r + 1) / 2 > t) r -= 4;
+  while (r + 4 < n && (r + 4) * (r + 5) / 2 <= t) r += 4;
+  const int h = n - r < 4 ? n - r : 4;            // the band's rows
+  int in = t - r * (r + 1) / 2;
+  if (in < r * h) {
+    i = r + in % h;
+    j = in / h;
+    return;
+  }
+  in -= r * h;                                    // its own triangle
+  int c = 0;
+  while (in >= h - c) in -= h - c++;
+  i = r + c + in;
+  j = r + c;
 }
 
 // At most N global loads of this wave are still under way, and no LDS read.
@@ -165,7 +176,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   const int kind = p.kind;
   if (kind == kSym || kind == kPoly) {
     if (local >= p.ti * (p.ti + 1) / 2) return;
-    tri_of(local, ti, tj);
+    tri_of(local, p.ti, ti, tj);
   } else {
     if (local >= p.ti * p.tj) return;
     tile_of(local, p.ti, p.tj, ti, tj);
