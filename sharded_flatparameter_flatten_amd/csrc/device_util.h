@@ -57,9 +57,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0,
                                            static_cast<int>(bytes), kRsrcWord3);
 }
-// CPol of the streaming accesses: 2 = nt for loads read once, 18 = sc1 nt for stores.
-constexpr int kLoadNt = 2;
-constexpr int kStoreNt = 18;
+// A streaming store (device scope, not kept in L2: sc1 nt), for outputs far
+// larger than L2: their write-back then ends within the kernel instead of
+// slowing the next. 16-byte or 8-byte aligned.
+constexpr int kStoreStream = 18;
+__device__ __forceinline__ void st_stream(__amdgpu_buffer_rsrc_t r, int off, u32x4 x) {
+  __builtin_amdgcn_raw_buffer_store_b128(x, r, off, 0, kStoreStream);
+}
+__device__ __forceinline__ void st_stream(__amdgpu_buffer_rsrc_t r, int off, u32x2 x) {
+  __builtin_amdgcn_raw_buffer_store_b64(x, r, off, 0, kStoreStream);
+}
 
 template <typename T>
 __device__ __forceinline__ T wave_sum(T x) {

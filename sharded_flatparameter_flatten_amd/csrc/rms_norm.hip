@@ -31,50 +31,87 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.1754943508222875e-38f;   // 2^-126: a row of zeros divides by this
-constexpr int kMaxBlocks = 512;        // workgroups of a backward launch, at most
-constexpr int64_t kRegDim = 32768;     // rows up to this length are held in registers
+constexpr int64_t kStreamBytes = int64_t(32) << 20;    // outputs from here on are streamed past L2
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const uint16_t* p) { return widen(*p); }
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store1(uint16_t* p, float x) { *p = uint16_t(to_bf16(x)); }
 
-// 8 consecutive elements at column c of a row, from element alignment; the
-// elements at or past `dim` are zeros (loads) or left alone (stores).
-__device__ __forceinline__ void load8(const float* p, int64_t c, int64_t dim, float (&x)[8]) {
-  if (c + 8 <= dim) {
-    const f32x4 a = ld_loose<f32x4, 4>(p + c), b = ld_loose<f32x4, 4>(p + c + 4);
+// 8 consecutive elements of a row as they lie in memory. A lane holds kChunks<T>
+// of these, 32 bytes of every array.
+template <typename T>
+constexpr int kChunks = sizeof(T) == 2 ? 2 : 1;
+template <typename T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  u32x4 v;
+};
+template <>
+struct Raw<float> {
+  u32x4 a, b;
+};
+// From element alignment; elements at or past `dim` are zeros.
+template <typename I>   // int within a row held in registers, int64_t in the long kernels
+__device__ __forceinline__ Raw<uint16_t> load_raw(const uint16_t* p, I c, I dim) {
+  if (c + 8 <= dim) return {ld_loose<u32x4, 2>(p + c)};
+  Raw<uint16_t> r{};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) { x[e] = a[e]; x[4 + e] = b[e]; }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = c + e < dim ? p[c + e] : 0.f;
-  }
+  for (int e = 0; e < 8; ++e)
+    if (c + e < dim) r.v[e / 2] |= uint32_t(p[c + e]) << (16 * (e & 1));
+  return r;
 }
-__device__ __forceinline__ void load8(const uint16_t* p, int64_t c, int64_t dim, float (&x)[8]) {
-  if (c + 8 <= dim) {
-    const u32x4 q = ld_loose<u32x4, 2>(p + c);
+template <typename I>
+__device__ __forceinline__ Raw<float> load_raw(const float* p, I c, I dim) {
+  if (c + 8 <= dim) return {ld_loose<u32x4, 4>(p + c), ld_loose<u32x4, 4>(p + c + 4)};
+  Raw<float> r{};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) { x[2 * e] = lo_bf16(q[e]); x[2 * e + 1] = hi_bf16(q[e]); }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = c + e < dim ? widen(p[c + e]) : 0.f;
+  for (int e = 0; e < 4; ++e) {
+    if (c + e < dim) r.a[e] = __float_as_uint(p[c + e]);
+    if (c + 4 + e < dim) r.b[e] = __float_as_uint(p[c + 4 + e]);
   }
+  return r;
 }
-__device__ __forceinline__ void store8(float* p, int64_t c, int64_t dim, const float (&x)[8]) {
+__device__ __forceinline__ void unpack(const Raw<uint16_t>& r, float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) { x[2 * e] = lo_bf16(r.v[e]); x[2 * e + 1] = hi_bf16(r.v[e]); }
+}
+__device__ __forceinline__ void unpack(const Raw<float>& r, float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) { x[e] = __uint_as_float(r.a[e]); x[4 + e] = __uint_as_float(r.b[e]); }
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int64_t c, int64_t dim, float (&x)[8]) {
+  unpack(load_raw(p, c, dim), x);
+}
+
+// V at element c of a row p: with STREAM past L2, which takes a row start of V's
+// alignment, the same for the whole wave.
+template <bool STREAM, typename V, typename T, typename I>
+__device__ __forceinline__ void store_vector(T* p, I c, I dim, V x) {
+  if constexpr (STREAM) st_stream(rsrc(p, int64_t(dim) * sizeof(T)), int(c) * int(sizeof(T)), x);
+  else st_loose<V, sizeof(T)>(p + c, x);
+}
+// 8 values to column c of a row; elements at or past `dim` are left alone.
+template <bool STREAM, typename I>
+__device__ __forceinline__ void store8(float* p, I c, I dim, const float (&x)[8]) {
   if (c + 8 <= dim) {
-    st_loose<f32x4, 4>(p + c, f32x4{x[0], x[1], x[2], x[3]});
-    st_loose<f32x4, 4>(p + c + 4, f32x4{x[4], x[5], x[6], x[7]});
+    const u32x4 a = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+    const u32x4 b = {__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7])};
+    store_vector<STREAM>(p, c, dim, a);
+    store_vector<STREAM>(p, I(c + 4), dim, b);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (c + e < dim) p[c + e] = x[e];
   }
 }
-__device__ __forceinline__ void store8(uint16_t* p, int64_t c, int64_t dim, const float (&x)[8]) {
+template <bool STREAM, typename I>
+__device__ __forceinline__ void store8(uint16_t* p, I c, I dim, const float (&x)[8]) {
   if (c + 8 <= dim) {
-    st_loose<u32x4, 2>(p + c, u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                    pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])});
+    store_vector<STREAM>(p, c, dim, u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                          pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])});
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -82,13 +119,14 @@ __device__ __forceinline__ void store8(uint16_t* p, int64_t c, int64_t dim, cons
   }
 }
 // 8 values in e4m3 (nearest, ties to even; the caller clamped them).
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, int64_t c, int64_t dim, const float (&x)[8]) {
+template <bool STREAM, typename I>
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, I c, I dim, const float (&x)[8]) {
   int a = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
   a = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], a, true);
   int b = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], 0, false);
   b = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], b, true);
   if (c + 8 <= dim) {
-    st_loose<u32x2, 1>(p + c, u32x2{uint32_t(a), uint32_t(b)});
+    store_vector<STREAM>(p, c, dim, u32x2{uint32_t(a), uint32_t(b)});
   } else {
     const uint64_t q = uint32_t(a) | (uint64_t(uint32_t(b)) << 32);
 #pragma unroll
@@ -100,29 +138,32 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* p, int64_t c, int64_t dim, 
 __device__ __forceinline__ float round_to(float x, const float*) { return x; }
 __device__ __forceinline__ float round_to(float x, const uint16_t*) { return __uint_as_float(to_bf16(x) << 16); }
 
-// The sum (and the largest bit pattern) over a workgroup, the same in every lane.
-template <int WAVES>
-__device__ __forceinline__ float block_sum(float v, float* lds) {
+// The sum (and the largest bit pattern) over a row's W waves, the same in every
+// lane; `lds` holds a value for each wave of the workgroup.
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float* lds) {
   v = wave_sum(v);
-  if constexpr (WAVES == 1) return v;
+  if constexpr (W == 1) return v;
+  const int wave = threadIdx.x >> 6;
   __syncthreads();                      // lds may still be read by an earlier call
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  if ((threadIdx.x & 63) == 0) lds[wave] = v;
   __syncthreads();
-  float s = lds[0];
+  const float* mine = lds + wave / W * W;
+  float s = mine[0];
 #pragma unroll
-  for (int w = 1; w < WAVES; ++w) s += lds[w];
+  for (int w = 1; w < W; ++w) s += mine[w];
   return s;
 }
-template <int WAVES>
-__device__ __forceinline__ uint32_t block_max(uint32_t v, float* lds) {
+template <int W>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, float* lds) {
   v = wave_max(v);
-  if constexpr (WAVES == 1) return v;
+  if constexpr (W == 1) return v;
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = __uint_as_float(v);
   __syncthreads();
   uint32_t s = 0;
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) s = max(s, __float_as_uint(lds[w]));
+  for (int w = 0; w < W; ++w) s = max(s, __float_as_uint(lds[w]));
   return s;
 }
 
@@ -153,58 +194,63 @@ __device__ __forceinline__ float clamp_e4m3(float q) {
   return q > kE4m3Max ? kE4m3Max : q < -kE4m3Max ? -kE4m3Max : q;
 }
 
-// One row a workgroup, held in registers: lane t's chunk c is elements
-// (c * threads + t) * 8 onward.
-template <typename T, bool RES, bool BITS8, int WAVES, int CH>
-__global__ __launch_bounds__(64 * WAVES) void k_norm(NormArgs<T> a) {
-  __shared__ float lds[WAVES];
-  const int64_t row = blockIdx.x, dim = a.dim;
-  const T* x = a.x + row * a.x_ld;
+// One row a workgroup of W waves, held in registers: lane t's chunk k is elements
+// (64 W k + t) * 8 onward. All three arrays are loaded before the row's sum is
+// waited for. 8192 bf16 rows of 4096 with a residual and an e4m3 output take 38 us
+// (6.2 TB/s; 44 us with ordinary stores), a single row 3 us.
+template <typename T, bool RES, bool BITS8, int W, bool STREAM>
+__global__ __launch_bounds__(64 * W) void k_norm(NormArgs<T> a) {
+  constexpr int CH = kChunks<T>;
+  __shared__ float lds[W];
+  const int64_t row = blockIdx.x;
+  const int dim = int(a.dim);
+  auto col = [](int k) { return (k * 64 * W + int(threadIdx.x)) * 8; };
+  Raw<T> x[CH], r[CH], w[CH];
+#pragma unroll
+  for (int k = 0; k < CH; ++k) x[k] = load_raw(a.x + row * a.x_ld, col(k), dim);
+  if constexpr (RES) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) r[k] = load_raw(a.res + row * a.res_ld, col(k), dim);
+  }
+#pragma unroll
+  for (int k = 0; k < CH; ++k) w[k] = load_raw(a.w, col(k), dim);
   float h[CH][8];
   float sq = 0.f;
 #pragma unroll
-  for (int k = 0; k < CH; ++k) load8(x, (int64_t(k) * 64 * WAVES + threadIdx.x) * 8, dim, h[k]);
-  if constexpr (RES) {
-    const T* r = a.res + row * a.res_ld;
-    T* s = a.sum + row * a.sum_ld;
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int64_t c = (int64_t(k) * 64 * WAVES + threadIdx.x) * 8;
+  for (int k = 0; k < CH; ++k) {
+    unpack(x[k], h[k]);
+    if constexpr (RES) {
       float y[8];
-      load8(r, c, dim, y);
+      unpack(r[k], y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[k][e] = round_to(h[k][e] + y[e], s);
-      store8(s, c, dim, h[k]);
+      for (int e = 0; e < 8; ++e) h[k][e] = round_to(h[k][e] + y[e], a.sum);
+      store8<STREAM>(a.sum + row * a.sum_ld, col(k), dim, h[k]);
     }
-  }
-#pragma unroll
-  for (int k = 0; k < CH; ++k)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sq += h[k][e] * h[k][e];
-  const float rstd = rstd_of(block_sum<WAVES>(sq, lds), dim, a.eps);
+  }
+  const float rstd = rstd_of(row_sum<W>(sq, lds), dim, a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
   uint32_t top = 0;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int64_t c = (int64_t(k) * 64 * WAVES + threadIdx.x) * 8;
-    float w[8];
-    load8(a.w, c, dim, w);
+    float wk[8];
+    unpack(w[k], wk);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      h[k][e] = h[k][e] * rstd * w[e];
-      if (BITS8 && c + e < dim) top = max(top, abs_bits(h[k][e]));   // past dim: 0 * rstd may be NaN
+      h[k][e] = h[k][e] * rstd * wk[e];
+      if (BITS8 && col(k) + e < dim) top = max(top, abs_bits(h[k][e]));   // past dim: 0 * rstd may be NaN
     }
-    if constexpr (!BITS8) store8(static_cast<T*>(a.out) + row * a.out_ld, c, dim, h[k]);
+    if constexpr (!BITS8) store8<STREAM>(static_cast<T*>(a.out) + row * a.out_ld, col(k), dim, h[k]);
   }
   if constexpr (BITS8) {
-    const float scale = scale_of(block_max<WAVES>(top, lds));
+    const float scale = scale_of(row_max<W>(top, lds));
     if (threadIdx.x == 0) a.scales[row] = scale;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int64_t c = (int64_t(k) * 64 * WAVES + threadIdx.x) * 8;
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[k][e] = clamp_e4m3(h[k][e] / scale);
-      store8_e4m3(static_cast<uint8_t*>(a.out) + row * a.out_ld, c, dim, h[k]);
+      store8_e4m3<STREAM>(static_cast<uint8_t*>(a.out) + row * a.out_ld, col(k), dim, h[k]);
     }
   }
 }
@@ -232,9 +278,9 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_long(NormArgs<T> a) {
     get(c, h);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sq += h[e] * h[e];
-    if constexpr (RES) store8(a.sum + row * a.sum_ld, c, dim, h);
+    if constexpr (RES) store8<false>(a.sum + row * a.sum_ld, c, dim, h);
   }
-  const float rstd = rstd_of(block_sum<kLongWaves>(sq, lds), dim, a.eps);
+  const float rstd = rstd_of(row_sum<kLongWaves>(sq, lds), dim, a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
   float scale = 1.f;
   if constexpr (BITS8) {
@@ -247,7 +293,7 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_long(NormArgs<T> a) {
       for (int e = 0; e < 8; ++e)
         if (c + e < dim) top = max(top, abs_bits(h[e] * rstd * w[e]));
     }
-    scale = scale_of(block_max<kLongWaves>(top, lds));
+    scale = scale_of(row_max<kLongWaves>(top, lds));
     if (threadIdx.x == 0) a.scales[row] = scale;
   }
   for (int64_t c = int64_t(threadIdx.x) * 8; c < dim; c += step) {
@@ -259,8 +305,8 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_long(NormArgs<T> a) {
       h[e] = h[e] * rstd * w[e];
       if constexpr (BITS8) h[e] = clamp_e4m3(h[e] / scale);
     }
-    if constexpr (BITS8) store8_e4m3(static_cast<uint8_t*>(a.out) + row * a.out_ld, c, dim, h);
-    else store8(static_cast<T*>(a.out) + row * a.out_ld, c, dim, h);
+    if constexpr (BITS8) store8_e4m3<false>(static_cast<uint8_t*>(a.out) + row * a.out_ld, c, dim, h);
+    else store8<false>(static_cast<T*>(a.out) + row * a.out_ld, c, dim, h);
   }
 }
 
@@ -280,59 +326,108 @@ struct NormBackArgs {
   int64_t rows, dim, dy_ld, x_ld, dres_ld, dx_ld;
 };
 
-// Rows b, b + gridDim.x, ... of workgroup b; lane columns as in k_norm.
-template <typename T, bool RES, int WAVES, int CH>
-__global__ __launch_bounds__(64 * WAVES) void k_norm_back(NormBackArgs<T> a) {
-  __shared__ float lds[WAVES];
-  const int64_t dim = a.dim;
-  float w[CH][8], dw[CH][8];
+// A workgroup of 16 waves holds kRows = 16 / W rows at a time, W waves each, lane
+// columns as in k_norm. The arrays of the next rows are loaded before this row's
+// sum is joined, so that memory is busy while the waves wait for each other
+// (512 workgroups of one row at a time took 70 us where this takes 42, 6.4 TB/s,
+// at 8192 bf16 rows of 4096 with dresidual). Each lane sums its columns of dweight over its rows; the rows
+// of a workgroup are joined in LDS at the end.
+constexpr int kBackWaves = 16;
+template <typename T, bool RES, int W, bool STREAM>
+__global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a) {
+  constexpr int CH = kChunks<T>, kRows = kBackWaves / W, kThreads = 64 * W;
+  __shared__ float lds[kBackWaves];
+  __shared__ float join[kRows > 1 ? (kRows - 1) * kThreads * CH * 8 : 1];
+  const int dim = int(a.dim);
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads), t = threadIdx.x % kThreads;
+  auto col = [&](int k) { return (k * kThreads + t) * 8; };
+  Raw<T> w[CH], x[CH], y[CH], r[CH];
+  float dw[CH][8];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    load8(a.w, (int64_t(k) * 64 * WAVES + threadIdx.x) * 8, dim, w[k]);
+    w[k] = load_raw(a.w, col(k), dim);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[k][e] = 0.f;
   }
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const T* x = a.x + row * a.x_ld;
-    const T* dy = a.dy + row * a.dy_ld;
-    const float rstd = a.rstd[row];
-    float h[CH][8], g[CH][8];
+  const int64_t step = int64_t(gridDim.x) * kRows;
+  float rstd = 0.f;
+  auto load = [&](int64_t row) {
+    if (row >= a.rows) return;
+    rstd = a.rstd[row];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      x[k] = load_raw(a.x + row * a.x_ld, col(k), dim);
+      y[k] = load_raw(a.dy + row * a.dy_ld, col(k), dim);
+      if constexpr (RES) r[k] = load_raw(a.dres + row * a.dres_ld, col(k), dim);
+    }
+  };
+  int64_t row = int64_t(blockIdx.x) * kRows + group;
+  load(row);
+  // every wave of the workgroup runs the same number of rounds (they meet in row_sum)
+  for (int64_t first = int64_t(blockIdx.x) * kRows; first < a.rows; first += step, row += step) {
+    const bool live = row < a.rows;
+    Raw<T> cx[CH], cy[CH], cr[CH];
+    const float cs = rstd;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      cx[k] = x[k];
+      cy[k] = y[k];
+      if constexpr (RES) cr[k] = r[k];
+    }
+    load(row + step);
     float dot = 0.f;
+    if (live) {
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int64_t c = (int64_t(k) * 64 * WAVES + threadIdx.x) * 8;
-      load8(x, c, dim, h[k]);
-      load8(dy, c, dim, g[k]);
+      for (int k = 0; k < CH; ++k) {
+        float h[8], g[8], wk[8];
+        unpack(cx[k], h);
+        unpack(cy[k], g);
+        unpack(w[k], wk);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          h[e] = h[e] * cs;
+          dw[k][e] += g[e] * h[e];
+          dot += g[e] * wk[e] * h[e];             // zeros past dim
+        }
+      }
     }
+    const float mean = row_sum<W>(dot, lds) / float(dim);
+    if (live) {
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
+      for (int k = 0; k < CH; ++k) {
+        float h[8], g[8], wk[8];
+        unpack(cx[k], h);
+        unpack(cy[k], g);
+        unpack(w[k], wk);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[k][e] = h[k][e] * rstd;
-        dw[k][e] += g[k][e] * h[k][e];
-        g[k][e] = g[k][e] * w[k][e];
-        if ((int64_t(k) * 64 * WAVES + threadIdx.x) * 8 + e < dim) dot += g[k][e] * h[k][e];
+        for (int e = 0; e < 8; ++e) h[e] = cs * (g[e] * wk[e] - h[e] * cs * mean);
+        if constexpr (RES) {
+          unpack(cr[k], g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] += g[e];
+        }
+        store8<STREAM>(a.dx + row * a.dx_ld, col(k), dim, h);
       }
-    const float mean = block_sum<WAVES>(dot, lds) / float(dim);
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int64_t c = (int64_t(k) * 64 * WAVES + threadIdx.x) * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[k][e] = rstd * (g[k][e] - h[k][e] * mean);
-      if constexpr (RES) {
-        float y[8];
-        load8(a.dres + row * a.dres_ld, c, dim, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[k][e] += y[e];
-      }
-      store8(a.dx + row * a.dx_ld, c, dim, h[k]);
     }
   }
-  if (a.partial) {
+  if (!a.partial) return;
+  if constexpr (kRows > 1) {
+    if (group > 0) {
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
-      store8(a.partial + blockIdx.x * dim, (int64_t(k) * 64 * WAVES + threadIdx.x) * 8, dim, dw[k]);
+      for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) join[((group - 1) * CH * 8 + k * 8 + e) * kThreads + t] = dw[k][e];
+    }
+    __syncthreads();
+    if (group > 0) return;
+    for (int q = 0; q < kRows - 1; ++q)
+#pragma unroll
+      for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[k][e] += join[(q * CH * 8 + k * 8 + e) * kThreads + t];
   }
+#pragma unroll
+  for (int k = 0; k < CH; ++k) store8<false>(a.partial + int64_t(blockIdx.x) * dim, col(k), dim, dw[k]);
 }
 
 // Rows too long for registers: dx here, the weight's sums in k_norm_back_cols.
@@ -354,7 +449,7 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_back_long(NormBackArgs
       for (int e = 0; e < 8; ++e)
         if (c + e < dim) dot += g[e] * w[e] * (h[e] * rstd);
     }
-    const float mean = block_sum<kLongWaves>(dot, lds) / float(dim);
+    const float mean = row_sum<kLongWaves>(dot, lds) / float(dim);
     for (int64_t c = int64_t(threadIdx.x) * 8; c < dim; c += step) {
       float h[8], g[8], w[8];
       load8(x, c, dim, h);
@@ -368,7 +463,7 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_back_long(NormBackArgs
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] += y[e];
       }
-      store8(a.dx + row * a.dx_ld, c, dim, h);
+      store8<false>(a.dx + row * a.dx_ld, c, dim, h);
     }
   }
 }
@@ -385,7 +480,7 @@ __global__ __launch_bounds__(256) void k_norm_back_cols(NormBackArgs<T> a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[e] += g[e] * (h[e] * a.rstd[row]);
   }
-  store8(a.partial + int64_t(blockIdx.y) * a.dim, c, a.dim, dw);
+  store8<false>(a.partial + int64_t(blockIdx.y) * a.dim, c, a.dim, dw);
 }
 
 // dweight[c] = the sum over the workgroups' partial rows, in a fixed order: 16
@@ -397,8 +492,17 @@ __global__ __launch_bounds__(1024) void k_norm_dweight(const float* partial, int
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = int64_t(blockIdx.x) * 64 + lane;
   float s = 0.f;
-  if (c < dim)
-    for (int r = wave; r < parts; r += 16) s += partial[int64_t(r) * dim + c];
+  if (c < dim) {
+    int r = wave;
+    for (; r + 7 * 16 < parts; r += 8 * 16) {     // 8 loads under way
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = partial[int64_t(r + 16 * q) * dim + c];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += v[q];
+    }
+    for (; r < parts; r += 16) s += partial[int64_t(r) * dim + c];
+  }
   lds[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && c < dim) {
@@ -411,43 +515,71 @@ __global__ __launch_bounds__(1024) void k_norm_dweight(const float* partial, int
 // host side
 // ---------------------------------------------------------------------------
 
-int32_t back_blocks(int64_t rows) { return int32_t(std::min<int64_t>(rows, kMaxBlocks)); }
+// Elements of a row that W waves hold, 32 bytes a lane; longer rows than 16 waves
+// hold go through the k_*_long kernels.
+constexpr int64_t wave_dim(int elem) { return 64 * 32 / elem; }
+constexpr int64_t kLongBlocks = 512;
+int row_waves(int64_t dim, int elem) {
+  int w = 1;
+  while (w < 16 && w * wave_dim(elem) < dim) w *= 2;
+  return w;
+}
+bool row_fits(int64_t dim, int elem) { return dim <= 16 * wave_dim(elem); }
 
-// The row's shape: waves a workgroup and chunks of 8 elements a lane.
+// Workgroups (and partial rows) of a backward launch: one a CU, or fewer for
+// few rows.
+constexpr int64_t kBackBlocks = 256;
+int32_t back_blocks(int64_t rows, int64_t dim, int elem) {
+  if (!row_fits(dim, elem)) return int32_t(std::min(rows, kLongBlocks));
+  const int64_t per = kBackWaves / row_waves(dim, elem);
+  return int32_t(std::min((rows + per - 1) / per, kBackBlocks));
+}
+
 template <typename F>
-void with_shape(int64_t dim, F&& f) {
+void with_waves(int w, F&& f) {
   using std::integral_constant;
-  if (dim <= 512) f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  else if (dim <= 1024) f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-  else if (dim <= 2048) f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
-  else if (dim <= 4096) f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-  else if (dim <= 8192) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-  else if (dim <= 16384) f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  else f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  if (w == 1) f(integral_constant<int, 1>{});
+  else if (w == 2) f(integral_constant<int, 2>{});
+  else if (w == 4) f(integral_constant<int, 4>{});
+  else if (w == 8) f(integral_constant<int, 8>{});
+  else f(integral_constant<int, 16>{});
+}
+
+bool rows_aligned(const void* p, int64_t ld, int elem, int to) {
+  return reinterpret_cast<uintptr_t>(p) % to == 0 && ld * elem % to == 0;
 }
 
 template <typename T, bool RES, bool BITS8>
 void launch_norm(const NormArgs<T>& a, int64_t rows, hipStream_t stream) {
-  if (a.dim > kRegDim) {
+  if (!row_fits(a.dim, sizeof(T))) {
     k_norm_long<T, RES, BITS8><<<unsigned(rows), 64 * kLongWaves, 0, stream>>>(a);
     return;
   }
-  with_shape(a.dim, [&](auto waves, auto ch) {
-    k_norm<T, RES, BITS8, waves.value, ch.value><<<unsigned(rows), 64 * waves.value, 0, stream>>>(a);
+  const int64_t written = rows * a.dim * ((RES ? int(sizeof(T)) : 0) + (BITS8 ? 1 : int(sizeof(T))));
+  const bool past_l2 = written >= kStreamBytes && rows_aligned(a.out, a.out_ld, BITS8 ? 1 : sizeof(T), BITS8 ? 8 : 16) &&
+                      (!RES || rows_aligned(a.sum, a.sum_ld, sizeof(T), 16));
+  with_waves(row_waves(a.dim, sizeof(T)), [&](auto w) {
+    if (past_l2)
+      k_norm<T, RES, BITS8, w.value, true><<<unsigned(rows), 64 * w.value, 0, stream>>>(a);
+    else
+      k_norm<T, RES, BITS8, w.value, false><<<unsigned(rows), 64 * w.value, 0, stream>>>(a);
   });
 }
 
 template <typename T, bool RES>
 void launch_back(const NormBackArgs<T>& a, hipStream_t stream) {
-  const int32_t blocks = back_blocks(a.rows);
-  if (a.dim > kRegDim) {
+  const int32_t blocks = back_blocks(a.rows, a.dim, sizeof(T));
+  if (!row_fits(a.dim, sizeof(T))) {
     k_norm_back_long<T, RES><<<blocks, 64 * kLongWaves, 0, stream>>>(a);
     if (a.partial)
       k_norm_back_cols<T><<<dim3(unsigned((a.dim + 2047) / 2048), blocks), 256, 0, stream>>>(a);
     return;
   }
-  with_shape(a.dim, [&](auto waves, auto ch) {
-    k_norm_back<T, RES, waves.value, ch.value><<<blocks, 64 * waves.value, 0, stream>>>(a);
+  with_waves(row_waves(a.dim, sizeof(T)), [&](auto w) {
+    if (a.rows * a.dim * int64_t(sizeof(T)) >= kStreamBytes && rows_aligned(a.dx, a.dx_ld, sizeof(T), 16))
+      k_norm_back<T, RES, w.value, true><<<blocks, 64 * kBackWaves, 0, stream>>>(a);
+    else
+      k_norm_back<T, RES, w.value, false><<<blocks, 64 * kBackWaves, 0, stream>>>(a);
   });
 }
 
@@ -553,11 +685,13 @@ fsdp_status launch_back_as(const fsdp_rms_norm_backward_args& n, hipStream_t str
   }
   if (!n.dweight) return FSDP_OK;
   k_norm_dweight<T><<<unsigned((n.dim + 63) / 64), 1024, 0, stream>>>(
-      a.partial, back_blocks(n.rows), n.dim, static_cast<T*>(n.dweight));
+      a.partial, back_blocks(n.rows, n.dim, sizeof(T)), n.dim, static_cast<T*>(n.dweight));
   return fsdp::after_launch("fsdp_rms_norm_backward");
 }
 
-int64_t back_workspace(int64_t rows, int64_t dim) { return int64_t(back_blocks(rows)) * dim * 4; }
+int64_t back_workspace(int64_t rows, int64_t dim) {
+  return int64_t(std::max(back_blocks(rows, dim, 2), back_blocks(rows, dim, 4))) * dim * 4;
+}
 
 fsdp_status norm_backward(const fsdp_rms_norm_backward_args* n, hipStream_t stream) {
   if (!n) return fail(FSDP_ERR_INVALID_ARG, "arguments pointer is NULL");
