@@ -21,6 +21,11 @@ namespace {
 constexpr int kThreads = 64;      // one wave a workgroup
 constexpr int kV = 4;             // consecutive elements a lane
 constexpr int64_t kTile = int64_t(kThreads) * kV;
+constexpr int64_t kFastElems = int64_t(1) << 22;   // windows from here on stream past L2
+// Workgroups per CU of the streaming momentum kernel (8 rows of the 7B block's
+// window: 105 us without a limit, 100 with 14, 103 with 16 to 24, 117 with 10).
+// The streaming apply is best without one (44 us; 47 with 16, 56 with 12).
+constexpr int kMomentumPerCu = 14;
 
 // ---------------------------------------------------------------------------
 // gradient rows -> momentum and update
@@ -41,36 +46,59 @@ __device__ __forceinline__ void momentum(const MomentumArgs& a, float g, float& 
   u = a.nesterov ? g + a.mu * m : m;
 }
 
+// A lane's 4 elements of an array that a workgroup reads or writes at tile start
+// t0. FAST: through a descriptor over the tile, the loads of data read once and
+// the stores streamed; the addresses are aligned to the access. Otherwise at
+// element alignment.
+template <bool FAST, typename V, int CPOL, typename T>
+__device__ __forceinline__ V load4(const T* p, int64_t t0, int64_t len) {
+  const int off = int(threadIdx.x) * kV * int(sizeof(T));
+  if constexpr (!FAST) return ld_loose<V, sizeof(T)>(reinterpret_cast<const char*>(p + t0) + off);
+  else if constexpr (sizeof(V) == 8) return __builtin_amdgcn_raw_buffer_load_b64(rsrc(p + t0, len * sizeof(T)), off, 0, CPOL);
+  else return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(rsrc(p + t0, len * sizeof(T)), off, 0, CPOL));
+}
+template <bool FAST, typename V, typename T>
+__device__ __forceinline__ void store4(T* p, int64_t t0, int64_t len, V x) {
+  const int off = int(threadIdx.x) * kV * int(sizeof(T));
+  if constexpr (FAST) st_stream(rsrc(p + t0, len * sizeof(T)), off, x);
+  else st_loose<V, sizeof(T)>(reinterpret_cast<char*>(p + t0) + off, x);
+}
+constexpr int kNt = 2;     // CPol nt
+
+__device__ __forceinline__ u32x4 bits4(const float (&x)[kV]) {
+  return u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+}
+
 // The rows are folded in rank order from row 0 in fp32 and scaled, as the
-// reduce of the other step calls does. C rows' loads are in flight at a time.
-template <int C>
+// reduce of the other step calls does; 8 rows' loads are under way at a time.
+template <bool FAST>
 __global__ __launch_bounds__(kThreads) void k_muon_momentum(MomentumArgs a) {
-  const int64_t i = int64_t(blockIdx.x) * kTile + int64_t(threadIdx.x) * kV;
+  const int64_t t0 = int64_t(blockIdx.x) * kTile, i = t0 + int64_t(threadIdx.x) * kV;
+  const int64_t len = a.n - t0 < kTile ? a.n - t0 : kTile;
   if (i + kV <= a.n) {
     float acc[kV];
-    for (int k = 0; k < a.n_grads; k += C) {
-      u32x2 q[C];
+    for (int k = 0; k < a.n_grads; k += 8) {
+      u32x2 q[8];
 #pragma unroll
-      for (int j = 0; j < C; ++j)
-        if (k + j < a.n_grads) q[j] = ld_loose<u32x2, 2>(a.g[k + j] + i);
+      for (int j = 0; j < 8; ++j)
+        if (k + j < a.n_grads) q[j] = load4<FAST, u32x2, kNt>(a.g[k + j], t0, len);
 #pragma unroll
-      for (int j = 0; j < C; ++j)
+      for (int j = 0; j < 8; ++j)
         if (k + j < a.n_grads) {
           const float x[kV] = {lo_bf16(q[j].x), hi_bf16(q[j].x), lo_bf16(q[j].y), hi_bf16(q[j].y)};
 #pragma unroll
           for (int e = 0; e < kV; ++e) acc[e] = k + j ? acc[e] + x[e] : x[e];
         }
     }
-    f32x4 m = ld_loose<f32x4, 4>(a.m + i);
-    float u[kV];
+    const f32x4 old = load4<FAST, f32x4, 0>(a.m, t0, len);
+    float m[kV], u[kV];
 #pragma unroll
     for (int e = 0; e < kV; ++e) {
-      float me = m[e];
-      momentum(a, acc[e] * a.gs, me, u[e]);
-      m[e] = me;
+      m[e] = old[e];
+      momentum(a, acc[e] * a.gs, m[e], u[e]);
     }
-    st_loose<f32x4, 4>(a.m + i, m);
-    st_loose<u32x2, 2>(a.u + i, u32x2{pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3])});
+    store4<FAST>(a.m, t0, len, bits4(m));
+    store4<FAST>(a.u, t0, len, u32x2{pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3])});
   } else {
     for (int64_t j = i; j < a.n; ++j) {
       float acc = widen(a.g[0][j]);
@@ -112,6 +140,7 @@ __device__ __forceinline__ float apply(const ApplyArgs& a, float scale, float u,
 // A part's tiles start at the window position at or below its start that is a
 // multiple of 4, so the fp32 accesses keep the master's alignment whatever the
 // tensors' lengths are; lanes that straddle an end go element by element.
+template <bool FAST>
 __global__ __launch_bounds__(kThreads) void k_muon_apply(ApplyArgs a) {
   const int64_t t = blockIdx.x;
   int lo = 0, hi = a.np - 1;
@@ -122,17 +151,18 @@ __global__ __launch_bounds__(kThreads) void k_muon_apply(ApplyArgs a) {
   }
   const Part& d = a.part[lo];
   const int64_t tile0 = lo ? a.part[lo - 1].tile_end : 0;
-  const int64_t i = d.at / kV * kV + (t - tile0) * kTile + int64_t(threadIdx.x) * kV;
-  const int64_t end = d.at + d.len;
+  const int64_t t0 = d.at / kV * kV + (t - tile0) * kTile, i = t0 + int64_t(threadIdx.x) * kV;
+  const int64_t end = d.at + d.len, len = end - t0 < kTile ? end - t0 : kTile;
   const uint16_t* u = d.u - d.at;      // only dereferenced within [at, end)
   if (i >= d.at && i + kV <= end) {
     const u32x2 q = ld_loose<u32x2, 2>(u + i);
+    const f32x4 old = load4<FAST, f32x4, 0>(a.p, t0, len);
     const float x[kV] = {lo_bf16(q.x), hi_bf16(q.x), lo_bf16(q.y), hi_bf16(q.y)};
-    f32x4 p = ld_loose<f32x4, 4>(a.p + i);
+    float p[kV];
 #pragma unroll
-    for (int e = 0; e < kV; ++e) p[e] = apply(a, d.scale, x[e], p[e]);
-    st_loose<f32x4, 4>(a.p + i, p);
-    if (a.w) st_loose<u32x2, 2>(a.w + i, u32x2{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3])});
+    for (int e = 0; e < kV; ++e) p[e] = apply(a, d.scale, x[e], old[e]);
+    store4<FAST>(a.p, t0, len, bits4(p));
+    if (a.w) store4<FAST>(a.w, t0, len, u32x2{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3])});
   } else {
     const int64_t from = i < d.at ? d.at : i, to = i + kV < end ? i + kV : end;
     for (int64_t j = from; j < to; ++j) {
@@ -161,6 +191,11 @@ fsdp_status check_hparams(const fsdp_muon_hparams* hp) {
     return fail(FSDP_ERR_INVALID_ARG, "grad_scale must be finite");
   return FSDP_OK;
 }
+
+bool aligned(const void* p, int to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+// Unused dynamic LDS that leaves room for n workgroups per CU (160 KiB of LDS).
+size_t cap_lds(int n) { return size_t(163840 / n / 512 * 512); }
 
 // A launch holds fewer than 2^32 threads.
 fsdp_status check_grid(int64_t tiles, const char* what) {
@@ -202,7 +237,10 @@ fsdp_status reduce_momentum(const fsdp_unit* u, int32_t n_grads, const void* con
   a.gs = static_cast<float>(hp->grad_scale);
   a.mu = static_cast<float>(hp->momentum);
   if (fsdp_status st = fsdp::check_no_pending_error(what)) return st;
-  k_muon_momentum<8><<<unsigned(tiles), kThreads, 0, stream>>>(a);
+  bool fast = u->valid >= kFastElems && aligned(momentum, 16) && aligned(update, 8);
+  for (int32_t k = 0; k < n_grads; ++k) fast = fast && aligned(a.g[k], 8);
+  if (fast) k_muon_momentum<true><<<unsigned(tiles), kThreads, cap_lds(kMomentumPerCu), stream>>>(a);
+  else k_muon_momentum<false><<<unsigned(tiles), kThreads, 0, stream>>>(a);
   return fsdp::after_launch(what);
 }
 
@@ -252,8 +290,10 @@ fsdp_status muon_apply(const fsdp_unit* u, const void* const* tensors, const dou
   for (const ApplyArgs& a : launches)
     if (fsdp_status st = check_grid(a.tiles, what)) return st;
   if (fsdp_status st = fsdp::check_no_pending_error(what)) return st;
+  const bool fast = u->valid >= kFastElems && aligned(master, 16) && aligned(param, 8);
   for (const ApplyArgs& a : launches) {
-    k_muon_apply<<<unsigned(a.tiles), kThreads, 0, stream>>>(a);
+    if (fast) k_muon_apply<true><<<unsigned(a.tiles), kThreads, 0, stream>>>(a);
+    else k_muon_apply<false><<<unsigned(a.tiles), kThreads, 0, stream>>>(a);
     if (fsdp_status st = fsdp::after_launch(what)) return st;
   }
   return FSDP_OK;
