@@ -84,17 +84,27 @@ struct Prod {
   int32_t lda, ldb, ldc, ldct;
   int32_t kt;        // stages
   int32_t kind;
+  // A symmetric product of few tiles and a long contraction is split over the
+  // stages: `splits` workgroups a tile store their sums, register by register,
+  // in `part`, and a second launch (join) adds them in order and finishes.
+  int32_t splits;
+  int32_t join;      // 0, or the tile of the split launch
+  float* part;
   float alpha, beta, delta;
   int32_t side_i, side_j;   // padded lengths
   int32_t ti, tj;    // tiles on each axis
   int32_t out_i, out_j;
   int32_t per_xcd;   // tiles on one XCD
 };
+// CAP: products a launch can hold. Arguments of few products are 6 us a call
+// cheaper than those of 24 (19 launches; 95 against 100 us of GPU time).
+template <int CAP>
 struct ProdArgs {
-  Prod p[kMaxMats];
-  int32_t slot_end[kMaxMats];   // exclusive prefix of per_xcd; past the last: the largest int
+  Prod p[CAP];
+  int32_t slot_end[CAP];        // exclusive prefix of per_xcd; past the last: the largest int
   int32_t slots;                // workgroups on one XCD
 };
+constexpr int kFewMats = 4;
 
 // Tile t of a ti x tj grid, walked in bands of 8 tile rows.
 __device__ __forceinline__ void tile_of(int t, int ti, int tj, int& i, int& j) {
@@ -122,6 +132,13 @@ __device__ __forceinline__ void tri_of(int t, int n, int& i, int& j) {
   j = r + c;
 }
 
+// The inverse of tri_of.
+__device__ __forceinline__ int tri_index(int i, int j, int n) {
+  const int r = i & ~3, h = n - r < 4 ? n - r : 4, c = j - r;
+  if (c < 0) return r * (r + 1) / 2 + j * h + i - r;
+  return r * (r + 1) / 2 + r * h + c * h - c * (c - 1) / 2 + i - j;
+}
+
 // At most N global loads of this wave are still under way, and no LDS read.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -145,8 +162,8 @@ __device__ __forceinline__ void meet() {
 // stands between the halves: by then every wave holds the second half's
 // fragments in registers, so stage k + S may be loaded over stage k, and has
 // S - 1 stages' time to arrive.
-template <int T, int WM, int WN, int S>
-__global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
+template <int T, int WM, int WN, int S, int CAP>
+__global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> args) {
   constexpr int kWaves = WM * WN;
   constexpr int kLoads = 2 * T / 8;               // 1 KB loads a stage
   static_assert(kWaves % 2 == 0 && kLoads % kWaves == 0, "whole loads per wave");
@@ -164,18 +181,27 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   const int xcd = blockIdx.x % 8, slot = blockIdx.x / 8;
   int s = 0, before = 0;
 #pragma unroll
-  for (int q = 0; q < kMaxMats - 1; ++q) {        // slot < the last entry's end
+  for (int q = 0; q < CAP - 1; ++q) {             // slot < the last entry's end
     const int end = args.slot_end[q];
     s += slot >= end;
     before = slot >= end ? end : before;
   }
   s = __builtin_amdgcn_readfirstlane(s);
   const Prod& p = args.p[s];
-  const int local = xcd * p.per_xcd + slot - __builtin_amdgcn_readfirstlane(before);
-  int ti, tj;
-  const int kind = p.kind;
+  int local = xcd * p.per_xcd + slot - __builtin_amdgcn_readfirstlane(before);
+  int ti, tj, k0 = 0, kt = p.kt;
+  const int kind = p.kind, splits = p.splits;
+  int64_t part = 0;                               // this workgroup's place in p.part, in tiles
   if (kind == kSym || kind == kPoly) {
-    if (local >= p.ti * (p.ti + 1) / 2) return;
+    const int tiles = p.ti * (p.ti + 1) / 2;
+    if (local >= (p.join ? tiles : tiles * splits)) return;
+    part = local;
+    if (splits > 1 && !p.join) {
+      const int z = local / tiles;
+      local -= z * tiles;
+      k0 = kt * z / splits;
+      kt = kt * (z + 1) / splits - k0;
+    }
     tri_of(local, p.ti, ti, tj);
   } else {
     if (local >= p.ti * p.tj) return;
@@ -187,8 +213,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   // The first half of the waves load A's rows, the other half B's.
   const bool of_b = wave >= kWaves / 2;
   const int ld = of_b ? p.ldb : p.lda;
-  const f16* base = of_b ? p.b + int64_t(tj) * T * ld : p.a + int64_t(ti) * T * ld;
-  const __amdgpu_buffer_rsrc_t r = rsrc(base, int64_t(T) * ld * 2);
+  const f16* base = (of_b ? p.b + int64_t(tj) * T * ld : p.a + int64_t(ti) * T * ld) + k0 * kBK;
+  const __amdgpu_buffer_rsrc_t r = rsrc(base, (int64_t(T) * ld - k0 * kBK) * 2);
   const int first = (wave % (kWaves / 2)) * kPer;
   // row 8 q + lane / 8: its r / 2 % 8 is lane / 16, plus 4 for odd q
   const int v0 = (lane >> 3) * ld * 2 + ((lane & 7) ^ (lane >> 4)) * 16, v1 = v0 ^ 64;
@@ -256,35 +282,71 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs args) {
   using std::false_type;
   using std::true_type;
 
-  const int kt = p.kt;
-  if (kt >= S) {
+  if (!p.join) {
+    if (kt >= S) {
 #pragma unroll
-    for (int k = 0; k < S; ++k) load(k);
-    wait_loads<(S - 1) * kPer>();
-  } else {
-    for (int k = 0; k < kt; ++k) load(k);
-    wait_loads<0>();
-  }
-  meet();
+      for (int k = 0; k < S; ++k) load(k);
+      wait_loads<(S - 1) * kPer>();
+    } else {
+      for (int k = 0; k < kt; ++k) load(k);
+      wait_loads<0>();
+    }
+    meet();
 #pragma unroll
-  for (int n = 0; n < kReads; ++n) read_one(0, 0, n);
-  int k = 0;
-  for (; k + S < kt; ++k) {                       // stages k + 2 to k + S - 1 may be under way
-    half(k, 0, false_type{}, true_type{});
-    wait_loads<(S - 2) * kPer>();
-    meet();
-    half(k, 1, true_type{}, true_type{});
-  }
-  for (; k + 1 < kt; ++k) {
+    for (int n = 0; n < kReads; ++n) read_one(0, 0, n);
+    int k = 0;
+    for (; k + S < kt; ++k) {                       // stages k + 2 to k + S - 1 may be under way
+      half(k, 0, false_type{}, true_type{});
+      wait_loads<(S - 2) * kPer>();
+      meet();
+      half(k, 1, true_type{}, true_type{});
+    }
+    for (; k + 1 < kt; ++k) {
+      half(k, 0, false_type{}, true_type{});
+      wait_loads<0>();
+      meet();
+      half(k, 1, false_type{}, true_type{});
+    }
     half(k, 0, false_type{}, true_type{});
     wait_loads<0>();
     meet();
-    half(k, 1, false_type{}, true_type{});
+    half(k, 1, false_type{}, false_type{});
+    if constexpr (T < 256) {
+      if (splits > 1) {
+        f32x4* to = reinterpret_cast<f32x4*>(p.part + part * (T * T)) + threadIdx.x;
+#pragma unroll
+        for (int x = 0; x < MI; ++x)
+#pragma unroll
+          for (int y = 0; y < NI; ++y)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              to[((x * NI + y) * 4 + g) * 64 * kWaves] = f32x4{acc[x][y][4 * g], acc[x][y][4 * g + 1],
+                                                               acc[x][y][4 * g + 2], acc[x][y][4 * g + 3]};
+        return;
+      }
+    }
+  } else if constexpr (T == 64) {
+    // A 64 tile of the sums of a launch on 64 or 128 tiles. In the latter it is one
+    // wave's share, and this workgroup's waves are that wave's four fragments.
+    int64_t tile = part, tiles = int64_t(p.ti) * (p.ti + 1) / 2;
+    int at = threadIdx.x;
+    if (p.join == 128) {
+      const int n = p.ti / 2;
+      tile = tri_index(ti / 2, tj / 2, n);
+      tiles = int64_t(n) * (n + 1) / 2;
+      at = wave * 1024 + ((ti & 1) * 2 + (tj & 1)) * 64 + lane;
+    }
+    const int area = p.join * p.join;
+    for (int z = 0; z < splits; ++z) {
+      const f32x4* from = reinterpret_cast<const f32x4*>(p.part + (z * tiles + tile) * area) + at;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 q = from[g * 256];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[0][0][4 * g + e] += q[e];
+      }
+    }
   }
-  half(k, 0, false_type{}, true_type{});
-  wait_loads<0>();
-  meet();
-  half(k, 1, false_type{}, false_type{});
 
   // The result goes through LDS, so that global memory is written in whole
   // lines: as it lies in the registers, a lane holds 4 values of each of 64
@@ -565,10 +627,16 @@ fsdp_status check_shapes(int32_t count, const int64_t* rows, const int64_t* cols
   return FSDP_OK;
 }
 
-// Lays the buffers of every matrix that has elements out in the workspace.
+constexpr int kSplitSlots = 256;          // workgroups of a split launch, at most
+constexpr int kSplitStages = 8;           // stages of a split, at least
+
+// Lays the buffers of every matrix that has elements out in the workspace; *part
+// is where the sums of split launches go, or -1 if the call's S = X X^T have
+// enough tiles, or stages too few, to be split.
 int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int pad,
-                  std::vector<Plan>* plans) {
-  int64_t at = 0;
+                  std::vector<Plan>* plans, int64_t* part) {
+  int64_t at = 0, tiles = 0, longest = 0;
+  const int tile = std::min(pad, 128);
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
     at += round_up(bytes, 1024);
@@ -591,9 +659,14 @@ int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int p
       q.sym2 = pair_steps(q) ? take(q.mp * q.mp * 2) : 0;
       q.parts = int32_t(std::min<int64_t>(kSumBlocks, (int64_t(q.m) * q.n + kSumRow - 1) / kSumRow));
       q.partial = take(q.parts * 8);
+      const int64_t side = q.mp / tile;
+      tiles += side * (side + 1) / 2;
+      longest = std::max(longest, q.np / kBK);
     }
     if (plans) plans->push_back(q);
   }
+  const bool split = tiles > 0 && 2 * tiles <= kSplitSlots && longest >= 2 * kSplitStages;
+  *part = split ? take(int64_t(kSplitSlots) * tile * tile * 4) : -1;
   return at;
 }
 
@@ -603,47 +676,91 @@ int64_t tiles_of(const Prod& p, int t) {
   return p.kind == kSym || p.kind == kPoly ? i * (i + 1) / 2 : i * j;
 }
 
-// The tile of a launch: the one of the least estimated time. A launch takes at
-// least the chain of stages of its longest tile, and at least the work of all
-// tiles over the CUs. Units are one stage of a 256 tile (1.1 us), measured: a
-// workgroup that has its CU to itself needs 1, 0.5 or 0.37 of that a stage on a
-// tile of 256, 128 or 64, and a full CU gets through one in 1, 0.3 or 0.11; a
-// tile's start and end take about 6 stages.
-int launch_tile(const std::vector<const Prod*>& now, int pad) {
-  int best = pad;
+// How a launch is run: its tile, and whether its products' stages are split over
+// several workgroups a tile (joined by a second launch): what takes the least
+// estimated time. A launch takes at least the time of its longest tile, and at
+// least the work of all tiles over the 256 CUs, in whole rounds. Measured, in
+// units of 1.1 us: a tile of kt stages on a CU of its own takes 16 + 0.9 kt, 4 +
+// 0.5 kt or 2 + 0.2 kt (tiles of 256, 128, 64; 3 + 0.42 kt with the deeper
+// pipeline of split launches), and a CU among many busy ones gets through one in
+// 14 + 1.4 kt, 3 + 0.45 kt or 0.9 + 0.2 kt. A join takes 5.
+struct Shape {
+  int tile;
+  bool split;
+};
+int splits_of(const Prod& p, int64_t all_tiles) {
+  return int(std::max<int64_t>(1, std::min<int64_t>(kSplitSlots / all_tiles, p.kt / kSplitStages)));
+}
+Shape launch_shape(const std::vector<const Prod*>& now, int pad, bool may_split) {
+  Shape best{pad, false};
   double least = 0;
   for (int t = pad; t >= 64; t /= 2) {
-    const double alone = t == 256 ? 1.0 : t == 128 ? 0.5 : 0.37, full = t == 256 ? 1.0 : t == 128 ? 0.3 : 0.11;
-    double work = 0, longest = 0;
+    int64_t tiles = 0;
+    bool sym = true;
     for (const Prod* p : now) {
-      work += double(tiles_of(*p, t)) * (p->kt + 6) * full / 256;
-      longest = std::max(longest, double(p->kt + 6));
+      tiles += tiles_of(*p, t);
+      sym = sym && p->kind == kSym;
     }
-    const double time = std::max(longest * alone, work + longest * full / 2);
-    if (t == pad || time < least) {
-      best = t;
-      least = time;
+    for (int split = 0; split <= (may_split && sym && t < 256 && 2 * tiles <= kSplitSlots); ++split) {
+      double work = 0, longest = 0;
+      int64_t groups = 0;
+      for (const Prod* p : now) {
+        const int z = split ? splits_of(*p, tiles) : 1;
+        const double kt = double(p->kt) / z, n = double(tiles_of(*p, t)) * z;
+        work += n * (t == 256 ? 14 + 1.4 * kt : t == 128 ? 3 + 0.45 * kt : 0.9 + 0.2 * kt);
+        longest = std::max(longest, t == 256              ? 16 + 0.9 * kt
+                                    : t == 128 && split   ? 3 + 0.42 * kt
+                                    : t == 128            ? 4 + 0.5 * kt
+                                                          : 2 + 0.2 * kt);
+        groups += tiles_of(*p, t) * z;
+      }
+      const double time = std::max(longest, work / groups * double((groups + 255) / 256)) + (split ? 5 : 0);
+      if ((t == pad && !split) || time < least) {
+        best = Shape{t, split != 0};
+        least = time;
+      }
     }
   }
   return best;
 }
 
-void launch_products(const std::vector<const Prod*>& now, int pad, hipStream_t stream) {
-  const int tile = launch_tile(now, pad);
-  ProdArgs a{};
-  std::fill(a.slot_end, a.slot_end + kMaxMats, INT32_MAX);
+// One launch of a shape's: the products, or (join) the sums of a split one.
+template <int CAP>
+void launch_products(const std::vector<const Prod*>& now, Shape shape, bool join, float* part,
+                     hipStream_t stream) {
+  ProdArgs<CAP> a{};
+  std::fill(a.slot_end, a.slot_end + CAP, INT32_MAX);
+  int64_t all_tiles = 0;
+  for (const Prod* p : now) all_tiles += tiles_of(*p, shape.tile);
+  const int tile = join ? 64 : shape.tile;
   int n = 0;
   for (const Prod* p : now) {
     Prod& to = a.p[n] = *p;
     to.ti = p->side_i / tile;
     to.tj = p->side_j / tile;
-    to.per_xcd = int32_t((tiles_of(*p, tile) + 7) / 8);
+    to.splits = shape.split ? splits_of(*p, all_tiles) : 1;
+    to.join = join ? shape.tile : 0;
+    to.part = part;
+    part += tiles_of(*p, shape.tile) * to.splits * shape.tile * shape.tile;
+    to.per_xcd = int32_t(tiles_of(*p, tile) * (join ? 1 : to.splits) + 7) / 8;
     a.slots += to.per_xcd;
     a.slot_end[n++] = a.slots;
   }
-  if (tile == 256) k_ortho_product<256, 2, 4, 2><<<8 * a.slots, 512, 0, stream>>>(a);
-  else if (tile == 128) k_ortho_product<128, 2, 2, 2><<<8 * a.slots, 256, 0, stream>>>(a);
-  else k_ortho_product<64, 2, 2, 4><<<8 * a.slots, 256, 0, stream>>>(a);
+  const int blocks = 8 * a.slots;
+  if (tile == 256) k_ortho_product<256, 2, 4, 2, CAP><<<blocks, 512, 0, stream>>>(a);
+  else if (tile == 128 && shape.split) k_ortho_product<128, 2, 2, 4, CAP><<<blocks, 256, 0, stream>>>(a);
+  else if (tile == 128) k_ortho_product<128, 2, 2, 2, CAP><<<blocks, 256, 0, stream>>>(a);
+  else k_ortho_product<64, 2, 2, 4, CAP><<<blocks, 256, 0, stream>>>(a);
+}
+
+fsdp_status launch(const std::vector<const Prod*>& now, int pad, float* part, hipStream_t stream) {
+  const Shape shape = launch_shape(now, pad, part != nullptr);
+  for (int join = 0; join <= int(shape.split); ++join) {
+    if (now.size() <= kFewMats) launch_products<kFewMats>(now, shape, join != 0, part, stream);
+    else launch_products<kMaxMats>(now, shape, join != 0, part, stream);
+    if (fsdp_status st = fsdp::after_launch("fsdp_orthogonalize")) return st;
+  }
+  return FSDP_OK;
 }
 
 // The products of one matrix, in order; the n-th of every matrix go into one launch.
@@ -719,8 +836,8 @@ void list_products(const Plan& q, char* ws, int steps, const double* coeffs,
 
 template <typename T>
 fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const int64_t* mat_ld,
-                void* const* outs, const int64_t* out_ld, char* ws, int pad, int steps,
-                const double* coeffs, double eps, hipStream_t stream) {
+                void* const* outs, const int64_t* out_ld, char* ws, float* part, int pad,
+                int steps, const double* coeffs, double eps, hipStream_t stream) {
   const char* what = "fsdp_orthogonalize";
   std::vector<int> live;
   for (size_t i = 0; i < plans.size(); ++i)
@@ -770,8 +887,7 @@ fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const i
       for (const std::vector<Prod>& list : lists)
         if (n < list.size()) now.push_back(&list[n]);
       std::stable_sort(now.begin(), now.end(), [](const Prod* a, const Prod* b) { return a->kt > b->kt; });
-      launch_products(now, pad, stream);
-      if (fsdp_status st = fsdp::after_launch(what)) return st;
+      if (fsdp_status st = launch(now, pad, part, stream)) return st;
     }
   }
   return FSDP_OK;
@@ -797,7 +913,8 @@ fsdp_status orthogonalize(int32_t count, fsdp_dtype dtype, const void* const* ma
   const int64_t es = dtype == FSDP_F32 ? 4 : 2;
   const int pad = choose_pad(count, rows, cols);
   std::vector<Plan> plans;
-  const int64_t need = make_plan(count, rows, cols, pad, &plans);
+  int64_t part_at = -1;
+  const int64_t need = make_plan(count, rows, cols, pad, &plans, &part_at);
   if (need == 0) return FSDP_OK;               // only empty matrices
   if (!mats || !mat_ld || !outs || !out_ld)
     return fail(FSDP_ERR_INVALID_ARG, "a matrix array is NULL");
@@ -825,9 +942,10 @@ fsdp_status orthogonalize(int32_t count, fsdp_dtype dtype, const void* const* ma
   if (fsdp_status st = fsdp::check_alias(ranges)) return st;
   if (fsdp_status st = fsdp::check_no_pending_error(what)) return st;
   char* ws = static_cast<char*>(workspace);
+  float* part = part_at >= 0 ? reinterpret_cast<float*>(ws + part_at) : nullptr;
   if (dtype == FSDP_F32)
-    return run<float>(plans, mats, mat_ld, outs, out_ld, ws, pad, steps, coeffs, eps, stream);
-  return run<uint16_t>(plans, mats, mat_ld, outs, out_ld, ws, pad, steps, coeffs, eps, stream);
+    return run<float>(plans, mats, mat_ld, outs, out_ld, ws, part, pad, steps, coeffs, eps, stream);
+  return run<uint16_t>(plans, mats, mat_ld, outs, out_ld, ws, part, pad, steps, coeffs, eps, stream);
 }
 
 }  // namespace
@@ -839,7 +957,8 @@ fsdp_status fsdp_orthogonalize_workspace(int32_t n_mats, const int64_t* rows, co
   fsdp::clear_error();
   if (!bytes) return fail(FSDP_ERR_INVALID_ARG, "bytes pointer is NULL");
   if (fsdp_status st = check_shapes(n_mats, rows, cols)) return st;
-  *bytes = make_plan(n_mats, rows, cols, choose_pad(n_mats, rows, cols), nullptr);
+  int64_t part_at = -1;
+  *bytes = make_plan(n_mats, rows, cols, choose_pad(n_mats, rows, cols), nullptr, &part_at);
   return FSDP_OK;
 }
 
