@@ -172,7 +172,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
   static_assert(S >= 2 && (S & (S - 1)) == 0 && (S - 1) * kPer < 64, "stages");
   constexpr int MI = T / WM / 32, NI = T / WN / 32;
   constexpr int kStage = 2 * T * kBK * 2;
-  constexpr int kLds = std::max(S * kStage, T * (2 * T + 16));   // the stages, or the result
+  constexpr int kLds = std::max(S * kStage, T * (2 * T + 64));   // the stages, or the result
   __shared__ __attribute__((aligned(1024))) char lds[kLds];
 
   // Workgroup b runs on XCD b % 8. Every XCD takes an eighth of each matrix, in
@@ -349,60 +349,42 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
   }
 
   // The result goes through LDS, so that global memory is written in whole
-  // lines: as it lies in the registers, a lane holds 4 values of each of 64
-  // lines, and writing those directly took as long as a third of the main loop
-  // at 4096. acc[x][y][4 g + e] is i = 8 g + 4 (lane / 32) + e of one j = lane % 32.
-  // A row of LDS is T values and 16 bytes more, which spreads a column over all banks.
-  constexpr int kRow = 2 * T + 16, kChunks = T / 8, kThreads = 64 * kWaves;
+  // lines, first as it lies (rows j), then turned (rows i). A lane holds 4
+  // consecutive i of one j = lane % 32 at a time. LDS rows are T values and a pad
+  // that spreads the 8-byte writes of a wave over all banks.
+  constexpr int kRowJ = 2 * T + 16, kRowI = 2 * T + 64;
+  constexpr int kCols = T / 8, kStep = 64 * kWaves / kCols, kSteps = T / kStep;
   const int64_t i0 = int64_t(ti) * T, j0 = int64_t(tj) * T;
   const int il = wm * (T / WM) + (lane >> 5) * 4, jl = wn * (T / WN) + (lane & 31);
-  auto each_chunk = [&](auto f) {                 // 8 values of one row a lane
+  const int row0 = threadIdx.x / kCols, col = threadIdx.x % kCols * 8;   // 16 bytes a lane, kStep rows a step
+  auto each_four = [&](auto f) {
 #pragma unroll
-    for (int q = 0; q < T * kChunks / kThreads; ++q) {
-      const int at = q * kThreads + threadIdx.x;
-      f(at / kChunks, at % kChunks * 8);
-    }
+    for (int x = 0; x < MI; ++x)
+#pragma unroll
+      for (int y = 0; y < NI; ++y)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) f(x, y, g, il + x * 32 + g * 8, jl + y * 32);
   };
-  auto row_at = [&](int row, int col) { return lds + row * kRow + col * 2; };
+  const float alpha = p.alpha;
+  auto scaled = [&](int x, int y, int g) {
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = acc[x][y][4 * g + e] * alpha;
+    return v;
+  };
+  auto place = [&](int i, int j) { return reinterpret_cast<u32x2*>(lds + j * kRowJ + i * 2); };
 
-  if (kind == kPoly) {                            // A, in the order of its mirror image
-    each_chunk([&](int row, int col) {
-      *reinterpret_cast<f16x8*>(row_at(row, col)) =
-          *reinterpret_cast<const f16x8*>(p.a + (j0 + row) * p.lda + i0 + col);
+  if (kind == kFinal) {
+    each_four([&](int x, int y, int g, int i, int j) {
+      const f32x4 v = scaled(x, y, g);
+      *place(i, j) = u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)};
     });
     __syncthreads();
-  }
-  const float alpha = p.alpha, beta = p.beta, delta = p.delta;
-  f16x4 result[MI][NI][4];
 #pragma unroll
-  for (int x = 0; x < MI; ++x)
-#pragma unroll
-    for (int y = 0; y < NI; ++y)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int i = il + x * 32 + g * 8, j = jl + y * 32;
-        u32x2* at = reinterpret_cast<u32x2*>(row_at(j, i));
-        f32x4 v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[x][y][4 * g + e] * alpha;
-        if (kind == kFinal) {
-          *at = u32x2{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)};
-          continue;
-        }
-        if (kind == kPoly) {
-          const f16x4 d = __builtin_bit_cast(f16x4, *at);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = v[e] + beta * float(d[e]) + (i0 + i + e == j0 + j ? delta : 0.f);
-        }
-        result[x][y][g] = f16x4{f16(v.x), f16(v.y), f16(v.z), f16(v.w)};
-        *at = __builtin_bit_cast(u32x2, result[x][y][g]);
-      }
-  __syncthreads();
-  if (kind == kFinal) {
-    each_chunk([&](int row, int col) {
-      if (j0 + row >= p.out_j || i0 + col >= p.out_i) return;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(row_at(row, col));
+    for (int q = 0; q < kSteps; ++q) {
+      const int row = row0 + q * kStep;
+      if (j0 + row >= p.out_j || i0 + col >= p.out_i) continue;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * kRowJ + col * 2);
       uint16_t* o = p.out + (j0 + row) * p.out_ld + i0 + col;
       if (i0 + col + 8 <= p.out_i) {
         st_loose<u32x4, 2>(o, v);
@@ -411,38 +393,78 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
         for (int e = 0; e < 8; ++e)
           if (i0 + col + e < p.out_i) o[e] = uint16_t(v[e / 2] >> (16 * (e & 1)));
       }
-    });
+    }
     return;
   }
+
+  f16x4 result[MI][NI][4];
+  auto keep = [&](int x, int y, int g, int i, int j, f32x4 v) {
+    result[x][y][g] = f16x4{f16(v.x), f16(v.y), f16(v.z), f16(v.w)};
+    *place(i, j) = __builtin_bit_cast(u32x2, result[x][y][g]);
+  };
+  if (kind == kPoly) {                            // A's tile, in the order of its mirror image
+    const __amdgpu_buffer_rsrc_t from = rsrc(p.a + j0 * p.lda + i0, int64_t(T) * p.lda * 2);
+    u32x4 v[kSteps];
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q)
+      v[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, (row0 * p.lda + col) * 2,
+                                                                            q * kStep * p.lda * 2, 0));
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q)
+      *reinterpret_cast<u32x4*>(lds + (row0 + q * kStep) * kRowJ + col * 2) = v[q];
+    __syncthreads();
+    const float beta = p.beta, delta = p.delta;
+    const int diagonal = ti == tj ? 0 : T;        // i - j of the diagonal's elements in this tile
+    each_four([&](int x, int y, int g, int i, int j) {
+      f32x4 r = scaled(x, y, g);
+      const f16x4 d = __builtin_bit_cast(f16x4, *place(i, j));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = r[e] + beta * float(d[e]) + (i + e - j == diagonal ? delta : 0.f);
+      keep(x, y, g, i, j, r);
+    });
+  } else {
+    each_four([&](int x, int y, int g, int i, int j) { keep(x, y, g, i, j, scaled(x, y, g)); });
+  }
+  __syncthreads();
   // A tile on the diagonal is made exactly symmetric, like the mirrored ones: a
   // product of two matrices that commute only up to rounding is not, and later
   // products would amplify the difference (four times the error after 5 steps).
   const bool diagonal = kind != kUpdate && ti == tj;
-  each_chunk([&](int row, int col) {
-    f16x8 v = *reinterpret_cast<const f16x8*>(row_at(row, col));
+  const __amdgpu_buffer_rsrc_t to_j = rsrc(p.ct + j0 * p.ldct + i0, int64_t(T) * p.ldct * 2);
+#pragma unroll
+  for (int q = 0; q < kSteps; ++q) {
+    const int row = row0 + q * kStep;
+    u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * kRowJ + col * 2);
     if (diagonal && col < row) {
+      f16x8 w = __builtin_bit_cast(f16x8, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (col + e < row) v[e] = *reinterpret_cast<const f16*>(row_at(col + e, row));
+        if (col + e < row) w[e] = *reinterpret_cast<const f16*>(lds + (col + e) * kRowJ + row * 2);
+      v = __builtin_bit_cast(u32x4, w);
     }
-    *reinterpret_cast<f16x8*>(p.ct + (j0 + row) * p.ldct + i0 + col) = v;
-  });
+    __builtin_amdgcn_raw_buffer_store_b128(v, to_j, (row0 * p.ldct + col) * 2, q * kStep * p.ldct * 2, 0);
+  }
   if (diagonal) return;
   __syncthreads();
-#pragma unroll
-  for (int x = 0; x < MI; ++x)
-#pragma unroll
-    for (int y = 0; y < NI; ++y)
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<f16*>(row_at(il + x * 32 + g * 8 + e, jl + y * 32)) = result[x][y][g][e];
-  __syncthreads();
-  each_chunk([&](int row, int col) {
-    *reinterpret_cast<f16x8*>(p.c + (i0 + row) * p.ldc + j0 + col) =
-        *reinterpret_cast<const f16x8*>(row_at(row, col));
+  // Turned in registers: four lanes of consecutive j exchange their 4 x 4 values
+  // (first with the neighbour, then with the lane two further), after which lane
+  // l of the four holds row i + l of the four j and writes 8 bytes.
+  const bool odd = lane & 1, high = lane & 2;
+  const uint32_t select = odd ? 0x03020706u : 0x05040100u;
+  each_four([&](int x, int y, int g, int i, int j) {
+    const u32x2 d = __builtin_bit_cast(u32x2, result[x][y][g]);
+    const uint32_t r0 = __builtin_amdgcn_perm(__builtin_amdgcn_mov_dpp(d.x, 0xB1, 0xF, 0xF, true), d.x, select);
+    const uint32_t r1 = __builtin_amdgcn_perm(__builtin_amdgcn_mov_dpp(d.y, 0xB1, 0xF, 0xF, true), d.y, select);
+    const uint32_t other = __builtin_amdgcn_mov_dpp(high ? r0 : r1, 0x4E, 0xF, 0xF, true);
+    *reinterpret_cast<u32x2*>(lds + (i + (lane & 3)) * kRowI + (j & ~3) * 2) =
+        high ? u32x2{other, r1} : u32x2{r0, other};
   });
+  __syncthreads();
+  const __amdgpu_buffer_rsrc_t to_i = rsrc(p.c + i0 * p.ldc + j0, int64_t(T) * p.ldc * 2);
+#pragma unroll
+  for (int q = 0; q < kSteps; ++q)
+    __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(lds + (row0 + q * kStep) * kRowI + col * 2),
+                                           to_i, (row0 * p.ldc + col) * 2, q * kStep * p.ldc * 2, 0);
 }
 
 // ---------------------------------------------------------------------------
