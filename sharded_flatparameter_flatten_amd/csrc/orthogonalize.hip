@@ -57,6 +57,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr float kScaleX = 4096.f;     // stored X is X * 2^12
 constexpr float kScaleS = 1024.f;     // stored S and P are times 2^10
 constexpr int kBK = 64;               // contracted elements per stage: one 128-byte line a row
+constexpr int kPitchPad = 64;         // elements between rows: see pitch_of
 constexpr int kMaxMats = 24;          // matrices per launch (kernel arguments < 4 KB)
 constexpr int kSumBlocks = 256;       // partial sums of squares per matrix, at most
 constexpr int kSumRow = 8192;         // a contiguous matrix is summed as rows of this length
@@ -131,6 +132,11 @@ __device__ __forceinline__ void tri_of(int t, int n, int& i, int& j) {
   i = r + c + in;
   j = r + c;
 }
+
+// Row pitch of a buffer whose rows are `length` elements: one line more, so that
+// the rows a stage reads, all at the same place of their row, do not fall on the
+// same channels and sets of L2 when lengths are powers of two.
+__host__ __device__ __forceinline__ int64_t pitch_of(int64_t length) { return length + kPitchPad; }
 
 // The inverse of tri_of.
 __device__ __forceinline__ int tri_index(int i, int j, int n) {
@@ -578,7 +584,7 @@ __global__ __launch_bounds__(256) void k_ortho_start(SourceArgs args) {
     f16x8 q;
 #pragma unroll
     for (int e = 0; e < 8; ++e) q[e] = f16(x[e] * scale);
-    *reinterpret_cast<f16x8*>(as_is + int64_t(r0 + r) * pc + c0 + c) = q;
+    *reinterpret_cast<f16x8*>(as_is + int64_t(r0 + r) * pitch_of(pc) + c0 + c) = q;
     *reinterpret_cast<f16x8*>(&tile[r][c]) = q;
   }
   __syncthreads();
@@ -588,7 +594,7 @@ __global__ __launch_bounds__(256) void k_ortho_start(SourceArgs args) {
     f16x8 q;
 #pragma unroll
     for (int e = 0; e < 8; ++e) q[e] = tile[c + e][r];
-    *reinterpret_cast<f16x8*>(turned + int64_t(c0 + r) * pr + r0 + c) = q;
+    *reinterpret_cast<f16x8*>(turned + int64_t(c0 + r) * pitch_of(pr) + r0 + c) = q;
   }
 }
 
@@ -673,12 +679,12 @@ int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int p
     if (q.m > 0) {
       q.mp = round_up(q.m, pad);
       q.np = round_up(q.n, pad);
-      q.x = take(q.mp * q.np * 2);
-      q.xt0 = take(q.mp * q.np * 2);
-      q.xt1 = take(q.mp * q.np * 2);
-      q.sym0 = take(q.mp * q.mp * 2);
-      q.sym1 = take(q.mp * q.mp * 2);
-      q.sym2 = pair_steps(q) ? take(q.mp * q.mp * 2) : 0;
+      q.x = take(q.mp * pitch_of(q.np) * 2);
+      q.xt0 = take(q.np * pitch_of(q.mp) * 2);
+      q.xt1 = take(q.np * pitch_of(q.mp) * 2);
+      q.sym0 = take(q.mp * pitch_of(q.mp) * 2);
+      q.sym1 = take(q.mp * pitch_of(q.mp) * 2);
+      q.sym2 = pair_steps(q) ? take(q.mp * pitch_of(q.mp) * 2) : 0;
       q.parts = int32_t(std::min<int64_t>(kSumBlocks, (int64_t(q.m) * q.n + kSumRow - 1) / kSumRow));
       q.partial = take(q.parts * 8);
       const int64_t side = q.mp / tile;
@@ -791,23 +797,23 @@ void list_products(const Plan& q, char* ws, int steps, const double* coeffs,
   auto at = [&](int64_t offset) { return reinterpret_cast<f16*>(ws + offset); };
   f16 *x = at(q.x), *xt = at(q.xt0), *xt_next = at(q.xt1);
   f16 *s0 = at(q.sym0), *s1 = at(q.sym1), *s2 = at(q.sym2);
-  auto add = [&](Kind kind, const f16* a, const f16* b, int64_t ld, double alpha) -> Prod& {
+  auto add = [&](Kind kind, const f16* a, const f16* b, int64_t length, double alpha) -> Prod& {
     list->emplace_back();
     Prod& p = list->back();
     p = Prod{};
     p.kind = kind;
     p.a = a;
     p.b = b;
-    p.lda = p.ldb = int32_t(ld);
-    p.kt = int32_t(ld / kBK);
+    p.lda = p.ldb = int32_t(pitch_of(length));
+    p.kt = int32_t(length / kBK);
     p.alpha = float(alpha);
     p.side_i = p.side_j = int32_t(q.mp);
     return p;
   };
-  auto symmetric = [&](Kind kind, const f16* a, const f16* b, f16* to, int64_t ld, double alpha) -> Prod& {
-    Prod& p = add(kind, a, b, ld, alpha);
+  auto symmetric = [&](Kind kind, const f16* a, const f16* b, f16* to, int64_t length, double alpha) -> Prod& {
+    Prod& p = add(kind, a, b, length, alpha);
     p.c = p.ct = to;
-    p.ldc = p.ldct = int32_t(q.mp);
+    p.ldc = p.ldct = int32_t(pitch_of(q.mp));
     return p;
   };
   auto poly = [&](const f16* a, f16* to) {
@@ -840,9 +846,9 @@ void list_products(const Plan& q, char* ws, int steps, const double* coeffs,
     u.out_j = q.m;
     if (!last) {
       u.c = xt_next;
-      u.ldc = int32_t(q.mp);
+      u.ldc = int32_t(pitch_of(q.mp));
       u.ct = x;
-      u.ldct = int32_t(q.np);
+      u.ldct = int32_t(pitch_of(q.np));
       std::swap(xt, xt_next);
     } else {
       u.out = static_cast<uint16_t*>(out);
