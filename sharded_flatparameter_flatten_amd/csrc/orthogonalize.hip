@@ -403,6 +403,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
     return;
   }
 
+  // The step's offset is added to the lane's: with a scalar offset in the store the
+  // compiler lets the next instruction overwrite the registers being stored, and
+  // now and then one of them went out with its new value.
+  auto store = [&](u32x4 v, __amdgpu_buffer_rsrc_t to, int ld, int q) {
+    __builtin_amdgcn_raw_buffer_store_b128(v, to, ((row0 + q * kStep) * ld + col) * 2, 0, 0);
+  };
   f16x4 result[MI][NI][4];
   auto keep = [&](int x, int y, int g, int i, int j, f32x4 v) {
     result[x][y][g] = f16x4{f16(v.x), f16(v.y), f16(v.z), f16(v.w)};
@@ -448,7 +454,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
         if (col + e < row) w[e] = *reinterpret_cast<const f16*>(lds + (col + e) * kRowJ + row * 2);
       v = __builtin_bit_cast(u32x4, w);
     }
-    __builtin_amdgcn_raw_buffer_store_b128(v, to_j, (row0 * p.ldct + col) * 2, q * kStep * p.ldct * 2, 0);
+    store(v, to_j, p.ldct, q);
   }
   if (diagonal) return;
   __syncthreads();
@@ -469,8 +475,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
   const __amdgpu_buffer_rsrc_t to_i = rsrc(p.c + i0 * p.ldc + j0, int64_t(T) * p.ldc * 2);
 #pragma unroll
   for (int q = 0; q < kSteps; ++q)
-    __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(lds + (row0 + q * kStep) * kRowI + col * 2),
-                                           to_i, (row0 * p.ldc + col) * 2, q * kStep * p.ldc * 2, 0);
+    store(*reinterpret_cast<const u32x4*>(lds + (row0 + q * kStep) * kRowI + col * 2), to_i, p.ldc, q);
 }
 
 // ---------------------------------------------------------------------------

@@ -63,6 +63,25 @@ def test_large_square(lib):
     assert (o.double() - x).norm() / x.norm() <= M.polar_tolerance(5)
 
 
+@pytest.mark.parametrize("shapes", [[(4096, 4096)], [(2048, 8192)], [(8200, 2040), (3000, 4100)], [(1024, 8192)] * 2])
+def test_largest_tiles(lib, shapes):
+    """Launches on the largest tiles and split ones; the same bits again, and the value in 64 bits
+    on the GPU."""
+    mats = [matrix(*s, seed=i) for i, s in enumerate(shapes)]
+    outs = run(lib, mats)
+    for _ in range(2):
+        for a, b in zip(outs, run(lib, mats)):
+            assert M.same_bits(a, b)
+    for m, o in zip(mats, outs):
+        x = (m.T if m.shape[0] > m.shape[1] else m).double().contiguous()
+        x = x / (x.norm() + 1e-7)
+        for _ in range(5):
+            s = x @ x.T.contiguous()
+            x = M.COEFFS[0] * x + (M.COEFFS[1] * s + M.COEFFS[2] * (s @ s)) @ x
+        x = x.T if m.shape[0] > m.shape[1] else x
+        assert (o.double() - x).norm() / x.norm() <= M.polar_tolerance(5)
+
+
 def test_many_matrices_one_call(lib):
     """More matrices than a launch holds, wide, tall, square and empty ones mixed."""
     shapes = [(32, 64), (64, 32), (0, 9), (33, 31), (1, 50)] * 11 + [(400, 150), (150, 400)]
