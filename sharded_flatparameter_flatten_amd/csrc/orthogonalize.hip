@@ -102,7 +102,8 @@ struct Prod {
 template <int CAP>
 struct ProdArgs {
   Prod p[CAP];
-  int32_t slot_end[CAP];        // exclusive prefix of per_xcd; past the last: the largest int
+  int32_t end[CAP];             // exclusive prefix of workgroups; past the last: the largest int
+  int32_t run;                  // workgroups of one XCD's run over all products, or 0
   int32_t slots;                // workgroups on one XCD
 };
 constexpr int kFewMats = 4;
@@ -181,20 +182,22 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
   constexpr int kLds = std::max(S * kStage, T * (2 * T + 64));   // the stages, or the result
   __shared__ __attribute__((aligned(1024))) char lds[kLds];
 
-  // Workgroup b runs on XCD b % 8. Every XCD takes an eighth of each matrix, in
-  // one run of tiles, whose shared rows then stay in its L2; the matrix of the
-  // longest contraction comes first, so that no XCD ends on a long tile.
+  // Workgroup b runs on XCD b % 8, and tiles that share rows should share its L2.
+  // Where all products are equally long, an XCD takes one run of the tiles of all of
+  // them (two 1024 x 8192 matrices: 359 us, 369 otherwise). Otherwise it takes an eighth of each product, the longest first, so that
+  // no XCD gets more long tiles than the others.
   const int xcd = blockIdx.x % 8, slot = blockIdx.x / 8;
+  const int key = args.run ? xcd * args.run + slot : slot;
   int s = 0, before = 0;
 #pragma unroll
-  for (int q = 0; q < CAP - 1; ++q) {             // slot < the last entry's end
-    const int end = args.slot_end[q];
-    s += slot >= end;
-    before = slot >= end ? end : before;
+  for (int q = 0; q < CAP - 1; ++q) {             // past all products: an empty one, or the last
+    const int end = args.end[q];
+    s += key >= end;
+    before = key >= end ? end : before;
   }
   s = __builtin_amdgcn_readfirstlane(s);
   const Prod& p = args.p[s];
-  int local = xcd * p.per_xcd + slot - __builtin_amdgcn_readfirstlane(before);
+  int local = key - __builtin_amdgcn_readfirstlane(before) + (args.run ? 0 : xcd * p.per_xcd);
   int ti, tj, k0 = 0, kt = p.kt;
   const int kind = p.kind, splits = p.splits;
   int64_t part = 0;                               // this workgroup's place in p.part, in tiles
@@ -762,11 +765,14 @@ template <int CAP>
 void launch_products(const std::vector<const Prod*>& now, Shape shape, bool join, float* part,
                      hipStream_t stream) {
   ProdArgs<CAP> a{};
-  std::fill(a.slot_end, a.slot_end + CAP, INT32_MAX);
+  std::fill(a.end, a.end + CAP, INT32_MAX);
   int64_t all_tiles = 0;
   for (const Prod* p : now) all_tiles += tiles_of(*p, shape.tile);
   const int tile = join ? 64 : shape.tile;
-  int n = 0;
+  // 256 tiles keep a share of each product an XCD (the 7B block: 11.95 ms, 12.4 in runs)
+  bool even = tile < 256;
+  for (const Prod* p : now) even = even && p->kt == now[0]->kt;
+  int n = 0, groups = 0;
   for (const Prod* p : now) {
     Prod& to = a.p[n] = *p;
     to.ti = p->side_i / tile;
@@ -775,10 +781,13 @@ void launch_products(const std::vector<const Prod*>& now, Shape shape, bool join
     to.join = join ? shape.tile : 0;
     to.part = part;
     part += tiles_of(*p, shape.tile) * to.splits * shape.tile * shape.tile;
-    to.per_xcd = int32_t(tiles_of(*p, tile) * (join ? 1 : to.splits) + 7) / 8;
+    const int count = int(tiles_of(*p, tile) * (join ? 1 : to.splits));
+    groups += count;
+    to.per_xcd = (count + 7) / 8;
     a.slots += to.per_xcd;
-    a.slot_end[n++] = a.slots;
+    a.end[n++] = even ? groups : a.slots;
   }
+  if (even) a.run = a.slots = (groups + 7) / 8;
   const int blocks = 8 * a.slots;
   if (tile == 256) k_ortho_product<256, 2, 4, 2, CAP><<<blocks, 512, 0, stream>>>(a);
   else if (tile == 128 && shape.split) k_ortho_product<128, 2, 2, 4, CAP><<<blocks, 256, 0, stream>>>(a);
