@@ -540,7 +540,17 @@ __global__ __launch_bounds__(256) void k_ortho_sumsq(SourceArgs args) {
   for (int64_t r = part; r < rows; r += src.parts) {
     const T* row = g + r * ld;
     const int64_t n = flat && total - r * len < len ? total - r * len : len;
-    for (int64_t c = int64_t(threadIdx.x) * 8; c < n; c += 2048) {
+    int64_t c = int64_t(threadIdx.x) * 8;
+    for (; c + 3 * 2048 + 8 <= n; c += 4 * 2048) {          // four loads under way
+      float x[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) load8(row + c + u * 2048, x[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += double(x[u][e]) * double(x[u][e]);
+    }
+    for (; c < n; c += 2048) {
       if (c + 8 <= n) {
         float x[8];
         load8(row + c, x);
@@ -716,10 +726,10 @@ int64_t tiles_of(const Prod& p, int t) {
 // several workgroups a tile (joined by a second launch): what takes the least
 // estimated time. A launch takes at least the time of its longest tile, and at
 // least the work of all tiles over the 256 CUs, in whole rounds. Measured, in
-// units of 1.1 us: a tile of kt stages on a CU of its own takes 16 + 0.9 kt, 4 +
-// 0.5 kt or 2 + 0.2 kt (tiles of 256, 128, 64; 3 + 0.42 kt with the deeper
-// pipeline of split launches), and a CU among many busy ones gets through one in
-// 14 + 1.4 kt, 3 + 0.45 kt or 0.9 + 0.2 kt. A join takes 5.
+// units of 1.1 us: a tile of kt stages on a CU of its own takes 16 + 0.9 kt, 6 +
+// 0.5 kt or 2 + 0.2 kt (tiles of 256, 128, 64; 5 + 0.42 kt with the deeper
+// pipeline of launches of at most one 128 tile a CU), and a CU among many busy ones gets through one in
+// 14 + 1.4 kt, 3 + 0.45 kt or 0.9 + 0.18 kt. A join takes 5.
 struct Shape {
   int tile;
   bool split;
@@ -743,10 +753,10 @@ Shape launch_shape(const std::vector<const Prod*>& now, int pad, bool may_split)
       for (const Prod* p : now) {
         const int z = split ? splits_of(*p, tiles) : 1;
         const double kt = double(p->kt) / z, n = double(tiles_of(*p, t)) * z;
-        work += n * (t == 256 ? 14 + 1.4 * kt : t == 128 ? 3 + 0.45 * kt : 0.9 + 0.2 * kt);
+        work += n * (t == 256 ? 14 + 1.4 * kt : t == 128 ? 3 + 0.45 * kt : 0.9 + 0.18 * kt);
         longest = std::max(longest, t == 256              ? 16 + 0.9 * kt
-                                    : t == 128 && split   ? 3 + 0.42 * kt
-                                    : t == 128            ? 4 + 0.5 * kt
+                                    : t == 128 && tiles <= 256 ? 5 + 0.42 * kt
+                                    : t == 128            ? 6 + 0.5 * kt
                                                           : 2 + 0.2 * kt);
         groups += tiles_of(*p, t) * z;
       }
@@ -790,7 +800,7 @@ void launch_products(const std::vector<const Prod*>& now, Shape shape, bool join
   if (even) a.run = a.slots = (groups + 7) / 8;
   const int blocks = 8 * a.slots;
   if (tile == 256) k_ortho_product<256, 2, 4, 2, CAP><<<blocks, 512, 0, stream>>>(a);
-  else if (tile == 128 && shape.split) k_ortho_product<128, 2, 2, 4, CAP><<<blocks, 256, 0, stream>>>(a);
+  else if (tile == 128 && groups <= 256) k_ortho_product<128, 2, 2, 4, CAP><<<blocks, 256, 0, stream>>>(a);
   else if (tile == 128) k_ortho_product<128, 2, 2, 2, CAP><<<blocks, 256, 0, stream>>>(a);
   else k_ortho_product<64, 2, 2, 4, CAP><<<blocks, 256, 0, stream>>>(a);
 }
