@@ -791,6 +791,10 @@ void launch_products(const std::vector<const Prod*>& now, Shape shape, bool join
     to.join = join ? shape.tile : 0;
     to.part = part;
     part += tiles_of(*p, shape.tile) * to.splits * shape.tile * shape.tile;
+    if (join && to.splits == 1) {                 // too short to be split: the first launch finished it
+      to = Prod{};
+      continue;
+    }
     const int count = int(tiles_of(*p, tile) * (join ? 1 : to.splits));
     groups += count;
     to.per_xcd = (count + 7) / 8;

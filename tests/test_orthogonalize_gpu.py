@@ -82,6 +82,14 @@ def test_largest_tiles(lib, shapes):
         assert (o.double() - x).norm() / x.norm() <= M.polar_tolerance(5)
 
 
+@pytest.mark.parametrize("shapes", [[(1024, 4096), (300, 320)], [(64, 200), (256, 8192)], [(700, 90), (4000, 513), (1300, 2600)],
+                                    [(2048, 260), (260, 2048), (65, 66)], [(9000, 100), (120, 500)]])
+def test_one_product_split_and_others_not(lib, shapes):
+    """Launches whose long contractions are split over workgroups, next to short ones that are not."""
+    mats = [matrix(*s, seed=i) for i, s in enumerate(shapes)]
+    check(mats, run(lib, mats))
+
+
 def test_many_matrices_one_call(lib):
     """More matrices than a launch holds, wide, tall, square and empty ones mixed."""
     shapes = [(32, 64), (64, 32), (0, 9), (33, 31), (1, 50)] * 11 + [(400, 150), (150, 400)]
