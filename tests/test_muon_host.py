@@ -193,7 +193,7 @@ def test_norm_empty_and_null(lib):
     assert lib._lib.fsdp_rms_norm_backward(None, None) == INVALID
     assert lib._lib.fsdp_rms_norm_backward_workspace(1, 1, None) == INVALID
     assert lib.rms_norm_backward_workspace(0, 100) == 0
-    assert lib.rms_norm_backward_workspace(3, 100) >= 1200
+    assert lib.rms_norm_backward_workspace(3, 100) >= 400        # a row of fp32 sums, at least
 
 
 def test_binding_refuses(lib):
