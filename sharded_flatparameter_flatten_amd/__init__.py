@@ -1,4 +1,5 @@
-"""Python binding of libfsdpshard.so (argument marshalling only).
+"""Python binding of libfsdpshard.so (argument marshalling only), through ctypes, and for the
+calls with the shortest kernels through the extension module ``_calls`` (csrc/calls.cpp).
 
 Every step of the path runs in the HIP library; this module only turns torch
 tensors into device pointers, picks the current HIP stream, and turns status
@@ -117,7 +118,7 @@ def library_path() -> str:
 
 def _load():
     path = library_path()
-    if not os.path.exists(path):
+    if not os.path.exists(path) or not os.path.exists(os.path.join(_HERE, "_calls.so")):
         raise ImportError(
             f"{path} is not built; run `python -c 'import __graft_entry__ as g; g.build()'` "
             "(or python sharded_flatparameter_flatten_amd/build.py) first")
@@ -171,13 +172,16 @@ def _load():
 
 
 _lib = _load()
+from . import _calls  # noqa: E402  (links against the library that _load opened)
 
 
 def abi_version() -> int:
     return int(_lib.fsdp_abi_version())
 
 
-def _check(status: int):
+def _check(status: int | None):
+    if status is None:
+        raise TypeError("an argument cannot be used")
     if status != 0:
         msg = _lib.fsdp_last_error().decode() or _lib.fsdp_status_string(status).decode()
         raise FsdpError(status, msg)
@@ -190,6 +194,7 @@ def _ptr_array(ptrs):
 # The current stream's handle without a torch.cuda.Stream object around it (0.1 us
 # instead of 2 us a call, which shows in the calls whose kernels take 3 us).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_calls.set_current_stream(_raw_stream or (lambda index: torch.cuda.current_stream(index).cuda_stream))
 
 
 def _stream(stream, device=None):
@@ -244,6 +249,7 @@ class Unit:
         h = ctypes.c_void_p()
         _check(_lib.fsdp_unit_create(F, rank, len(shapes), ndim, dims, ctypes.byref(h)))
         self._h = h
+        self._address = h.value
         self.shapes = shapes
         info = _UnitInfo()
         _check(_lib.fsdp_unit_query(self._h, ctypes.byref(info)))
@@ -453,38 +459,44 @@ class MuonHparams:
     nesterov: bool = True
     weight_decay: float = 0.0
 
-    def _c(self, grad_scale: float = 0.0) -> _MuonHparams:
-        return _MuonHparams(self.lr, self.momentum, self.weight_decay, grad_scale,
-                            1 if self.nesterov else 0, 0)
-
 
 def reduce_momentum_shard(unit: Unit, grads, momentum: torch.Tensor, update: torch.Tensor,
                           hp: MuonHparams, grad_scale: float | None = None, stream=None):
     """The gradient rows reduced into this rank's momentum; ``update``: its bf16 update."""
-    ptrs = _grad_ptrs(unit, grads)
-    c = hp._c(1.0 / len(grads) if grad_scale is None else float(grad_scale))
-    m = _dev(momentum, torch.float32, "momentum", unit.shard_valid)
-    u = _dev(update, torch.bfloat16, "update", unit.shard_valid)
-    _check(_lib.fsdp_reduce_momentum_shard(unit.handle, len(ptrs), _ptr_array(ptrs), m, u,
-                                           ctypes.byref(c), _stream(stream, momentum.device)))
+    if not grads:
+        _grad_ptrs(unit, grads)
+    status = _calls.reduce_momentum_shard(
+        unit._address, unit.U, unit.shard_valid, grads, momentum, update, hp.lr, hp.momentum,
+        hp.weight_decay, hp.nesterov, 1.0 / len(grads) if grad_scale is None else grad_scale,
+        stream if stream is None else _stream(stream))
+    if status == 0:
+        return
+    if status is None:
+        _grad_ptrs(unit, grads)
+        _dev(momentum, torch.float32, "momentum", unit.shard_valid)
+        _dev(update, torch.bfloat16, "update", unit.shard_valid)
+    _check(status)
 
 
 def muon_apply_shard(unit: Unit, tensors, scales, master: torch.Tensor,
                      param_out: torch.Tensor | None, hp: MuonHparams, stream=None):
     """This rank's window of the whole update tensors, each times its scale, applied to its
     master weights (and the bf16 parameter)."""
-    if len(tensors) != unit.n_tensors or len(scales) != unit.n_tensors:
-        raise ValueError(f"need {unit.n_tensors} tensors and scales, got {len(tensors)} and "
-                         f"{len(scales)}")
-    ptrs = [_dev(t, torch.bfloat16, "tensors", n, i) for i, (t, n) in
-            enumerate(zip(tensors, unit.numels))]
-    p = _dev(master, torch.float32, "master", unit.shard_valid)
-    w = None if param_out is None else _dev(param_out, torch.bfloat16, "param_out",
-                                            unit.shard_valid)
-    c = hp._c()
-    _check(_lib.fsdp_muon_apply_shard(unit.handle, _ptr_array(ptrs),
-                                      (ctypes.c_double * len(scales))(*scales), p, w,
-                                      ctypes.byref(c), _stream(stream, master.device)))
+    status = _calls.muon_apply_shard(
+        unit._address, unit.numels, unit.shard_valid, tensors, scales, master, param_out, hp.lr,
+        hp.momentum, hp.weight_decay, hp.nesterov, stream if stream is None else _stream(stream))
+    if status == 0:
+        return
+    if status is None:
+        if len(tensors) != unit.n_tensors or len(scales) != unit.n_tensors:
+            raise ValueError(f"need {unit.n_tensors} tensors and scales, got {len(tensors)} and "
+                             f"{len(scales)}")
+        for i, (t, n) in enumerate(zip(tensors, unit.numels)):
+            _dev(t, torch.bfloat16, "tensors", n, i)
+        _dev(master, torch.float32, "master", unit.shard_valid)
+        if param_out is not None:
+            _dev(param_out, torch.bfloat16, "param_out", unit.shard_valid)
+    _check(status)
 
 
 def _dev_rows(t: torch.Tensor, dtype: torch.dtype, name: str, shape=None):
@@ -550,12 +562,11 @@ def orthogonalize(mats, outs, workspace: torch.Tensor, steps: int = 5,
 # --- RMS norm -------------------------------------------------------------------------------
 
 
-def _norm_type(x: torch.Tensor):
+def _check_norm_type(x: torch.Tensor):
     if not isinstance(x, torch.Tensor) or x.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("x must be a float32 or bfloat16 tensor")
     if x.dim() != 2:
         raise ValueError(f"x must be 2-d (rows, dim), got {tuple(x.shape)}")
-    return F32 if x.dtype == torch.float32 else BF16
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, eps: float = 1e-6,
@@ -564,23 +575,25 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, eps: floa
     """``out`` = the RMS norm of x's rows (of x + residual, which goes to ``residual_out``)
     times weight: in x's type, or in e4m3 (torch.float8_e4m3fn) with a scale a row in ``scales``.
     ``rstd`` (fp32, a value a row) is kept for the backward pass."""
-    code = _norm_type(x)
-    dtype, size = x.dtype, x.shape
-    rows, dim = size
-    if (residual is None) != (residual_out is None):
-        raise ValueError("residual and residual_out go together")
-    xp, x_ld = _dev_rows(x, dtype, "x")
-    op, o_ld = _dev_rows(out, dtype if scales is None else torch.float8_e4m3fn, "out", size)
-    rp = sp = None
-    r_ld = s_ld = 0
-    if residual is not None:
-        rp, r_ld = _dev_rows(residual, dtype, "residual", size)
-        sp, s_ld = _dev_rows(residual_out, dtype, "residual_out", size)
-    a = _NormArgs(xp, rp, _dev(weight, dtype, "weight", dim), sp, op,
-                  None if rstd is None else _dev(rstd, torch.float32, "rstd", rows),
-                  None if scales is None else _dev(scales, torch.float32, "scales", rows),
-                  rows, dim, x_ld, r_ld, s_ld, o_ld, eps, code, 0)
-    _check(_lib.fsdp_rms_norm(a, _stream(stream, x.device)))
+    status = _calls.rms_norm(x, weight, out, residual, residual_out, rstd, scales, eps,
+                             stream if stream is None else _stream(stream))
+    if status == 0:
+        return
+    if status is None:
+        _check_norm_type(x)
+        dtype, size = x.dtype, x.shape
+        if (residual is None) != (residual_out is None):
+            raise ValueError("residual and residual_out go together")
+        _dev_rows(x, dtype, "x")
+        _dev_rows(out, dtype if scales is None else torch.float8_e4m3fn, "out", size)
+        if residual is not None:
+            _dev_rows(residual, dtype, "residual", size)
+            _dev_rows(residual_out, dtype, "residual_out", size)
+        _dev(weight, dtype, "weight", size[1])
+        for t, name in ((rstd, "rstd"), (scales, "scales")):
+            if t is not None:
+                _dev(t, torch.float32, name, size[0])
+    _check(status)
 
 
 def rms_norm_backward_workspace(rows: int, dim: int) -> int:
@@ -596,18 +609,20 @@ def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                       stream=None):
     """Gradients of ``rms_norm``: dx (plus dresidual, the gradient that reaches the summed
     residual from elsewhere) and dweight (None: not computed, and no workspace needed)."""
-    code = _norm_type(x)
-    dtype, size = x.dtype, x.shape
-    rows, dim = size
-    yp, y_ld = _dev_rows(dy, dtype, "dy", size)
-    xp, x_ld = _dev_rows(x, dtype, "x")
-    dp, d_ld = _dev_rows(dx, dtype, "dx", size)
-    rp, r_ld = (None, 0) if dresidual is None else _dev_rows(dresidual, dtype, "dresidual", size)
-    wp = None if dweight is None else _dev(dweight, dtype, "dweight", dim)
-    ws, ws_bytes = None, 0
-    if dweight is not None and workspace is not None:
-        ws, ws_bytes = _dev(workspace, torch.uint8, "workspace"), workspace.numel()
-    a = _NormBackwardArgs(yp, xp, _dev(weight, dtype, "weight", dim),
-                          _dev(rstd, torch.float32, "rstd", rows), rp, dp, wp, ws, ws_bytes,
-                          rows, dim, y_ld, x_ld, r_ld, d_ld, code, 0)
-    _check(_lib.fsdp_rms_norm_backward(a, _stream(stream, x.device)))
+    status = _calls.rms_norm_backward(dy, x, weight, rstd, dx, dweight, workspace, dresidual,
+                                      stream if stream is None else _stream(stream))
+    if status == 0:
+        return
+    if status is None:
+        _check_norm_type(x)
+        dtype, size = x.dtype, x.shape
+        for t, name in ((dy, "dy"), (x, "x"), (dx, "dx"), (dresidual, "dresidual")):
+            if t is not None or name != "dresidual":
+                _dev_rows(t, dtype, name, size)
+        _dev(weight, dtype, "weight", size[1])
+        _dev(rstd, torch.float32, "rstd", size[0])
+        if dweight is not None:
+            _dev(dweight, dtype, "dweight", size[1])
+            if workspace is not None:
+                _dev(workspace, torch.uint8, "workspace")
+    _check(status)

@@ -2,7 +2,9 @@
 
 The host indexer (csrc/unit.cpp) is plain C++; the kernels and their entry
 points are HIP: csrc/kernels.hip (the shard step), csrc/muon_step.hip,
-csrc/orthogonalize.hip and csrc/rms_norm.hip, compiled side by side. Flags that fix the numerics:
+csrc/orthogonalize.hip and csrc/rms_norm.hip, compiled side by side. csrc/calls.cpp
+becomes _calls.so, the extension module that marshals the shortest calls' tensors;
+it links against the library beside it. Flags that fix the numerics:
 -ffp-contract=off (no fused multiply-add anywhere on the path), the default
 correctly rounded fp32 division and square root (never -ffast-math), and
 packed-fp32 instructions disabled for device code.
@@ -10,10 +12,12 @@ packed-fp32 instructions disabled for device code.
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +25,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfsdpshard.so"
+CALLS_NAME = "_calls.so"
 SOURCES = ["unit.cpp", "kernels.hip", "muon_step.hip", "orthogonalize.hip", "rms_norm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -57,12 +62,28 @@ def build(out_dir: str | None = None, defines=(), verbose: bool = False) -> str:
         _run([HIPCC, *lang, *COMMON, *dflags, "-c", os.path.join(CSRC, source), "-o", obj], verbose)
         return obj
 
-    with ThreadPoolExecutor(4) as pool:
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch_include = os.path.join(torch_dir, "include")
+    calls = os.path.join(obj_dir, "calls.o")
+    includes = [sysconfig.get_paths()["include"], torch_include,
+                os.path.join(torch_include, "torch", "csrc", "api", "include")]
+
+    def compile_calls():
+        _run([HIPCC, "-x", "c++", *COMMON, "-fvisibility=hidden", *[x for i in includes for x in ("-isystem", i)],
+              "-c", os.path.join(CSRC, "calls.cpp"), "-o", calls], verbose)
+
+    with ThreadPoolExecutor(5) as pool:
+        binding = pool.submit(compile_calls)
         objects = list(pool.map(compile_one, SOURCES))
+        binding.result()
     tmp = os.path.join(out_dir, LIB_NAME + ".tmp")
     _run([HIPCC, *DEVICE, "-shared", "-fPIC", "-o", tmp, *objects], verbose)
     final = os.path.join(out_dir, LIB_NAME)
     os.replace(tmp, final)
+    tmp = os.path.join(out_dir, CALLS_NAME + ".tmp")
+    _run([HIPCC, "-shared", "-fPIC", "-o", tmp, calls, "-L", out_dir, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN",
+          "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"], verbose)
+    os.replace(tmp, os.path.join(out_dir, CALLS_NAME))
     shutil.rmtree(obj_dir, ignore_errors=True)
     return final
 
