@@ -39,6 +39,7 @@
 #include <cmath>
 #include <new>
 #include <type_traits>
+#include <utility>
 
 #include "device_util.h"
 
@@ -52,6 +53,7 @@ namespace {
 typedef _Float16 f16;
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kScaleX = 4096.f;     // stored X is X * 2^12
@@ -108,23 +110,30 @@ struct ProdArgs {
 };
 constexpr int kFewMats = 4;
 
+// t / d for 0 <= t < 2^24, 0 < d and quotients below 2^20 (the estimate is then off by at most one): a few instructions, where a division takes 40 that wait for each other.
+__device__ __forceinline__ int divide(int t, int d) {
+  int q = int(float(t) * __builtin_amdgcn_rcpf(float(d)));
+  q -= q * d > t;
+  q += (q + 1) * d <= t;
+  return __builtin_amdgcn_readfirstlane(q);
+}
 // Tile t of a ti x tj grid, walked in bands of 8 tile rows.
 __device__ __forceinline__ void tile_of(int t, int ti, int tj, int& i, int& j) {
-  const int band = t / (8 * tj), r0 = band * 8, h = ti - r0 < 8 ? ti - r0 : 8, in = t - r0 * tj;
-  i = r0 + in % h;
-  j = in / h;
+  const int r0 = divide(t, 8 * tj) * 8, h = ti - r0 < 8 ? ti - r0 : 8, in = t - r0 * tj;
+  j = divide(in, h);
+  i = r0 + in - j * h;
 }
 // Tile t of the lower triangle of n rows, in bands of 4 rows walked by columns:
 // neighbours in this order share rows of both operands.
 __device__ __forceinline__ void tri_of(int t, int n, int& i, int& j) {
-  int r = int((sqrtf(8.f * float(t) + 1.f) - 1.f) * 0.5f) & ~3;
+  int r = __builtin_amdgcn_readfirstlane(int((__builtin_amdgcn_sqrtf(8.f * float(t) + 1.f) - 1.f) * 0.5f)) & ~3;
   while (r * (r + 1) / 2 > t) r -= 4;
   while (r + 4 < n && (r + 4) * (r + 5) / 2 <= t) r += 4;
   const int h = n - r < 4 ? n - r : 4;            // the band's rows
   int in = t - r * (r + 1) / 2;
   if (in < r * h) {
-    i = r + in % h;
-    j = in / h;
+    j = divide(in, h);
+    i = r + in - j * h;
     return;
   }
   in -= r * h;                                    // its own triangle
@@ -154,6 +163,16 @@ __device__ __forceinline__ void wait_loads() {
 __device__ __forceinline__ void meet() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// f(0), ..., f(N - 1) with constants, whatever the compiler's limits on unrolling.
+template <int N, typename F, int... I>
+__device__ __forceinline__ void static_for_each(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_each<N>(f, std::make_integer_sequence<int, N>{});
 }
 
 // T x T tile by WM x WN waves, on 32 x 32 x 16 matrix instructions.
@@ -196,7 +215,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
     before = key >= end ? end : before;
   }
   s = __builtin_amdgcn_readfirstlane(s);
-  const Prod& p = args.p[s];
+  // The product's arguments in one round of scalar loads: as they are needed they would
+  // be fetched in four, each waiting for the one before.
+  u32x16 words[2];
+  static_assert(sizeof(Prod) == sizeof(words), "two loads");
+  __builtin_memcpy(words, &args.p[s], sizeof(words));
+  asm volatile("" : "+s"(words[0]), "+s"(words[1]));
+  const Prod p = __builtin_bit_cast(Prod, words);
   int local = key - __builtin_amdgcn_readfirstlane(before) + (args.run ? 0 : xcd * p.per_xcd);
   int ti, tj, k0 = 0, kt = p.kt;
   const int kind = p.kind, splits = p.splits;
@@ -206,10 +231,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
     if (local >= (p.join ? tiles : tiles * splits)) return;
     part = local;
     if (splits > 1 && !p.join) {
-      const int z = local / tiles;
+      const int z = divide(local, tiles);
       local -= z * tiles;
-      k0 = kt * z / splits;
-      kt = kt * (z + 1) / splits - k0;
+      k0 = divide(kt * z, splits);
+      kt = divide(kt * (z + 1), splits) - k0;
     }
     tri_of(local, p.ti, ti, tj);
   } else {
@@ -239,6 +264,22 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
     for (int q = 0; q < kPer; ++q) load_one(k, q);
   };
 
+  constexpr int kCols = T / 8, kStep = 64 * kWaves / kCols, kSteps = T / kStep;
+  const int64_t i0 = int64_t(ti) * T, j0 = int64_t(tj) * T;
+  const int il = wm * (T / WM) + (lane >> 5) * 4, jl = wn * (T / WN) + (lane & 31);
+  const int row0 = threadIdx.x / kCols, col = threadIdx.x % kCols * 8;   // 16 bytes a lane, kStep rows a step
+  // kPoly: A's tile, in the order of its mirror image. Small tiles load it ahead of the
+  // products (0.5 us a launch); the largest have no registers left for it.
+  u32x4 whole[kSteps];
+  auto load_whole = [&] {
+    const __amdgpu_buffer_rsrc_t from = rsrc(p.a + j0 * p.lda + i0, int64_t(T) * p.lda * 2);
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q)
+      whole[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, (row0 * p.lda + col) * 2,
+                                                                                q * kStep * p.lda * 2, 0));
+  };
+  if (T < 256 && kind == kPoly) load_whole();
+
   f32x16 acc[MI][NI];
 #pragma unroll
   for (int x = 0; x < MI; ++x)
@@ -262,32 +303,30 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
   // The multiplies of half h of stage k, each followed by a share of the next
   // half's fragment reads and, in the second half, of the loads of stage k + S
   // (reads and loads in this order: both are LDS accesses to the compiler).
-  auto half = [&](int k, int h, auto load_next, auto read_next) {
-    int reads = 0, loads = 0;
-#pragma unroll
-    for (int i = 0; i < kMuls; ++i) {
-      if constexpr (read_next.value) {
-#pragma unroll
-        for (int z = 0; z < kReads; ++z)
-          if (reads < kReads && reads <= (i + 1) * kAhead) {
-            read_one(h ? k + 1 : k, 1 - h, reads++);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-          }
-      }
-      const int q = i / (MI * NI), x = i % (MI * NI) / NI, y = i % NI;
+  auto half = [&](int k, auto of, auto load_next, auto read_next) {
+    static_for<kMuls>([&](auto at) {
+      constexpr int h = of.value, i = at.value;
+      constexpr int r0 = i ? std::min(kReads, i * kAhead + 1) : 0, r1 = std::min(kReads, (i + 1) * kAhead + 1);
+      constexpr int l0 = std::min(kPer, (i * kPer * 2 + kMuls - 1) / kMuls);
+      constexpr int l1 = std::min(kPer, ((i + 1) * kPer * 2 + kMuls - 1) / kMuls);
+      if constexpr (read_next.value)
+        static_for<r1 - r0>([&](auto z) {
+          read_one(h ? k + 1 : k, 1 - h, r0 + z.value);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        });
+      constexpr int q = i / (MI * NI), x = i % (MI * NI) / NI, y = i % NI;
       acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[h][q][x], fb[h][q][y], acc[x][y], 0, 0, 0);
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if constexpr (load_next.value) {
-#pragma unroll
-        for (int z = 0; z < kPer; ++z)
-          if (loads < kPer && loads * kMuls < (i + 1) * kPer * 2) {
-            load_one(k + S, loads++);
-            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
-          }
-      }
-    }
+      if constexpr (load_next.value)
+        static_for<l1 - l0>([&](auto z) {
+          load_one(k + S, l0 + z.value);
+          __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+        });
+    });
     __builtin_amdgcn_sched_barrier(0);
   };
+  const std::integral_constant<int, 0> lower;
+  const std::integral_constant<int, 1> upper;
   using std::false_type;
   using std::true_type;
 
@@ -305,21 +344,21 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
     for (int n = 0; n < kReads; ++n) read_one(0, 0, n);
     int k = 0;
     for (; k + S < kt; ++k) {                       // stages k + 2 to k + S - 1 may be under way
-      half(k, 0, false_type{}, true_type{});
+      half(k, lower, false_type{}, true_type{});
       wait_loads<(S - 2) * kPer>();
       meet();
-      half(k, 1, true_type{}, true_type{});
+      half(k, upper, true_type{}, true_type{});
     }
     for (; k + 1 < kt; ++k) {
-      half(k, 0, false_type{}, true_type{});
+      half(k, lower, false_type{}, true_type{});
       wait_loads<0>();
       meet();
-      half(k, 1, false_type{}, true_type{});
+      half(k, upper, false_type{}, true_type{});
     }
-    half(k, 0, false_type{}, true_type{});
+    half(k, lower, false_type{}, true_type{});
     wait_loads<0>();
     meet();
-    half(k, 1, false_type{}, false_type{});
+    half(k, upper, false_type{}, false_type{});
     if constexpr (T < 256) {
       if (splits > 1) {
         f32x4* to = reinterpret_cast<f32x4*>(p.part + part * (T * T)) + threadIdx.x;
@@ -362,10 +401,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
   // consecutive i of one j = lane % 32 at a time. LDS rows are T values and a pad
   // that spreads the 8-byte writes of a wave over all banks.
   constexpr int kRowJ = 2 * T + 16, kRowI = 2 * T + 64;
-  constexpr int kCols = T / 8, kStep = 64 * kWaves / kCols, kSteps = T / kStep;
-  const int64_t i0 = int64_t(ti) * T, j0 = int64_t(tj) * T;
-  const int il = wm * (T / WM) + (lane >> 5) * 4, jl = wn * (T / WN) + (lane & 31);
-  const int row0 = threadIdx.x / kCols, col = threadIdx.x % kCols * 8;   // 16 bytes a lane, kStep rows a step
+  // where there is room the turned form has a place of its own, which saves two of three barriers
+  constexpr bool kApart = T * (kRowJ + kRowI) <= kLds;
+  char* const lds_i = lds + (kApart ? T * kRowJ : 0);
   auto each_four = [&](auto f) {
 #pragma unroll
     for (int x = 0; x < MI; ++x)
@@ -417,16 +455,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
     result[x][y][g] = f16x4{f16(v.x), f16(v.y), f16(v.z), f16(v.w)};
     *place(i, j) = __builtin_bit_cast(u32x2, result[x][y][g]);
   };
-  if (kind == kPoly) {                            // A's tile, in the order of its mirror image
-    const __amdgpu_buffer_rsrc_t from = rsrc(p.a + j0 * p.lda + i0, int64_t(T) * p.lda * 2);
-    u32x4 v[kSteps];
+  if (kind == kPoly) {
+    if (T == 256) load_whole();
 #pragma unroll
     for (int q = 0; q < kSteps; ++q)
-      v[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, (row0 * p.lda + col) * 2,
-                                                                            q * kStep * p.lda * 2, 0));
-#pragma unroll
-    for (int q = 0; q < kSteps; ++q)
-      *reinterpret_cast<u32x4*>(lds + (row0 + q * kStep) * kRowJ + col * 2) = v[q];
+      *reinterpret_cast<u32x4*>(lds + (row0 + q * kStep) * kRowJ + col * 2) = whole[q];
     __syncthreads();
     const float beta = p.beta, delta = p.delta;
     const int diagonal = ti == tj ? 0 : T;        // i - j of the diagonal's elements in this tile
@@ -440,11 +473,27 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
   } else {
     each_four([&](int x, int y, int g, int i, int j) { keep(x, y, g, i, j, scaled(x, y, g)); });
   }
-  __syncthreads();
   // A tile on the diagonal is made exactly symmetric, like the mirrored ones: a
   // product of two matrices that commute only up to rounding is not, and later
   // products would amplify the difference (four times the error after 5 steps).
   const bool diagonal = kind != kUpdate && ti == tj;
+  // Turned in registers: four lanes of consecutive j exchange their 4 x 4 values
+  // (first with the neighbour, then with the lane two further), after which lane
+  // l of the four holds row i + l of the four j and writes 8 bytes.
+  const bool odd = lane & 1, high = lane & 2;
+  const uint32_t select = odd ? 0x03020706u : 0x05040100u;
+  auto turn = [&] {
+    each_four([&](int x, int y, int g, int i, int j) {
+      const u32x2 d = __builtin_bit_cast(u32x2, result[x][y][g]);
+      const uint32_t r0 = __builtin_amdgcn_perm(__builtin_amdgcn_mov_dpp(d.x, 0xB1, 0xF, 0xF, true), d.x, select);
+      const uint32_t r1 = __builtin_amdgcn_perm(__builtin_amdgcn_mov_dpp(d.y, 0xB1, 0xF, 0xF, true), d.y, select);
+      const uint32_t other = __builtin_amdgcn_mov_dpp(high ? r0 : r1, 0x4E, 0xF, 0xF, true);
+      *reinterpret_cast<u32x2*>(lds_i + (i + (lane & 3)) * kRowI + (j & ~3) * 2) =
+          high ? u32x2{other, r1} : u32x2{r0, other};
+    });
+  };
+  if (kApart && !diagonal) turn();
+  __syncthreads();
   const __amdgpu_buffer_rsrc_t to_j = rsrc(p.ct + j0 * p.ldct + i0, int64_t(T) * p.ldct * 2);
 #pragma unroll
   for (int q = 0; q < kSteps; ++q) {
@@ -460,25 +509,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
     store(v, to_j, p.ldct, q);
   }
   if (diagonal) return;
-  __syncthreads();
-  // Turned in registers: four lanes of consecutive j exchange their 4 x 4 values
-  // (first with the neighbour, then with the lane two further), after which lane
-  // l of the four holds row i + l of the four j and writes 8 bytes.
-  const bool odd = lane & 1, high = lane & 2;
-  const uint32_t select = odd ? 0x03020706u : 0x05040100u;
-  each_four([&](int x, int y, int g, int i, int j) {
-    const u32x2 d = __builtin_bit_cast(u32x2, result[x][y][g]);
-    const uint32_t r0 = __builtin_amdgcn_perm(__builtin_amdgcn_mov_dpp(d.x, 0xB1, 0xF, 0xF, true), d.x, select);
-    const uint32_t r1 = __builtin_amdgcn_perm(__builtin_amdgcn_mov_dpp(d.y, 0xB1, 0xF, 0xF, true), d.y, select);
-    const uint32_t other = __builtin_amdgcn_mov_dpp(high ? r0 : r1, 0x4E, 0xF, 0xF, true);
-    *reinterpret_cast<u32x2*>(lds + (i + (lane & 3)) * kRowI + (j & ~3) * 2) =
-        high ? u32x2{other, r1} : u32x2{r0, other};
-  });
-  __syncthreads();
+  if (!kApart) {
+    __syncthreads();
+    turn();
+    __syncthreads();
+  }
   const __amdgpu_buffer_rsrc_t to_i = rsrc(p.c + i0 * p.ldc + j0, int64_t(T) * p.ldc * 2);
 #pragma unroll
   for (int q = 0; q < kSteps; ++q)
-    store(*reinterpret_cast<const u32x4*>(lds + (row0 + q * kStep) * kRowI + col * 2), to_i, p.ldc, q);
+    store(*reinterpret_cast<const u32x4*>(lds_i + (row0 + q * kStep) * kRowI + col * 2), to_i, p.ldc, q);
 }
 
 // ---------------------------------------------------------------------------
