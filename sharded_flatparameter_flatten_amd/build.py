@@ -34,6 +34,8 @@ ARCH = "gfx950"
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Wall", "-I", INCLUDE, "-I", CSRC]
 DEVICE = [f"--offload-arch={ARCH}", "-mcode-object-version=5",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+# The small products' first arguments arrive in registers (a launch 0.2 us shorter).
+SOURCE_FLAGS = {"orthogonalize.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=4"]}
 
 
 def _run(cmd, verbose):
@@ -58,7 +60,7 @@ def build(out_dir: str | None = None, defines=(), verbose: bool = False) -> str:
 
     def compile_one(source):
         obj = os.path.join(obj_dir, os.path.splitext(source)[0] + ".o")
-        lang = ["-x", "hip", *DEVICE] if source.endswith(".hip") else ["-x", "c++"]
+        lang = ["-x", "hip", *DEVICE, *SOURCE_FLAGS.get(source, [])] if source.endswith(".hip") else ["-x", "c++"]
         _run([HIPCC, *lang, *COMMON, *dflags, "-c", os.path.join(CSRC, source), "-o", obj], verbose)
         return obj
 

@@ -188,8 +188,12 @@ __device__ __forceinline__ void static_for(F&& f) {
 // stands between the halves: by then every wave holds the second half's
 // fragments in registers, so stage k + S may be loaded over stage k, and has
 // S - 1 stages' time to arrive.
+//
+// end0 to end2 and run are args.end and args.run of up to 4 products, as arguments of
+// their own because only such ones can be preloaded into registers.
 template <int T, int WM, int WN, int S, int CAP>
-__global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> args) {
+__global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(int32_t end0, int32_t end1, int32_t end2,
+                                                                int32_t run, ProdArgs<CAP> args) {
   constexpr int kWaves = WM * WN;
   constexpr int kLoads = 2 * T / 8;               // 1 KB loads a stage
   static_assert(kWaves % 2 == 0 && kLoads % kWaves == 0, "whole loads per wave");
@@ -206,11 +210,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
   // them (two 1024 x 8192 matrices: 359 us, 369 otherwise). Otherwise it takes an eighth of each product, the longest first, so that
   // no XCD gets more long tiles than the others.
   const int xcd = blockIdx.x % 8, slot = blockIdx.x / 8;
-  const int key = args.run ? xcd * args.run + slot : slot;
+  const int key = run ? xcd * run + slot : slot;
   int s = 0, before = 0;
 #pragma unroll
   for (int q = 0; q < CAP - 1; ++q) {             // past all products: an empty one, or the last
-    const int end = args.end[q];
+    const int end = CAP == kFewMats ? (q == 0 ? end0 : q == 1 ? end1 : end2) : args.end[q];
     s += key >= end;
     before = key >= end ? end : before;
   }
@@ -222,7 +226,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(ProdArgs<CAP> ar
   __builtin_memcpy(words, &args.p[s], sizeof(words));
   asm volatile("" : "+s"(words[0]), "+s"(words[1]));
   const Prod p = __builtin_bit_cast(Prod, words);
-  int local = key - __builtin_amdgcn_readfirstlane(before) + (args.run ? 0 : xcd * p.per_xcd);
+  int local = key - __builtin_amdgcn_readfirstlane(before) + (run ? 0 : xcd * p.per_xcd);
   int ti, tj, k0 = 0, kt = p.kt;
   const int kind = p.kind, splits = p.splits;
   int64_t part = 0;                               // this workgroup's place in p.part, in tiles
@@ -842,10 +846,10 @@ void launch_products(const std::vector<const Prod*>& now, Shape shape, bool join
   }
   if (even) a.run = a.slots = (groups + 7) / 8;
   const int blocks = 8 * a.slots;
-  if (tile == 256) k_ortho_product<256, 2, 4, 2, CAP><<<blocks, 512, 0, stream>>>(a);
-  else if (tile == 128 && groups <= 256) k_ortho_product<128, 2, 2, 4, CAP><<<blocks, 256, 0, stream>>>(a);
-  else if (tile == 128) k_ortho_product<128, 2, 2, 2, CAP><<<blocks, 256, 0, stream>>>(a);
-  else k_ortho_product<64, 2, 2, 4, CAP><<<blocks, 256, 0, stream>>>(a);
+  if (tile == 256) k_ortho_product<256, 2, 4, 2, CAP><<<blocks, 512, 0, stream>>>(a.end[0], a.end[1], a.end[2], a.run, a);
+  else if (tile == 128 && groups <= 256) k_ortho_product<128, 2, 2, 4, CAP><<<blocks, 256, 0, stream>>>(a.end[0], a.end[1], a.end[2], a.run, a);
+  else if (tile == 128) k_ortho_product<128, 2, 2, 2, CAP><<<blocks, 256, 0, stream>>>(a.end[0], a.end[1], a.end[2], a.run, a);
+  else k_ortho_product<64, 2, 2, 4, CAP><<<blocks, 256, 0, stream>>>(a.end[0], a.end[1], a.end[2], a.run, a);
 }
 
 fsdp_status launch(const std::vector<const Prod*>& now, int pad, float* part, hipStream_t stream) {
