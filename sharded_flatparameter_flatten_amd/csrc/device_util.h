@@ -67,6 +67,9 @@ __device__ __forceinline__ void st_stream(__amdgpu_buffer_rsrc_t r, int off, u32
 __device__ __forceinline__ void st_stream(__amdgpu_buffer_rsrc_t r, int off, u32x2 x) {
   __builtin_amdgcn_raw_buffer_store_b64(x, r, off, 0, kStoreStream);
 }
+__device__ __forceinline__ void st_stream(__amdgpu_buffer_rsrc_t r, int off, uint32_t x) {
+  __builtin_amdgcn_raw_buffer_store_b32(x, r, off, 0, kStoreStream);
+}
 
 template <typename T>
 __device__ __forceinline__ T wave_sum(T x) {

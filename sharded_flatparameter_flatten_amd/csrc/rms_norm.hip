@@ -38,25 +38,22 @@ __device__ __forceinline__ float load1(const uint16_t* p) { return widen(*p); }
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store1(uint16_t* p, float x) { *p = uint16_t(to_bf16(x)); }
 
-// 8 consecutive elements of a row as they lie in memory. A lane holds kChunks<T>
-// of these, 32 bytes of every array.
+// 16 bytes of a row as they lie in memory, kElems<T> consecutive elements. A lane holds
+// two of these of every array, each next to its neighbour lane's: with 32 bytes a lane in
+// one piece the streamed stores of fp32 wrote half sectors (4096 rows of 4096: 79 us, 39 so).
 template <typename T>
-constexpr int kChunks = sizeof(T) == 2 ? 2 : 1;
+constexpr int kElems = 16 / int(sizeof(T));
+constexpr int kChunks = 2;
 template <typename T>
-struct Raw;
-template <>
-struct Raw<uint16_t> {
+struct Raw {
   u32x4 v;
-};
-template <>
-struct Raw<float> {
-  u32x4 a, b;
 };
 // From element alignment; elements at or past `dim` are zeros.
 template <typename I>   // int within a row held in registers, int64_t in the long kernels
 __device__ __forceinline__ Raw<uint16_t> load_raw(const uint16_t* p, I c, I dim) {
   if (c + 8 <= dim) return {ld_loose<u32x4, 2>(p + c)};
   Raw<uint16_t> r{};
+  if (c >= dim) return r;             // most lanes of a row's last piece
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (c + e < dim) r.v[e / 2] |= uint32_t(p[c + e]) << (16 * (e & 1));
@@ -64,25 +61,24 @@ __device__ __forceinline__ Raw<uint16_t> load_raw(const uint16_t* p, I c, I dim)
 }
 template <typename I>
 __device__ __forceinline__ Raw<float> load_raw(const float* p, I c, I dim) {
-  if (c + 8 <= dim) return {ld_loose<u32x4, 4>(p + c), ld_loose<u32x4, 4>(p + c + 4)};
+  if (c + 4 <= dim) return {ld_loose<u32x4, 4>(p + c)};
   Raw<float> r{};
+  if (c >= dim) return r;             // most lanes of a row's last piece
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (c + e < dim) r.a[e] = __float_as_uint(p[c + e]);
-    if (c + 4 + e < dim) r.b[e] = __float_as_uint(p[c + 4 + e]);
-  }
+  for (int e = 0; e < 4; ++e)
+    if (c + e < dim) r.v[e] = __float_as_uint(p[c + e]);
   return r;
 }
 __device__ __forceinline__ void unpack(const Raw<uint16_t>& r, float (&x)[8]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) { x[2 * e] = lo_bf16(r.v[e]); x[2 * e + 1] = hi_bf16(r.v[e]); }
 }
-__device__ __forceinline__ void unpack(const Raw<float>& r, float (&x)[8]) {
+__device__ __forceinline__ void unpack(const Raw<float>& r, float (&x)[4]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) { x[e] = __uint_as_float(r.a[e]); x[4 + e] = __uint_as_float(r.b[e]); }
+  for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(r.v[e]);
 }
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int64_t c, int64_t dim, float (&x)[8]) {
+__device__ __forceinline__ void load_as(const T* p, int64_t c, int64_t dim, float (&x)[kElems<T>]) {
   unpack(load_raw(p, c, dim), x);
 }
 
@@ -93,45 +89,48 @@ __device__ __forceinline__ void store_vector(T* p, I c, I dim, V x) {
   if constexpr (STREAM) st_stream(rsrc(p, int64_t(dim) * sizeof(T)), int(c) * int(sizeof(T)), x);
   else st_loose<V, sizeof(T)>(p + c, x);
 }
-// 8 values to column c of a row; elements at or past `dim` are left alone.
-template <bool STREAM, typename I>
-__device__ __forceinline__ void store8(float* p, I c, I dim, const float (&x)[8]) {
-  if (c + 8 <= dim) {
-    const u32x4 a = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
-    const u32x4 b = {__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7])};
-    store_vector<STREAM>(p, c, dim, a);
-    store_vector<STREAM>(p, I(c + 4), dim, b);
-  } else {
+// N values to column c of a row; elements at or past `dim` are left alone.
+template <bool STREAM, int N, typename I>
+__device__ __forceinline__ void store_as(float* p, I c, I dim, const float (&x)[N]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < dim) p[c + e] = x[e];
+  for (int q = 0; q < N; q += 4) {
+    if (c + q + 4 <= dim) {
+      store_vector<STREAM>(p, I(c + q), dim, u32x4{__float_as_uint(x[q]), __float_as_uint(x[q + 1]),
+                                                   __float_as_uint(x[q + 2]), __float_as_uint(x[q + 3])});
+    } else if (c + q < dim) {
+#pragma unroll
+      for (int e = q; e < q + 4; ++e)
+        if (c + e < dim) p[c + e] = x[e];
+    }
   }
 }
 template <bool STREAM, typename I>
-__device__ __forceinline__ void store8(uint16_t* p, I c, I dim, const float (&x)[8]) {
+__device__ __forceinline__ void store_as(uint16_t* p, I c, I dim, const float (&x)[8]) {
   if (c + 8 <= dim) {
     store_vector<STREAM>(p, c, dim, u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
                                           pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])});
-  } else {
+  } else if (c < dim) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (c + e < dim) store1(p + c + e, x[e]);
   }
 }
-// 8 values in e4m3 (nearest, ties to even; the caller clamped them).
-template <bool STREAM, typename I>
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, I c, I dim, const float (&x)[8]) {
-  int a = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
-  a = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], a, true);
-  int b = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], 0, false);
-  b = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], b, true);
-  if (c + 8 <= dim) {
-    store_vector<STREAM>(p, c, dim, u32x2{uint32_t(a), uint32_t(b)});
-  } else {
-    const uint64_t q = uint32_t(a) | (uint64_t(uint32_t(b)) << 32);
+// N values in e4m3 (nearest, ties to even; the caller clamped them).
+template <bool STREAM, int N, typename I>
+__device__ __forceinline__ void store_e4m3(uint8_t* p, I c, I dim, const float (&x)[N]) {
+  uint32_t q[N / 4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < dim) p[c + e] = uint8_t(q >> (8 * e));
+  for (int e = 0; e < N; e += 4) {
+    const int half = __builtin_amdgcn_cvt_pk_fp8_f32(x[e], x[e + 1], 0, false);
+    q[e / 4] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(x[e + 2], x[e + 3], half, true));
+  }
+  if (c + N <= dim) {
+    if constexpr (N == 8) store_vector<STREAM>(p, c, dim, u32x2{q[0], q[1]});
+    else store_vector<STREAM>(p, c, dim, q[0]);
+  } else if (c < dim) {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (c + e < dim) p[c + e] = uint8_t(q[e / 4] >> (8 * (e & 3)));
   }
 }
 
@@ -195,16 +194,16 @@ __device__ __forceinline__ float clamp_e4m3(float q) {
 }
 
 // One row a workgroup of W waves, held in registers: lane t's chunk k is elements
-// (64 W k + t) * 8 onward. All three arrays are loaded before the row's sum is
+// (64 W k + t) * kElems<T> onward. All three arrays are loaded before the row's sum is
 // waited for. 8192 bf16 rows of 4096 with a residual and an e4m3 output take 38 us
 // (6.2 TB/s; 44 us with ordinary stores), a single row 3 us.
 template <typename T, bool RES, bool BITS8, int W, bool STREAM>
 __global__ __launch_bounds__(64 * W) void k_norm(NormArgs<T> a) {
-  constexpr int CH = kChunks<T>;
+  constexpr int CH = kChunks, E = kElems<T>;
   __shared__ float lds[W];
   const int64_t row = blockIdx.x;
   const int dim = int(a.dim);
-  auto col = [](int k) { return (k * 64 * W + int(threadIdx.x)) * 8; };
+  auto col = [](int k) { return (k * 64 * W + int(threadIdx.x)) * E; };
   Raw<T> x[CH], r[CH], w[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) x[k] = load_raw(a.x + row * a.x_ld, col(k), dim);
@@ -214,34 +213,34 @@ __global__ __launch_bounds__(64 * W) void k_norm(NormArgs<T> a) {
   }
 #pragma unroll
   for (int k = 0; k < CH; ++k) w[k] = load_raw(a.w, col(k), dim);
-  float h[CH][8];
+  float h[CH][E];
   float sq = 0.f;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     unpack(x[k], h[k]);
     if constexpr (RES) {
-      float y[8];
+      float y[E];
       unpack(r[k], y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[k][e] = round_to(h[k][e] + y[e], a.sum);
-      store8<STREAM>(a.sum + row * a.sum_ld, col(k), dim, h[k]);
+      for (int e = 0; e < E; ++e) h[k][e] = round_to(h[k][e] + y[e], a.sum);
+      store_as<STREAM>(a.sum + row * a.sum_ld, col(k), dim, h[k]);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sq += h[k][e] * h[k][e];
+    for (int e = 0; e < E; ++e) sq += h[k][e] * h[k][e];
   }
   const float rstd = rstd_of(row_sum<W>(sq, lds), dim, a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
   uint32_t top = 0;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    float wk[8];
+    float wk[E];
     unpack(w[k], wk);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < E; ++e) {
       h[k][e] = h[k][e] * rstd * wk[e];
       if (BITS8 && col(k) + e < dim) top = max(top, abs_bits(h[k][e]));   // past dim: 0 * rstd may be NaN
     }
-    if constexpr (!BITS8) store8<STREAM>(static_cast<T*>(a.out) + row * a.out_ld, col(k), dim, h[k]);
+    if constexpr (!BITS8) store_as<STREAM>(static_cast<T*>(a.out) + row * a.out_ld, col(k), dim, h[k]);
   }
   if constexpr (BITS8) {
     const float scale = scale_of(row_max<W>(top, lds));
@@ -249,8 +248,8 @@ __global__ __launch_bounds__(64 * W) void k_norm(NormArgs<T> a) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[k][e] = clamp_e4m3(h[k][e] / scale);
-      store8_e4m3<STREAM>(static_cast<uint8_t*>(a.out) + row * a.out_ld, col(k), dim, h[k]);
+      for (int e = 0; e < E; ++e) h[k][e] = clamp_e4m3(h[k][e] / scale);
+      store_e4m3<STREAM>(static_cast<uint8_t*>(a.out) + row * a.out_ld, col(k), dim, h[k]);
     }
   }
 }
@@ -259,54 +258,55 @@ __global__ __launch_bounds__(64 * W) void k_norm(NormArgs<T> a) {
 constexpr int kLongWaves = 16;
 template <typename T, bool RES, bool BITS8>
 __global__ __launch_bounds__(64 * kLongWaves) void k_norm_long(NormArgs<T> a) {
+  constexpr int E = kElems<T>;
   __shared__ float lds[kLongWaves];
-  const int64_t row = blockIdx.x, dim = a.dim, step = 64 * kLongWaves * 8;
+  const int64_t row = blockIdx.x, dim = a.dim, step = 64 * kLongWaves * E;
   const T* x = a.x + row * a.x_ld;
   const T* r = RES ? a.res + row * a.res_ld : nullptr;
-  auto get = [&](int64_t c, float (&h)[8]) {
-    load8(x, c, dim, h);
+  auto get = [&](int64_t c, float (&h)[E]) {
+    load_as(x, c, dim, h);
     if constexpr (RES) {
-      float y[8];
-      load8(r, c, dim, y);
+      float y[E];
+      load_as(r, c, dim, y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = round_to(h[e] + y[e], x);
+      for (int e = 0; e < E; ++e) h[e] = round_to(h[e] + y[e], x);
     }
   };
   float sq = 0.f;
-  for (int64_t c = int64_t(threadIdx.x) * 8; c < dim; c += step) {
-    float h[8];
+  for (int64_t c = int64_t(threadIdx.x) * E; c < dim; c += step) {
+    float h[E];
     get(c, h);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sq += h[e] * h[e];
-    if constexpr (RES) store8<false>(a.sum + row * a.sum_ld, c, dim, h);
+    for (int e = 0; e < E; ++e) sq += h[e] * h[e];
+    if constexpr (RES) store_as<false>(a.sum + row * a.sum_ld, c, dim, h);
   }
   const float rstd = rstd_of(row_sum<kLongWaves>(sq, lds), dim, a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
   float scale = 1.f;
   if constexpr (BITS8) {
     uint32_t top = 0;
-    for (int64_t c = int64_t(threadIdx.x) * 8; c < dim; c += step) {
-      float h[8], w[8];
+    for (int64_t c = int64_t(threadIdx.x) * E; c < dim; c += step) {
+      float h[E], w[E];
       get(c, h);
-      load8(a.w, c, dim, w);
+      load_as(a.w, c, dim, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < E; ++e)
         if (c + e < dim) top = max(top, abs_bits(h[e] * rstd * w[e]));
     }
     scale = scale_of(row_max<kLongWaves>(top, lds));
     if (threadIdx.x == 0) a.scales[row] = scale;
   }
-  for (int64_t c = int64_t(threadIdx.x) * 8; c < dim; c += step) {
-    float h[8], w[8];
+  for (int64_t c = int64_t(threadIdx.x) * E; c < dim; c += step) {
+    float h[E], w[E];
     get(c, h);
-    load8(a.w, c, dim, w);
+    load_as(a.w, c, dim, w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < E; ++e) {
       h[e] = h[e] * rstd * w[e];
       if constexpr (BITS8) h[e] = clamp_e4m3(h[e] / scale);
     }
-    if constexpr (BITS8) store8_e4m3<false>(static_cast<uint8_t*>(a.out) + row * a.out_ld, c, dim, h);
-    else store8<false>(static_cast<T*>(a.out) + row * a.out_ld, c, dim, h);
+    if constexpr (BITS8) store_e4m3<false>(static_cast<uint8_t*>(a.out) + row * a.out_ld, c, dim, h);
+    else store_as<false>(static_cast<T*>(a.out) + row * a.out_ld, c, dim, h);
   }
 }
 
@@ -335,19 +335,19 @@ struct NormBackArgs {
 constexpr int kBackWaves = 16;
 template <typename T, bool RES, int W, bool STREAM>
 __global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a) {
-  constexpr int CH = kChunks<T>, kRows = kBackWaves / W, kThreads = 64 * W;
+  constexpr int CH = kChunks, E = kElems<T>, kRows = kBackWaves / W, kThreads = 64 * W;
   __shared__ float lds[kBackWaves];
-  __shared__ float join[kRows > 1 ? (kRows - 1) * kThreads * CH * 8 : 1];
+  __shared__ float join[kRows > 1 ? (kRows - 1) * kThreads * CH * E : 1];
   const int dim = int(a.dim);
   const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads), t = threadIdx.x % kThreads;
-  auto col = [&](int k) { return (k * kThreads + t) * 8; };
+  auto col = [&](int k) { return (k * kThreads + t) * E; };
   Raw<T> w[CH], x[CH], y[CH], r[CH];
-  float dw[CH][8];
+  float dw[CH][E];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     w[k] = load_raw(a.w, col(k), dim);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[k][e] = 0.f;
+    for (int e = 0; e < E; ++e) dw[k][e] = 0.f;
   }
   const int64_t step = int64_t(gridDim.x) * kRows;
   float rstd = 0.f;
@@ -379,12 +379,12 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a
     if (live) {
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        float h[8], g[8], wk[8];
+        float h[E], g[E], wk[E];
         unpack(cx[k], h);
         unpack(cy[k], g);
         unpack(w[k], wk);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < E; ++e) {
           h[e] = h[e] * cs;
           dw[k][e] += g[e] * h[e];
           dot += g[e] * wk[e] * h[e];             // zeros past dim
@@ -395,18 +395,18 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a
     if (live) {
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        float h[8], g[8], wk[8];
+        float h[E], g[E], wk[E];
         unpack(cx[k], h);
         unpack(cy[k], g);
         unpack(w[k], wk);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = cs * (g[e] * wk[e] - h[e] * cs * mean);
+        for (int e = 0; e < E; ++e) h[e] = cs * (g[e] * wk[e] - h[e] * cs * mean);
         if constexpr (RES) {
           unpack(cr[k], g);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] += g[e];
+          for (int e = 0; e < E; ++e) h[e] += g[e];
         }
-        store8<STREAM>(a.dx + row * a.dx_ld, col(k), dim, h);
+        store_as<STREAM>(a.dx + row * a.dx_ld, col(k), dim, h);
       }
     }
   }
@@ -416,7 +416,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a
 #pragma unroll
       for (int k = 0; k < CH; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) join[((group - 1) * CH * 8 + k * 8 + e) * kThreads + t] = dw[k][e];
+        for (int e = 0; e < E; ++e) join[((group - 1) * CH * E + k * E + e) * kThreads + t] = dw[k][e];
     }
     __syncthreads();
     if (group > 0) return;
@@ -424,63 +424,65 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a
 #pragma unroll
       for (int k = 0; k < CH; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[k][e] += join[(q * CH * 8 + k * 8 + e) * kThreads + t];
+        for (int e = 0; e < E; ++e) dw[k][e] += join[(q * CH * E + k * E + e) * kThreads + t];
   }
 #pragma unroll
-  for (int k = 0; k < CH; ++k) store8<false>(a.partial + int64_t(blockIdx.x) * dim, col(k), dim, dw[k]);
+  for (int k = 0; k < CH; ++k) store_as<false>(a.partial + int64_t(blockIdx.x) * dim, col(k), dim, dw[k]);
 }
 
 // Rows too long for registers: dx here, the weight's sums in k_norm_back_cols.
 template <typename T, bool RES>
 __global__ __launch_bounds__(64 * kLongWaves) void k_norm_back_long(NormBackArgs<T> a) {
+  constexpr int E = kElems<T>;
   __shared__ float lds[kLongWaves];
-  const int64_t dim = a.dim, step = 64 * kLongWaves * 8;
+  const int64_t dim = a.dim, step = 64 * kLongWaves * E;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* x = a.x + row * a.x_ld;
     const T* dy = a.dy + row * a.dy_ld;
     const float rstd = a.rstd[row];
     float dot = 0.f;
-    for (int64_t c = int64_t(threadIdx.x) * 8; c < dim; c += step) {
-      float h[8], g[8], w[8];
-      load8(x, c, dim, h);
-      load8(dy, c, dim, g);
-      load8(a.w, c, dim, w);
+    for (int64_t c = int64_t(threadIdx.x) * E; c < dim; c += step) {
+      float h[E], g[E], w[E];
+      load_as(x, c, dim, h);
+      load_as(dy, c, dim, g);
+      load_as(a.w, c, dim, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < E; ++e)
         if (c + e < dim) dot += g[e] * w[e] * (h[e] * rstd);
     }
     const float mean = row_sum<kLongWaves>(dot, lds) / float(dim);
-    for (int64_t c = int64_t(threadIdx.x) * 8; c < dim; c += step) {
-      float h[8], g[8], w[8];
-      load8(x, c, dim, h);
-      load8(dy, c, dim, g);
-      load8(a.w, c, dim, w);
+    for (int64_t c = int64_t(threadIdx.x) * E; c < dim; c += step) {
+      float h[E], g[E], w[E];
+      load_as(x, c, dim, h);
+      load_as(dy, c, dim, g);
+      load_as(a.w, c, dim, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = rstd * (g[e] * w[e] - h[e] * rstd * mean);
+      for (int e = 0; e < E; ++e) h[e] = rstd * (g[e] * w[e] - h[e] * rstd * mean);
       if constexpr (RES) {
-        float y[8];
-        load8(a.dres + row * a.dres_ld, c, dim, y);
+        float y[E];
+        load_as(a.dres + row * a.dres_ld, c, dim, y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] += y[e];
+        for (int e = 0; e < E; ++e) h[e] += y[e];
       }
-      store8<false>(a.dx + row * a.dx_ld, c, dim, h);
+      store_as<false>(a.dx + row * a.dx_ld, c, dim, h);
     }
   }
 }
-// The weight's sums of rows blockIdx.y, blockIdx.y + gridDim.y, ... for 2048 columns.
+// The weight's sums of rows blockIdx.y, blockIdx.y + gridDim.y, ... for 256 lanes' columns.
 template <typename T>
 __global__ __launch_bounds__(256) void k_norm_back_cols(NormBackArgs<T> a) {
-  const int64_t c = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 8;
+  constexpr int E = kElems<T>;
+  const int64_t c = (int64_t(blockIdx.x) * 256 + threadIdx.x) * E;
   if (c >= a.dim) return;
-  float dw[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float dw[E] = {};
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    float h[8], g[8];
-    load8(a.x + row * a.x_ld, c, a.dim, h);
-    load8(a.dy + row * a.dy_ld, c, a.dim, g);
+    float h[E], g[E];
+    load_as(a.x + row * a.x_ld, c, a.dim, h);
+    load_as(a.dy + row * a.dy_ld, c, a.dim, g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[e] += g[e] * (h[e] * a.rstd[row]);
+    for (int e = 0; e < E; ++e) dw[e] += g[e] * (h[e] * a.rstd[row]);
   }
-  store8<false>(a.partial + int64_t(blockIdx.y) * a.dim, c, a.dim, dw);
+  store_as<false>(a.partial + int64_t(blockIdx.y) * a.dim, c, a.dim, dw);
 }
 
 // dweight[c] = the sum over the workgroups' partial rows, in a fixed order: 16
@@ -572,7 +574,7 @@ void launch_back(const NormBackArgs<T>& a, hipStream_t stream) {
   if (!row_fits(a.dim, sizeof(T))) {
     k_norm_back_long<T, RES><<<blocks, 64 * kLongWaves, 0, stream>>>(a);
     if (a.partial)
-      k_norm_back_cols<T><<<dim3(unsigned((a.dim + 2047) / 2048), blocks), 256, 0, stream>>>(a);
+      k_norm_back_cols<T><<<dim3(unsigned((a.dim + 256 * kElems<T> - 1) / (256 * kElems<T>)), blocks), 256, 0, stream>>>(a);
     return;
   }
   with_waves(row_waves(a.dim, sizeof(T)), [&](auto w) {
