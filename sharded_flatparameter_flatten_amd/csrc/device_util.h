@@ -59,7 +59,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t
 }
 // A streaming store (device scope, not kept in L2: sc1 nt), for outputs far
 // larger than L2: their write-back then ends within the kernel instead of
-// slowing the next. 16-byte or 8-byte aligned.
+// slowing the next. Aligned to its size.
 constexpr int kStoreStream = 18;
 __device__ __forceinline__ void st_stream(__amdgpu_buffer_rsrc_t r, int off, u32x4 x) {
   __builtin_amdgcn_raw_buffer_store_b128(x, r, off, 0, kStoreStream);
@@ -75,14 +75,6 @@ template <typename T>
 __device__ __forceinline__ T wave_sum(T x) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
-  return x;
-}
-__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const uint32_t y = __shfl_xor(x, d);
-    x = y > x ? y : x;
-  }
   return x;
 }
 

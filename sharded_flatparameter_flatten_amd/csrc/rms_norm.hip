@@ -82,20 +82,22 @@ __device__ __forceinline__ void load_as(const T* p, int64_t c, int64_t dim, floa
   unpack(load_raw(p, c, dim), x);
 }
 
-// V at element c of a row p: with STREAM past L2, which takes a row start of V's
-// alignment, the same for the whole wave.
-template <bool STREAM, typename V, typename T, typename I>
+// How a store goes: to element alignment, or, aligned to its size, past L2: through a
+// descriptor of the row, where a row has whole waves, or not kept (nt) where it has not.
+enum Way { kPlain, kStream, kOnce };
+template <Way WAY, typename V, typename T, typename I>
 __device__ __forceinline__ void store_vector(T* p, I c, I dim, V x) {
-  if constexpr (STREAM) st_stream(rsrc(p, int64_t(dim) * sizeof(T)), int(c) * int(sizeof(T)), x);
+  if constexpr (WAY == kStream) st_stream(rsrc(p, int64_t(dim) * sizeof(T)), int(c) * int(sizeof(T)), x);
+  else if constexpr (WAY == kOnce) __builtin_nontemporal_store(x, reinterpret_cast<V*>(p + c));
   else st_loose<V, sizeof(T)>(p + c, x);
 }
 // N values to column c of a row; elements at or past `dim` are left alone.
-template <bool STREAM, int N, typename I>
+template <Way WAY, int N, typename I>
 __device__ __forceinline__ void store_as(float* p, I c, I dim, const float (&x)[N]) {
 #pragma unroll
   for (int q = 0; q < N; q += 4) {
     if (c + q + 4 <= dim) {
-      store_vector<STREAM>(p, I(c + q), dim, u32x4{__float_as_uint(x[q]), __float_as_uint(x[q + 1]),
+      store_vector<WAY>(p, I(c + q), dim, u32x4{__float_as_uint(x[q]), __float_as_uint(x[q + 1]),
                                                    __float_as_uint(x[q + 2]), __float_as_uint(x[q + 3])});
     } else if (c + q < dim) {
 #pragma unroll
@@ -104,10 +106,10 @@ __device__ __forceinline__ void store_as(float* p, I c, I dim, const float (&x)[
     }
   }
 }
-template <bool STREAM, typename I>
+template <Way WAY, typename I>
 __device__ __forceinline__ void store_as(uint16_t* p, I c, I dim, const float (&x)[8]) {
   if (c + 8 <= dim) {
-    store_vector<STREAM>(p, c, dim, u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+    store_vector<WAY>(p, c, dim, u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
                                           pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])});
   } else if (c < dim) {
 #pragma unroll
@@ -116,7 +118,7 @@ __device__ __forceinline__ void store_as(uint16_t* p, I c, I dim, const float (&
   }
 }
 // N values in e4m3 (nearest, ties to even; the caller clamped them).
-template <bool STREAM, int N, typename I>
+template <Way WAY, int N, typename I>
 __device__ __forceinline__ void store_e4m3(uint8_t* p, I c, I dim, const float (&x)[N]) {
   uint32_t q[N / 4];
 #pragma unroll
@@ -125,8 +127,8 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, I c, I dim, const float (
     q[e / 4] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(x[e + 2], x[e + 3], half, true));
   }
   if (c + N <= dim) {
-    if constexpr (N == 8) store_vector<STREAM>(p, c, dim, u32x2{q[0], q[1]});
-    else store_vector<STREAM>(p, c, dim, q[0]);
+    if constexpr (N == 8) store_vector<WAY>(p, c, dim, u32x2{q[0], q[1]});
+    else store_vector<WAY>(p, c, dim, q[0]);
   } else if (c < dim) {
 #pragma unroll
     for (int e = 0; e < N; ++e)
@@ -137,12 +139,14 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, I c, I dim, const float (
 __device__ __forceinline__ float round_to(float x, const float*) { return x; }
 __device__ __forceinline__ float round_to(float x, const uint16_t*) { return __uint_as_float(to_bf16(x) << 16); }
 
-// The sum (and the largest bit pattern) over a row's W waves, the same in every
-// lane; `lds` holds a value for each wave of the workgroup.
-template <int W>
+// The sum (and the largest bit pattern) over a row's L lanes, the same in every lane;
+// `lds` holds a value for each wave of the workgroup.
+template <int L>
 __device__ __forceinline__ float row_sum(float v, float* lds) {
-  v = wave_sum(v);
-  if constexpr (W == 1) return v;
+#pragma unroll
+  for (int d = (L < 64 ? L : 64) / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  if constexpr (L <= 64) return v;
+  constexpr int W = L / 64;
   const int wave = threadIdx.x >> 6;
   __syncthreads();                      // lds may still be read by an earlier call
   if ((threadIdx.x & 63) == 0) lds[wave] = v;
@@ -153,16 +157,17 @@ __device__ __forceinline__ float row_sum(float v, float* lds) {
   for (int w = 1; w < W; ++w) s += mine[w];
   return s;
 }
-template <int W>
+template <int L>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, float* lds) {
-  v = wave_max(v);
-  if constexpr (W == 1) return v;
+#pragma unroll
+  for (int d = (L < 64 ? L : 64) / 2; d > 0; d >>= 1) v = max(v, uint32_t(__shfl_xor(v, d)));
+  if constexpr (L <= 64) return v;
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = __uint_as_float(v);
   __syncthreads();
   uint32_t s = 0;
 #pragma unroll
-  for (int w = 0; w < W; ++w) s = max(s, __float_as_uint(lds[w]));
+  for (int w = 0; w < L / 64; ++w) s = max(s, __float_as_uint(lds[w]));
   return s;
 }
 
@@ -193,17 +198,24 @@ __device__ __forceinline__ float clamp_e4m3(float q) {
   return q > kE4m3Max ? kE4m3Max : q < -kE4m3Max ? -kE4m3Max : q;
 }
 
-// One row a workgroup of W waves, held in registers: lane t's chunk k is elements
-// (64 W k + t) * kElems<T> onward. All three arrays are loaded before the row's sum is
-// waited for. 8192 bf16 rows of 4096 with a residual and an e4m3 output take 38 us
-// (6.2 TB/s; 44 us with ordinary stores), a single row 3 us.
-template <typename T, bool RES, bool BITS8, int W, bool STREAM>
-__global__ __launch_bounds__(64 * W) void k_norm(NormArgs<T> a) {
+// A row is held by L lanes in registers: lane t's piece k is elements (L k + t) * kElems<T>
+// onward. Long rows take a workgroup each; rows that a part of a wave can hold share a
+// workgroup of four waves (32768 bf16 rows of 64 with a residual: 21 us with a wave
+// a row, 6.6 so; their gradients 31 and 15).
+// All three arrays are loaded before the row's sum is waited for. 8192 bf16 rows of 4096
+// with a residual and an e4m3 output take 38 us (6.2 TB/s; 44 us with ordinary stores; a
+// workgroup that stays for many rows and loads the next ahead 48), a single row 3 us.
+template <int L>
+constexpr int kNormRows = L < 64 ? 256 / L : 1;
+template <typename T, bool RES, bool BITS8, int L, Way WAY>
+__global__ __launch_bounds__(L * kNormRows<L>) void k_norm(NormArgs<T> a, int64_t rows) {
   constexpr int CH = kChunks, E = kElems<T>;
-  __shared__ float lds[W];
-  const int64_t row = blockIdx.x;
+  __shared__ float lds[(L + 63) / 64];
+  const int t = threadIdx.x % L;
+  const int64_t row = int64_t(blockIdx.x) * kNormRows<L> + threadIdx.x / L;
+  if (L < 64 && row >= rows) return;              // a whole row's lanes; nothing waits for them
   const int dim = int(a.dim);
-  auto col = [](int k) { return (k * 64 * W + int(threadIdx.x)) * E; };
+  auto col = [&](int k) { return (k * L + t) * E; };
   Raw<T> x[CH], r[CH], w[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) x[k] = load_raw(a.x + row * a.x_ld, col(k), dim);
@@ -223,13 +235,13 @@ __global__ __launch_bounds__(64 * W) void k_norm(NormArgs<T> a) {
       unpack(r[k], y);
 #pragma unroll
       for (int e = 0; e < E; ++e) h[k][e] = round_to(h[k][e] + y[e], a.sum);
-      store_as<STREAM>(a.sum + row * a.sum_ld, col(k), dim, h[k]);
+      store_as<WAY>(a.sum + row * a.sum_ld, col(k), dim, h[k]);
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) sq += h[k][e] * h[k][e];
   }
-  const float rstd = rstd_of(row_sum<W>(sq, lds), dim, a.eps);
-  if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+  const float rstd = rstd_of(row_sum<L>(sq, lds), dim, a.eps);
+  if (a.rstd && t == 0) a.rstd[row] = rstd;
   uint32_t top = 0;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
@@ -240,16 +252,16 @@ __global__ __launch_bounds__(64 * W) void k_norm(NormArgs<T> a) {
       h[k][e] = h[k][e] * rstd * wk[e];
       if (BITS8 && col(k) + e < dim) top = max(top, abs_bits(h[k][e]));   // past dim: 0 * rstd may be NaN
     }
-    if constexpr (!BITS8) store_as<STREAM>(static_cast<T*>(a.out) + row * a.out_ld, col(k), dim, h[k]);
+    if constexpr (!BITS8) store_as<WAY>(static_cast<T*>(a.out) + row * a.out_ld, col(k), dim, h[k]);
   }
   if constexpr (BITS8) {
-    const float scale = scale_of(row_max<W>(top, lds));
-    if (threadIdx.x == 0) a.scales[row] = scale;
+    const float scale = scale_of(row_max<L>(top, lds));
+    if (t == 0) a.scales[row] = scale;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
 #pragma unroll
       for (int e = 0; e < E; ++e) h[k][e] = clamp_e4m3(h[k][e] / scale);
-      store_e4m3<STREAM>(static_cast<uint8_t*>(a.out) + row * a.out_ld, col(k), dim, h[k]);
+      store_e4m3<WAY>(static_cast<uint8_t*>(a.out) + row * a.out_ld, col(k), dim, h[k]);
     }
   }
 }
@@ -278,9 +290,9 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_long(NormArgs<T> a) {
     get(c, h);
 #pragma unroll
     for (int e = 0; e < E; ++e) sq += h[e] * h[e];
-    if constexpr (RES) store_as<false>(a.sum + row * a.sum_ld, c, dim, h);
+    if constexpr (RES) store_as<kPlain>(a.sum + row * a.sum_ld, c, dim, h);
   }
-  const float rstd = rstd_of(row_sum<kLongWaves>(sq, lds), dim, a.eps);
+  const float rstd = rstd_of(row_sum<64 * kLongWaves>(sq, lds), dim, a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
   float scale = 1.f;
   if constexpr (BITS8) {
@@ -293,7 +305,7 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_long(NormArgs<T> a) {
       for (int e = 0; e < E; ++e)
         if (c + e < dim) top = max(top, abs_bits(h[e] * rstd * w[e]));
     }
-    scale = scale_of(row_max<kLongWaves>(top, lds));
+    scale = scale_of(row_max<64 * kLongWaves>(top, lds));
     if (threadIdx.x == 0) a.scales[row] = scale;
   }
   for (int64_t c = int64_t(threadIdx.x) * E; c < dim; c += step) {
@@ -305,8 +317,8 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_long(NormArgs<T> a) {
       h[e] = h[e] * rstd * w[e];
       if constexpr (BITS8) h[e] = clamp_e4m3(h[e] / scale);
     }
-    if constexpr (BITS8) store_e4m3<false>(static_cast<uint8_t*>(a.out) + row * a.out_ld, c, dim, h);
-    else store_as<false>(static_cast<T*>(a.out) + row * a.out_ld, c, dim, h);
+    if constexpr (BITS8) store_e4m3<kPlain>(static_cast<uint8_t*>(a.out) + row * a.out_ld, c, dim, h);
+    else store_as<kPlain>(static_cast<T*>(a.out) + row * a.out_ld, c, dim, h);
   }
 }
 
@@ -326,21 +338,25 @@ struct NormBackArgs {
   int64_t rows, dim, dy_ld, x_ld, dres_ld, dx_ld;
 };
 
-// A workgroup of 16 waves holds kRows = 16 / W rows at a time, W waves each, lane
+// A workgroup of 16 waves holds kRows = 1024 / L rows at a time, L lanes each, lane
 // columns as in k_norm. The arrays of the next rows are loaded before this row's
 // sum is joined, so that memory is busy while the waves wait for each other
 // (512 workgroups of one row at a time took 70 us where this takes 42, 6.4 TB/s,
 // at 8192 bf16 rows of 4096 with dresidual). Each lane sums its columns of dweight over its rows; the rows
 // of a workgroup are joined in LDS at the end.
 constexpr int kBackWaves = 16;
-template <typename T, bool RES, int W, bool STREAM>
+template <typename T, bool RES, int L, Way WAY>
 __global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a) {
-  constexpr int CH = kChunks, E = kElems<T>, kRows = kBackWaves / W, kThreads = 64 * W;
+  constexpr int CH = kChunks, E = kElems<T>, kRows = 64 * kBackWaves / L;
+  // rows of dweight sums to be joined, after those within a wave
+  constexpr int kJoin = L < 64 ? kBackWaves : kRows;
   __shared__ float lds[kBackWaves];
-  __shared__ float join[kRows > 1 ? (kRows - 1) * kThreads * CH * E : 1];
+  __shared__ float join[kJoin > 1 ? (kJoin - 1) * L * CH * E : 1];
   const int dim = int(a.dim);
-  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads), t = threadIdx.x % kThreads;
-  auto col = [&](int k) { return (k * kThreads + t) * E; };
+  const int t = threadIdx.x % L;
+  int group = threadIdx.x / L;
+  if constexpr (L >= 64) group = __builtin_amdgcn_readfirstlane(group);
+  auto col = [&](int k) { return (k * L + t) * E; };
   Raw<T> w[CH], x[CH], y[CH], r[CH];
   float dw[CH][E];
 #pragma unroll
@@ -391,7 +407,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a
         }
       }
     }
-    const float mean = row_sum<W>(dot, lds) / float(dim);
+    const float mean = row_sum<L>(dot, lds) / float(dim);
     if (live) {
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
@@ -406,28 +422,40 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a
 #pragma unroll
           for (int e = 0; e < E; ++e) h[e] += g[e];
         }
-        store_as<STREAM>(a.dx + row * a.dx_ld, col(k), dim, h);
+        store_as<WAY>(a.dx + row * a.dx_ld, col(k), dim, h);
       }
     }
   }
   if (!a.partial) return;
-  if constexpr (kRows > 1) {
-    if (group > 0) {
+  if constexpr (L < 64) {                           // the wave's rows, then wave by wave
+#pragma unroll
+    for (int d = L; d < 64; d <<= 1)
 #pragma unroll
       for (int k = 0; k < CH; ++k)
 #pragma unroll
-        for (int e = 0; e < E; ++e) join[((group - 1) * CH * E + k * E + e) * kThreads + t] = dw[k][e];
+        for (int e = 0; e < E; ++e) dw[k][e] += __shfl_xor(dw[k][e], d);
+    group = threadIdx.x >> 6;
+  }
+  if constexpr (kJoin > 1) {
+    const bool holds = L >= 64 || int(threadIdx.x & 63) < L;
+    if (group > 0 && holds) {
+#pragma unroll
+      for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) join[((group - 1) * CH * E + k * E + e) * L + t] = dw[k][e];
     }
     __syncthreads();
-    if (group > 0) return;
-    for (int q = 0; q < kRows - 1; ++q)
+    if (group > 0 || !holds) return;
+    constexpr int kUnroll = kJoin <= 4 ? kJoin - 1 : 1;   // more spills
+#pragma unroll kUnroll
+    for (int q = 0; q < kJoin - 1; ++q)
 #pragma unroll
       for (int k = 0; k < CH; ++k)
 #pragma unroll
-        for (int e = 0; e < E; ++e) dw[k][e] += join[(q * CH * E + k * E + e) * kThreads + t];
+        for (int e = 0; e < E; ++e) dw[k][e] += join[(q * CH * E + k * E + e) * L + t];
   }
 #pragma unroll
-  for (int k = 0; k < CH; ++k) store_as<false>(a.partial + int64_t(blockIdx.x) * dim, col(k), dim, dw[k]);
+  for (int k = 0; k < CH; ++k) store_as<kPlain>(a.partial + int64_t(blockIdx.x) * dim, col(k), dim, dw[k]);
 }
 
 // Rows too long for registers: dx here, the weight's sums in k_norm_back_cols.
@@ -450,7 +478,7 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_back_long(NormBackArgs
       for (int e = 0; e < E; ++e)
         if (c + e < dim) dot += g[e] * w[e] * (h[e] * rstd);
     }
-    const float mean = row_sum<kLongWaves>(dot, lds) / float(dim);
+    const float mean = row_sum<64 * kLongWaves>(dot, lds) / float(dim);
     for (int64_t c = int64_t(threadIdx.x) * E; c < dim; c += step) {
       float h[E], g[E], w[E];
       load_as(x, c, dim, h);
@@ -464,7 +492,7 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_back_long(NormBackArgs
 #pragma unroll
         for (int e = 0; e < E; ++e) h[e] += y[e];
       }
-      store_as<false>(a.dx + row * a.dx_ld, c, dim, h);
+      store_as<kPlain>(a.dx + row * a.dx_ld, c, dim, h);
     }
   }
 }
@@ -482,7 +510,7 @@ __global__ __launch_bounds__(256) void k_norm_back_cols(NormBackArgs<T> a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[e] += g[e] * (h[e] * a.rstd[row]);
   }
-  store_as<false>(a.partial + int64_t(blockIdx.y) * a.dim, c, a.dim, dw);
+  store_as<kPlain>(a.partial + int64_t(blockIdx.y) * a.dim, c, a.dim, dw);
 }
 
 // dweight[c] = the sum over the workgroups' partial rows, in a fixed order: 16
@@ -517,35 +545,36 @@ __global__ __launch_bounds__(1024) void k_norm_dweight(const float* partial, int
 // host side
 // ---------------------------------------------------------------------------
 
-// Elements of a row that W waves hold, 32 bytes a lane; longer rows than 16 waves
-// hold go through the k_*_long kernels.
-constexpr int64_t wave_dim(int elem) { return 64 * 32 / elem; }
-constexpr int64_t kLongBlocks = 512;
-int row_waves(int64_t dim, int elem) {
-  int w = 1;
-  while (w < 16 && w * wave_dim(elem) < dim) w *= 2;
-  return w;
+// Lanes that hold a row, 32 bytes each: 8 to 1024, a power of two. Longer rows go through
+// the k_*_long kernels.
+constexpr int kMaxLanes = 1024;
+int row_lanes(int64_t dim, int elem) {
+  int l = 8;
+  while (l < kMaxLanes && l * int64_t(32 / elem) < dim) l *= 2;
+  return l;
 }
-bool row_fits(int64_t dim, int elem) { return dim <= 16 * wave_dim(elem); }
+bool row_fits(int64_t dim, int elem) { return dim <= kMaxLanes * int64_t(32 / elem); }
 
 // Workgroups (and partial rows) of a backward launch: one a CU, or fewer for
 // few rows.
 constexpr int64_t kBackBlocks = 256;
+constexpr int64_t kLongBlocks = 512;
 int32_t back_blocks(int64_t rows, int64_t dim, int elem) {
   if (!row_fits(dim, elem)) return int32_t(std::min(rows, kLongBlocks));
-  const int64_t per = kBackWaves / row_waves(dim, elem);
+  const int64_t per = 64 * kBackWaves / row_lanes(dim, elem);
   return int32_t(std::min((rows + per - 1) / per, kBackBlocks));
 }
 
-template <typename F>
-void with_waves(int w, F&& f) {
-  using std::integral_constant;
-  if (w == 1) f(integral_constant<int, 1>{});
-  else if (w == 2) f(integral_constant<int, 2>{});
-  else if (w == 4) f(integral_constant<int, 4>{});
-  else if (w == 8) f(integral_constant<int, 8>{});
-  else f(integral_constant<int, 16>{});
+template <int L = 8, typename F>
+void with_lanes(int lanes, F&& f) {
+  if constexpr (L < kMaxLanes) {
+    if (lanes > L) return with_lanes<2 * L>(lanes, f);
+  }
+  f(std::integral_constant<int, L>{});
 }
+
+template <int L>
+constexpr Way past_l2_way = L < 64 ? kOnce : kStream;
 
 bool rows_aligned(const void* p, int64_t ld, int elem, int to) {
   return reinterpret_cast<uintptr_t>(p) % to == 0 && ld * elem % to == 0;
@@ -560,11 +589,11 @@ void launch_norm(const NormArgs<T>& a, int64_t rows, hipStream_t stream) {
   const int64_t written = rows * a.dim * ((RES ? int(sizeof(T)) : 0) + (BITS8 ? 1 : int(sizeof(T))));
   const bool past_l2 = written >= kStreamBytes && rows_aligned(a.out, a.out_ld, BITS8 ? 1 : sizeof(T), BITS8 ? 8 : 16) &&
                       (!RES || rows_aligned(a.sum, a.sum_ld, sizeof(T), 16));
-  with_waves(row_waves(a.dim, sizeof(T)), [&](auto w) {
-    if (past_l2)
-      k_norm<T, RES, BITS8, w.value, true><<<unsigned(rows), 64 * w.value, 0, stream>>>(a);
-    else
-      k_norm<T, RES, BITS8, w.value, false><<<unsigned(rows), 64 * w.value, 0, stream>>>(a);
+  with_lanes(row_lanes(a.dim, sizeof(T)), [&](auto l) {
+    constexpr int L = l.value, per = kNormRows<L>;
+    const unsigned blocks = unsigned((rows + per - 1) / per);
+    if (past_l2) k_norm<T, RES, BITS8, L, past_l2_way<L>><<<blocks, L * per, 0, stream>>>(a, rows);
+    else k_norm<T, RES, BITS8, L, kPlain><<<blocks, L * per, 0, stream>>>(a, rows);
   });
 }
 
@@ -577,11 +606,11 @@ void launch_back(const NormBackArgs<T>& a, hipStream_t stream) {
       k_norm_back_cols<T><<<dim3(unsigned((a.dim + 256 * kElems<T> - 1) / (256 * kElems<T>)), blocks), 256, 0, stream>>>(a);
     return;
   }
-  with_waves(row_waves(a.dim, sizeof(T)), [&](auto w) {
-    if (a.rows * a.dim * int64_t(sizeof(T)) >= kStreamBytes && rows_aligned(a.dx, a.dx_ld, sizeof(T), 16))
-      k_norm_back<T, RES, w.value, true><<<blocks, 64 * kBackWaves, 0, stream>>>(a);
-    else
-      k_norm_back<T, RES, w.value, false><<<blocks, 64 * kBackWaves, 0, stream>>>(a);
+  const bool past_l2 = a.rows * a.dim * int64_t(sizeof(T)) >= kStreamBytes && rows_aligned(a.dx, a.dx_ld, sizeof(T), 16);
+  with_lanes(row_lanes(a.dim, sizeof(T)), [&](auto l) {
+    constexpr int L = l.value;
+    if (past_l2) k_norm_back<T, RES, L, past_l2_way<L>><<<blocks, 64 * kBackWaves, 0, stream>>>(a);
+    else k_norm_back<T, RES, L, kPlain><<<blocks, 64 * kBackWaves, 0, stream>>>(a);
   });
 }
 

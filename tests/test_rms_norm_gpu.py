@@ -32,7 +32,10 @@ def rows_of(rows, dim, pitch, shift, dtype, scale, seed):
 SIZES = [(1, 1, 0, 0), (3, 5, 0, 0), (1, 4096, 0, 0), (7, 64, 0, 0), (5, 511, 3, 1), (4, 513, 0, 0),
          (9, 1024, 8, 0), (6, 1027, 73, 1), (3, 2049, 0, 3), (40, 4096, 0, 0), (2, 8191, 1, 0),
          (600, 130, 0, 0), (3, 8192, 0, 0), (2, 16384, 0, 0), (2, 16385, 0, 0), (2, 32768, 0, 0),
-         (2, 33000, 0, 0), (1, 70001, 5, 1)]
+         (2, 33000, 0, 0), (1, 70001, 5, 1),
+         # rows that share a wave, workgroups that are not full, and outputs that go past L2
+         (513, 33, 0, 0), (257, 128, 8, 0), (1030, 100, 4, 0), (130, 255, 1, 1), (66000, 128, 0, 0),
+         (33000, 256, 0, 0), (17000, 504, 8, 0)]
 
 
 @pytest.mark.parametrize("residual", [False, True])
