@@ -152,10 +152,17 @@ __device__ __forceinline__ float row_sum(float v, float* lds) {
   if ((threadIdx.x & 63) == 0) lds[wave] = v;
   __syncthreads();
   const float* mine = lds + wave / W * W;
-  float s = mine[0];
+  if constexpr (W < 16) {
+    float s = mine[0];
 #pragma unroll
-  for (int w = 1; w < W; ++w) s += mine[w];
-  return s;
+    for (int w = 1; w < W; ++w) s += mine[w];
+    return s;
+  } else {                              // 16 values at once would spill in k_norm_back
+    float s = mine[threadIdx.x % W];
+#pragma unroll
+    for (int d = W / 2; d > 0; d >>= 1) s += __shfl_xor(s, d);
+    return s;
+  }
 }
 template <int L>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, float* lds) {
@@ -350,6 +357,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a
   constexpr int CH = kChunks, E = kElems<T>, kRows = 64 * kBackWaves / L;
   // rows of dweight sums to be joined, after those within a wave
   constexpr int kJoin = L < 64 ? kBackWaves : kRows;
+  constexpr bool kKeepW = L < 1024;                 // otherwise the kernel spills; L2 holds it
   __shared__ float lds[kBackWaves];
   __shared__ float join[kJoin > 1 ? (kJoin - 1) * L * CH * E : 1];
   const int dim = int(a.dim);
@@ -361,7 +369,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a
   float dw[CH][E];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    w[k] = load_raw(a.w, col(k), dim);
+    if (kKeepW) w[k] = load_raw(a.w, col(k), dim);
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[k][e] = 0.f;
   }
@@ -398,7 +406,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a
         float h[E], g[E], wk[E];
         unpack(cx[k], h);
         unpack(cy[k], g);
-        unpack(w[k], wk);
+        unpack(kKeepW ? w[k] : load_raw(a.w, col(k), dim), wk);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           h[e] = h[e] * cs;
@@ -414,7 +422,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_norm_back(NormBackArgs<T> a
         float h[E], g[E], wk[E];
         unpack(cx[k], h);
         unpack(cy[k], g);
-        unpack(w[k], wk);
+        unpack(kKeepW ? w[k] : load_raw(a.w, col(k), dim), wk);
 #pragma unroll
         for (int e = 0; e < E; ++e) h[e] = cs * (g[e] * wk[e] - h[e] * cs * mean);
         if constexpr (RES) {
