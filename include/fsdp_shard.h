@@ -347,8 +347,8 @@ fsdp_status fsdp_muon_apply_shard(const fsdp_unit* unit, const void* const* tens
  * with a NaN or an infinity gives NaN. The same inputs give the same bits.
  * `workspace`: device memory, 256-byte aligned, of fsdp_orthogonalize_workspace
  * bytes for the same sizes; its contents need not be kept from call to call.
- * 1 <= steps <= 64; sides up to 2^20. The call enqueues 3 launches a step and 2
- * more per 24 matrices; if the runtime refuses one, those before it stay. */
+ * 1 <= steps <= 64; sides up to 2^20. Per 24 matrices the call enqueues 2 launches
+ * and 3 to 6 a step; if the runtime refuses one, those before it stay. */
 fsdp_status fsdp_orthogonalize_workspace(int32_t n_mats, const int64_t* rows, const int64_t* cols,
                                          int64_t* bytes);
 fsdp_status fsdp_orthogonalize(int32_t n_mats, fsdp_dtype dtype, const void* const* mats,
@@ -361,7 +361,7 @@ fsdp_status fsdp_orthogonalize(int32_t n_mats, fsdp_dtype dtype, const void* con
  *   h = x, or with a residual h = x + residual rounded to dtype, written to residual_out;
  *   rstd = 1/sqrt(mean(h*h) + eps);  y = h*rstd*weight   (fp32);
  *   out = y rounded to dtype; with `scales` instead
- *   scale = max(max|y| / 448, 2^-126),  out = e4m3_rne(clamp(y / scale, -448, 448)).
+ *   scale = max(max|y| / 448, 2^-126),  out = e4m3_rne(y * (1 / scale)).
  * A NaN in a row gives a NaN scale and a row of NaN. Every row argument has its
  * own pitch in elements (>= dim); rows and pointers may have any element
  * alignment. rows < 2^22, dim <= 2^24. rows == 0 is a no-op. */

@@ -33,6 +33,14 @@ constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.1754943508222875e-38f;   // 2^-126: a row of zeros divides by this
 constexpr int64_t kStreamBytes = int64_t(32) << 20;    // outputs from here on are streamed past L2
 
+// Two fp32 values to bf16 (nearest, ties to even; a NaN stays one) in one instruction: the
+// same bits as to_bf16 for every value that is not NaN.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t round_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const uint16_t* p) { return widen(*p); }
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
@@ -109,15 +117,15 @@ __device__ __forceinline__ void store_as(float* p, I c, I dim, const float (&x)[
 template <Way WAY, typename I>
 __device__ __forceinline__ void store_as(uint16_t* p, I c, I dim, const float (&x)[8]) {
   if (c + 8 <= dim) {
-    store_vector<WAY>(p, c, dim, u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                          pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])});
+    store_vector<WAY>(p, c, dim, u32x4{round_bf16(x[0], x[1]), round_bf16(x[2], x[3]),
+                                       round_bf16(x[4], x[5]), round_bf16(x[6], x[7])});
   } else if (c < dim) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (c + e < dim) store1(p + c + e, x[e]);
   }
 }
-// N values in e4m3 (nearest, ties to even; the caller clamped them).
+// N values in e4m3 (nearest, ties to even), whose magnitudes round to 448 at most.
 template <Way WAY, int N, typename I>
 __device__ __forceinline__ void store_e4m3(uint8_t* p, I c, I dim, const float (&x)[N]) {
   uint32_t q[N / 4];
@@ -136,8 +144,16 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, I c, I dim, const float (
   }
 }
 
-__device__ __forceinline__ float round_to(float x, const float*) { return x; }
-__device__ __forceinline__ float round_to(float x, const uint16_t*) { return __uint_as_float(to_bf16(x) << 16); }
+// h rounded to T's type, as values.
+__device__ __forceinline__ void round_to(float (&)[4]) {}
+__device__ __forceinline__ void round_to(float (&h)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const uint32_t q = round_bf16(h[e], h[e + 1]);
+    h[e] = lo_bf16(q);
+    h[e + 1] = hi_bf16(q);
+  }
+}
 
 // The sum (and the largest bit pattern) over a row's L lanes, the same in every lane;
 // `lds` holds a value for each wave of the workgroup.
@@ -201,16 +217,15 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
   const float s = __uint_as_float(top) / kE4m3Max;
   return s < kMinScale ? kMinScale : s;         // NaN stays NaN
 }
-__device__ __forceinline__ float clamp_e4m3(float q) {
-  return q > kE4m3Max ? kE4m3Max : q < -kE4m3Max ? -kE4m3Max : q;
-}
-
+// y is multiplied by 1 / scale: |y| <= 448 scale, so the product is below 448 (1 + 2^-22),
+// which still rounds to 448, and no clamp is needed. A division by scale for each value
+// took a quarter of the kernel's time; this differs from it by at most an fp32 step.
 // A row is held by L lanes in registers: lane t's piece k is elements (L k + t) * kElems<T>
 // onward. Long rows take a workgroup each; rows that a part of a wave can hold share a
 // workgroup of four waves (32768 bf16 rows of 64 with a residual: 21 us with a wave
 // a row, 6.6 so; their gradients 31 and 15).
 // All three arrays are loaded before the row's sum is waited for. 8192 bf16 rows of 4096
-// with a residual and an e4m3 output take 38 us (6.2 TB/s; 44 us with ordinary stores; a
+// with a residual and an e4m3 output take 38 us (6.2 TB/s; 44 with ordinary stores; a
 // workgroup that stays for many rows and loads the next ahead 48), a single row 3 us.
 template <int L>
 constexpr int kNormRows = L < 64 ? 256 / L : 1;
@@ -241,7 +256,8 @@ __global__ __launch_bounds__(L * kNormRows<L>) void k_norm(NormArgs<T> a, int64_
       float y[E];
       unpack(r[k], y);
 #pragma unroll
-      for (int e = 0; e < E; ++e) h[k][e] = round_to(h[k][e] + y[e], a.sum);
+      for (int e = 0; e < E; ++e) h[k][e] += y[e];
+      round_to(h[k]);
       store_as<WAY>(a.sum + row * a.sum_ld, col(k), dim, h[k]);
     }
 #pragma unroll
@@ -263,11 +279,12 @@ __global__ __launch_bounds__(L * kNormRows<L>) void k_norm(NormArgs<T> a, int64_
   }
   if constexpr (BITS8) {
     const float scale = scale_of(row_max<L>(top, lds));
+    const float inverse = 1.f / scale;
     if (t == 0) a.scales[row] = scale;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) h[k][e] = clamp_e4m3(h[k][e] / scale);
+      for (int e = 0; e < E; ++e) h[k][e] *= inverse;
       store_e4m3<WAY>(static_cast<uint8_t*>(a.out) + row * a.out_ld, col(k), dim, h[k]);
     }
   }
@@ -288,7 +305,8 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_long(NormArgs<T> a) {
       float y[E];
       load_as(r, c, dim, y);
 #pragma unroll
-      for (int e = 0; e < E; ++e) h[e] = round_to(h[e] + y[e], x);
+      for (int e = 0; e < E; ++e) h[e] += y[e];
+      round_to(h);
     }
   };
   float sq = 0.f;
@@ -301,7 +319,7 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_long(NormArgs<T> a) {
   }
   const float rstd = rstd_of(row_sum<64 * kLongWaves>(sq, lds), dim, a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-  float scale = 1.f;
+  float inverse = 1.f;
   if constexpr (BITS8) {
     uint32_t top = 0;
     for (int64_t c = int64_t(threadIdx.x) * E; c < dim; c += step) {
@@ -312,7 +330,8 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_long(NormArgs<T> a) {
       for (int e = 0; e < E; ++e)
         if (c + e < dim) top = max(top, abs_bits(h[e] * rstd * w[e]));
     }
-    scale = scale_of(row_max<64 * kLongWaves>(top, lds));
+    const float scale = scale_of(row_max<64 * kLongWaves>(top, lds));
+    inverse = 1.f / scale;
     if (threadIdx.x == 0) a.scales[row] = scale;
   }
   for (int64_t c = int64_t(threadIdx.x) * E; c < dim; c += step) {
@@ -322,7 +341,7 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_norm_long(NormArgs<T> a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       h[e] = h[e] * rstd * w[e];
-      if constexpr (BITS8) h[e] = clamp_e4m3(h[e] / scale);
+      if constexpr (BITS8) h[e] *= inverse;
     }
     if constexpr (BITS8) store_e4m3<kPlain>(static_cast<uint8_t*>(a.out) + row * a.out_ld, c, dim, h);
     else store_as<kPlain>(static_cast<T*>(a.out) + row * a.out_ld, c, dim, h);
