@@ -22,8 +22,10 @@ constexpr int kThreads = 64;      // one wave a workgroup
 constexpr int kV = 4;             // consecutive elements a lane
 constexpr int64_t kTile = int64_t(kThreads) * kV;
 constexpr int64_t kFastElems = int64_t(1) << 22;   // windows from here on stream past L2
-// Workgroups per CU of the streaming momentum kernel (8 rows of the 7B block's
-// window: 105 us without a limit, 100 with 14, 103 with 16 to 24, 117 with 10).
+// Workgroups per CU of the streaming momentum kernel with 8 rows (the 7B block's
+// window: 105 us without a limit, 100 with 14, 103 with 16 to 24, 117 with 10); with
+// fewer rows more of them, for alike many bytes (a window of 26.2 M elements and one
+// row: 65 us with 14, 48.5 so; 4 rows 79 and 72.7).
 // The streaming apply is best without one (44 us; 47 with 16, 56 with 12).
 constexpr int kMomentumPerCu = 14;
 
@@ -239,7 +241,8 @@ fsdp_status reduce_momentum(const fsdp_unit* u, int32_t n_grads, const void* con
   if (fsdp_status st = fsdp::check_no_pending_error(what)) return st;
   bool fast = u->valid >= kFastElems && aligned(momentum, 16) && aligned(update, 8);
   for (int32_t k = 0; k < n_grads; ++k) fast = fast && aligned(a.g[k], 8);
-  if (fast) k_muon_momentum<true><<<unsigned(tiles), kThreads, cap_lds(kMomentumPerCu), stream>>>(a);
+  const int per_cu = kMomentumPerCu * 80 / (8 * std::min(n_grads, 8) + 16);   // alike many bytes a CU
+  if (fast) k_muon_momentum<true><<<unsigned(tiles), kThreads, per_cu < 32 ? cap_lds(per_cu) : 0, stream>>>(a);
   else k_muon_momentum<false><<<unsigned(tiles), kThreads, 0, stream>>>(a);
   return fsdp::after_launch(what);
 }
