@@ -33,6 +33,7 @@ def close(got, want, size, rel):
     ([(256, 1024), (1024,), (1024, 256), (256,)], 4, 1, 4, 0), ([(1000, 1037)], 8, 7, 8, 0),
     ([(1000, 1037)], 8, 5, 8, 3), ([(300, 301)], 2, 1, 11, 2), ([(300, 300)], 3, 0, 16, 0),
     ([(97, 89)], 64, 63, 64, 1), ([(2048, 2048)], 1, 0, 2, 0),
+    ([(4099, 2051)], 2, 1, 3, 0), ([(4099, 2051)], 2, 1, 9, 0), ([(4099, 2051)], 2, 0, 1, 0),
 ])
 def test_reduce_momentum(lib, shapes, F, rank, rows, shift, nesterov):
     u = lib.Unit(shapes, F, rank)
@@ -80,7 +81,7 @@ def test_reduce_momentum_scale_specials_and_repeat(lib):
     ([(5, 7), (3,)], 4, 1, 0, True), ([(1,)], 1, 0, 0, True), ([(33, 77), (0, 4), (1001,), (2, 3)], 2, 1, 1, True),
     ([(256, 1024), (1024,), (1024, 256), (256,)], 4, 1, 0, True), ([(1000, 1037)], 8, 7, 0, False),
     ([(7,)] * 150 + [(400, 33)], 1, 0, 0, True), ([(3, 5)] * 333, 3, 2, 2, True),
-    ([(2000, 1024), (999,)], 2, 0, 0, True),
+    ([(2000, 1024), (999,)], 2, 0, 0, True), ([(4099, 2051), (5,)], 2, 1, 0, True),
 ])
 def test_apply(lib, shapes, F, rank, shift, emit):
     u = lib.Unit(shapes, F, rank)
