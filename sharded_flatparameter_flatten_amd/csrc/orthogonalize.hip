@@ -680,6 +680,7 @@ struct Plan {
   int64_t mp, np;             // padded
   int64_t x, xt0, xt1, sym0, sym1, sym2, partial;   // workspace offsets
   int32_t parts;
+  bool pairs;
 };
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
@@ -709,7 +710,13 @@ int choose_pad(int32_t count, const int64_t* rows, const int64_t* cols) {
 // and one launch more, so they pay from some n / m above 1 on. Nearly square
 // matrices, whose least singular values are tiny, also lose more that way
 // (2.9e-3 against 2.3e-3 after 5 steps at n = m; alike from n = 1.25 m on).
-bool pair_steps(const Plan& q) { return 4 * int64_t(q.n) >= 5 * int64_t(q.m) && 4 * q.np >= 5 * q.mp; }
+bool may_pair(int64_t m, int64_t n, int64_t mp, int64_t np) { return 4 * n >= 5 * m && 4 * np >= 5 * mp; }
+// For short matrices the launch weighs more. Measured in us, pairs and single steps:
+// 128 x 512 80 and 73, 256 x 1024 twice 90 and 87, 512 x 1536 alike, 512 x 2048 116 and
+// 120, 1024 x 2048 155 and 152, 1024 x 3000 175 and 181, 2048 x 4096 475 and 496. The
+// matrices of a call do alike, since their n-th products share a launch: pairs where one
+// of them gains (of 515 x 1373, 2049 x 771 and a square the first in single steps 204, both in pairs 195).
+bool gains_by_pairs(int64_t mp, int64_t np) { return np >= mp + 1152; }
 
 constexpr int64_t kMaxSide = int64_t(1) << 20;
 
@@ -738,6 +745,12 @@ int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int p
                   std::vector<Plan>* plans, int64_t* part) {
   int64_t at = 0, tiles = 0, longest = 0;
   const int tile = std::min(pad, 128);
+  bool gain = false;
+  for (int32_t i = 0; i < count; ++i) {
+    const int64_t m = std::min(rows[i], cols[i]), n = std::max(rows[i], cols[i]);
+    const int64_t mp = round_up(m, pad), np = round_up(n, pad);
+    gain = gain || (m > 0 && may_pair(m, n, mp, np) && gains_by_pairs(mp, np));
+  }
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
     at += round_up(bytes, 1024);
@@ -757,7 +770,8 @@ int64_t make_plan(int32_t count, const int64_t* rows, const int64_t* cols, int p
       q.xt1 = take(q.np * pitch_of(q.mp) * 2);
       q.sym0 = take(q.mp * pitch_of(q.mp) * 2);
       q.sym1 = take(q.mp * pitch_of(q.mp) * 2);
-      q.sym2 = pair_steps(q) ? take(q.mp * pitch_of(q.mp) * 2) : 0;
+      q.pairs = gain && may_pair(q.m, q.n, q.mp, q.np);
+      q.sym2 = q.pairs ? take(q.mp * pitch_of(q.mp) * 2) : 0;
       q.parts = int32_t(std::min<int64_t>(kSumBlocks, (int64_t(q.m) * q.n + kSumRow - 1) / kSumRow));
       q.partial = take(q.parts * 8);
       const int64_t side = q.mp / tile;
@@ -907,9 +921,8 @@ void list_products(const Plan& q, char* ws, int steps, const double* coeffs,
   auto multiply = [&](const f16* a, const f16* b, f16* to) {
     symmetric(kSym, a, b, to, q.mp, 1.0 / kScaleS);
   };
-  const bool pairs = pair_steps(q);
   for (int step = 0, group = 0; step < steps; ++group) {
-    const int n = pairs && group % 2 == 0 && step + 2 <= steps ? 2 : 1;
+    const int n = q.pairs && group % 2 == 0 && step + 2 <= steps ? 2 : 1;
     step += n;
     symmetric(kSym, x, x, s0, q.np, double(kScaleS) / (double(kScaleX) * kScaleX));
     poly(s0, s1);                               // P_1
