@@ -35,7 +35,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Wall", "-I", INCL
 DEVICE = [f"--offload-arch={ARCH}", "-mcode-object-version=5",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 # The small products' first arguments arrive in registers (a launch 0.2 us shorter).
-SOURCE_FLAGS = {"orthogonalize.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=4"]}
+SOURCE_FLAGS = {"orthogonalize.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=8"]}
 
 
 def _run(cmd, verbose):

@@ -100,7 +100,7 @@ struct Prod {
   int32_t per_xcd;   // tiles on one XCD
 };
 // CAP: products a launch can hold. Arguments of few products are 6 us a call
-// cheaper than those of 24 (19 launches; 95 against 100 us of GPU time).
+// cheaper than those of 24 (19 launches; 95 against 100 us of GPU time), those of 8 3 us.
 template <int CAP>
 struct ProdArgs {
   Prod p[CAP];
@@ -108,7 +108,7 @@ struct ProdArgs {
   int32_t run;                  // workgroups of one XCD's run over all products, or 0
   int32_t slots;                // workgroups on one XCD
 };
-constexpr int kFewMats = 4;
+constexpr int kFewMats = 4, kSomeMats = 8;
 
 // t / d for 0 <= t < 2^24, 0 < d and quotients below 2^20 (the estimate is then off by at most one): a few instructions, where a division takes 40 that wait for each other.
 __device__ __forceinline__ int divide(int t, int d) {
@@ -199,11 +199,13 @@ __device__ __forceinline__ void static_for(F&& f) {
 // waves of 128 x 128, which read a third less LDS (7B block 13.0 ms); half lines in twice as
 // many stages took 13.0 ms too.
 //
-// end0 to end2 and run are args.end and args.run of up to 4 products, as arguments of
+// run and end0 to end6 are args.run and args.end of up to 8 products, as arguments of
 // their own because only such ones can be preloaded into registers.
 template <int T, int WM, int WN, int S, int CAP>
-__global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(int32_t end0, int32_t end1, int32_t end2,
-                                                                int32_t run, ProdArgs<CAP> args) {
+__global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(int32_t run, int32_t end0, int32_t end1,
+                                                                int32_t end2, int32_t end3, int32_t end4,
+                                                                int32_t end5, int32_t end6, ProdArgs<CAP> args) {
+  const int32_t ends[kSomeMats - 1] = {end0, end1, end2, end3, end4, end5, end6};
   constexpr int kWaves = WM * WN;
   constexpr int kLoads = 2 * T / 8;               // 1 KB loads a stage
   static_assert(kWaves % 2 == 0 && kLoads % kWaves == 0, "whole loads per wave");
@@ -224,7 +226,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ortho_product(int32_t end0, in
   int s = 0, before = 0;
 #pragma unroll
   for (int q = 0; q < CAP - 1; ++q) {             // past all products: an empty one, or the last
-    const int end = CAP == kFewMats ? (q == 0 ? end0 : q == 1 ? end1 : end2) : args.end[q];
+    const int end = CAP <= kSomeMats ? ends[q] : args.end[q];
     s += key >= end;
     before = key >= end ? end : before;
   }
@@ -872,16 +874,23 @@ void launch_products(const std::vector<const Prod*>& now, Shape shape, bool join
   }
   if (even) a.run = a.slots = (groups + 7) / 8;
   const int blocks = 8 * a.slots;
-  if (tile == 256) k_ortho_product<256, 2, 4, 2, CAP><<<blocks, 512, 0, stream>>>(a.end[0], a.end[1], a.end[2], a.run, a);
-  else if (tile == 128 && groups <= 256) k_ortho_product<128, 2, 2, 4, CAP><<<blocks, 256, 0, stream>>>(a.end[0], a.end[1], a.end[2], a.run, a);
-  else if (tile == 128) k_ortho_product<128, 2, 2, 2, CAP><<<blocks, 256, 0, stream>>>(a.end[0], a.end[1], a.end[2], a.run, a);
-  else k_ortho_product<64, 2, 2, 4, CAP><<<blocks, 256, 0, stream>>>(a.end[0], a.end[1], a.end[2], a.run, a);
+  int32_t e[kSomeMats - 1];
+  std::fill(e, e + kSomeMats - 1, INT32_MAX);
+  std::copy(a.end, a.end + std::min(CAP, kSomeMats - 1), e);
+  auto go = [&](auto kernel, int threads) {
+    kernel<<<blocks, threads, 0, stream>>>(a.run, e[0], e[1], e[2], e[3], e[4], e[5], e[6], a);
+  };
+  if (tile == 256) go(k_ortho_product<256, 2, 4, 2, CAP>, 512);
+  else if (tile == 128 && groups <= 256) go(k_ortho_product<128, 2, 2, 4, CAP>, 256);
+  else if (tile == 128) go(k_ortho_product<128, 2, 2, 2, CAP>, 256);
+  else go(k_ortho_product<64, 2, 2, 4, CAP>, 256);
 }
 
 fsdp_status launch(const std::vector<const Prod*>& now, int pad, float* part, hipStream_t stream) {
   const Shape shape = launch_shape(now, pad, part != nullptr);
   for (int join = 0; join <= int(shape.split); ++join) {
     if (now.size() <= kFewMats) launch_products<kFewMats>(now, shape, join != 0, part, stream);
+    else if (now.size() <= kSomeMats) launch_products<kSomeMats>(now, shape, join != 0, part, stream);
     else launch_products<kMaxMats>(now, shape, join != 0, part, stream);
     if (fsdp_status st = fsdp::after_launch("fsdp_orthogonalize")) return st;
   }
