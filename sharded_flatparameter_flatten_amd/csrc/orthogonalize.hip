@@ -190,9 +190,9 @@ __device__ __forceinline__ void static_for(F&& f) {
 // S - 1 stages' time to arrive.
 //
 // What bounds it: with full launches of 256 tiles the card's power (the 7B block's matrices,
-// 12.1 ms, 1.2 PFLOP/s of the formula's operations; with zeros for data 10.1 ms): a stage
+// 12.1 to 12.5 ms, 1.2 PFLOP/s of the formula's operations; with zeros for data 10.1 ms): a stage
 // takes 2500 cycles at 1.65 GHz, 2048 of them matrix instructions, and reading its fragments
-// keeps LDS as busy. With few tiles the latency of a launch: 4.7 us for a 64 tile of 4 stages,
+// keeps LDS as busy. With few tiles the latency of a launch: 5 us for a 64 tile of 4 stages,
 // 0.2 us for each further one (16 KB at the 64 bytes a cycle that a CU loads).
 //
 // Why these tiles: 256 on 8 waves (two a SIMD) hides the stage's wait for loads better than 4

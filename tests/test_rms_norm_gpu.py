@@ -226,3 +226,34 @@ def test_streams_and_graph(lib):
         if i == 0:
             for k in a:
                 assert M.same_bits(a[k], c[k]), k
+
+
+def test_binding_says_which_argument_is_wrong(lib):
+    new = lambda *s, t=BF: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+    x, w, out = new(4, 32), new(32), new(4, 32)
+    good = dict(rstd=new(4, t=F), residual=new(4, 32), residual_out=new(4, 32))
+    lib.rms_norm(x, w, out, **good)
+    lib.rms_norm(x, w, out, stream=torch.cuda.current_stream(), **good)
+    lib.rms_norm(x, w, out, stream=torch.cuda.current_stream().cuda_stream, **good)
+    for args, kw, error, name in (
+            ((x, w.float(), out), {}, TypeError, "weight"), ((x, new(31), out), {}, ValueError, "weight"),
+            ((x, w, new(4, 31)), {}, ValueError, "out"), ((x, w, out.cpu()), {}, ValueError, "out"),
+            ((x, w, out), {"rstd": new(3, t=F)}, ValueError, "rstd"), ((x, w, out), {"rstd": new(4)}, TypeError, "rstd"),
+            ((x, w, out), {"residual": x}, ValueError, "residual"), ((x, w, out), {"scales": new(4, t=F)}, TypeError, "out"),
+            ((x.T, new(4), new(32, 4)), {}, ValueError, "x"), ((x, w, None), {}, TypeError, "out")):
+        with pytest.raises(error, match=name):
+            lib.rms_norm(*args, **kw)
+    with pytest.raises(ValueError, match="dresidual"):
+        lib.rms_norm_backward(x, x, w, new(4, t=F), out, None, None, dresidual=new(5, 32))
+    with pytest.raises(lib.FsdpError):                   # no workspace for dweight
+        lib.rms_norm_backward(x, x.clone(), w, new(4, t=F), out, new(32), None)
+    u = lib.Unit([(4, 32)], 1, 0)
+    hp, m = lib.MuonHparams(), new(128, t=F)
+    with pytest.raises(ValueError, match=r"grads\[1\]"):
+        lib.reduce_momentum_shard(u, [new(128), new(127)], m, new(128), hp)
+    with pytest.raises(TypeError, match="momentum"):
+        lib.reduce_momentum_shard(u, [new(128)], new(128), new(128), hp)
+    with pytest.raises(ValueError, match="scales"):
+        lib.muon_apply_shard(u, [x], [], m, None, hp)
+    with pytest.raises(TypeError, match=r"tensors\[0\]"):
+        lib.muon_apply_shard(u, [m], [1.0], m, None, hp)
