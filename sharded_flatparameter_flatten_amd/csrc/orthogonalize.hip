@@ -554,7 +554,7 @@ struct Source {
 struct SourceArgs {
   Source s[kMaxMats];
   int32_t ns;
-  float eps;
+  double eps;
 };
 
 // 8 consecutive elements as fp32, from element alignment.
@@ -634,7 +634,13 @@ __global__ __launch_bounds__(256) void k_ortho_start(SourceArgs args) {
   __shared__ double lds4[4];
   __shared__ f16 tile[64][64 + 8];
   const double sq = block_sum_256(int(threadIdx.x) < src.parts ? src.partial[threadIdx.x] : 0.0, lds4);
-  const float scale = float(double(kScaleX) / (sqrt(sq) + double(args.eps)));
+  // The scale as mantissa and exponent: it passes fp32's range where norm + eps is below
+  // 2^-116, and is subnormal far above 2^127. Where both are 0 it is infinite and X NaN.
+  const double norm = sqrt(sq) + args.eps;
+  double scale = double(kScaleX) / norm;
+  if (norm > 0.0 && scale > 0x1p1000) scale = 0x1p1000;      // zeros only, and an eps below 2^-988
+  const float mantissa = float(__builtin_amdgcn_frexp_mant(scale));
+  const int exponent = __builtin_amdgcn_frexp_exp(scale);
 
   const bool tall = src.rows > src.cols;
   const int pr = tall ? src.np : src.mp, pc = tall ? src.mp : src.np;   // G's padded sides
@@ -658,7 +664,7 @@ __global__ __launch_bounds__(256) void k_ortho_start(SourceArgs args) {
     }
     f16x8 q;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = f16(x[e] * scale);
+    for (int e = 0; e < 8; ++e) q[e] = f16(__builtin_amdgcn_ldexpf(x[e], exponent) * mantissa);
     *reinterpret_cast<f16x8*>(as_is + int64_t(r0 + r) * pitch_of(pc) + c0 + c) = q;
     *reinterpret_cast<f16x8*>(&tile[r][c]) = q;
   }
@@ -979,7 +985,7 @@ fsdp_status run(const std::vector<Plan>& plans, const void* const* mats, const i
     const int nb = int(std::min<size_t>(kMaxMats, live.size() - b));
     SourceArgs src{};
     src.ns = nb;
-    src.eps = float(eps);
+    src.eps = eps;
     int blocks = 0;
     for (int k = 0; k < nb; ++k) {
       const int i = live[b + k];
