@@ -341,9 +341,11 @@ fsdp_status fsdp_muon_apply_shard(const fsdp_unit* unit, const void* const* tens
  * in elements; any element alignment. Matrices with no elements are skipped.
  * Products are of fp16 operands with fp32 sums: an element of X is held to 2^-11
  * relative (2^-36 absolute), so the result of the usual 5 steps is within about
- * 1.5e-3 (2-norm) of the exact polynomial's before its rounding to bf16; X, its
- * powers of 2 scaled away, has to stay below 16 and S below 64, which holds for
- * any matrix with coefficients whose polynomial keeps [0, 1.3] below 4. A matrix
+ * 1.5e-3 (2-norm) of the exact polynomial's before its rounding to bf16. X,
+ * S and a I + b S + c S S are held times powers of 2 that are chosen from what the
+ * coefficients' polynomial reaches from [0, 1] step by step (and cost no accuracy):
+ * coefficients may grow X up to 1024, S and a I + b S + c S S, for a pair of steps their
+ * product, up to 2^20; past that the result holds infinities and NaN. A matrix
  * with a NaN or an infinity gives NaN. The same inputs give the same bits.
  * `workspace`: device memory, 256-byte aligned, of fsdp_orthogonalize_workspace
  * bytes for the same sizes; its contents need not be kept from call to call.

@@ -32,11 +32,13 @@
 // values are scaled by powers of two to sit in fp16's normal range: X by
 // 2^12, S and P by 2^10, so |X| < 16, |S| < 64 and |P| < 64 are representable;
 // singular values start at 1 or less and stay below 1.3 with the usual
-// coefficients. A matrix whose norm is far below eps loses precision (its X
+// coefficients. With others the host bounds what X, S and P can reach at each
+// step and takes smaller powers (see Reach). A matrix whose norm is far below eps loses precision (its X
 // has elements near fp16's subnormals once norm / eps < 1e-4).
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <new>
 #include <type_traits>
 #include <utility>
@@ -56,8 +58,8 @@ typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr float kScaleX = 4096.f;     // stored X is X * 2^12
-constexpr float kScaleS = 1024.f;     // stored S and P are times 2^10
+constexpr double kScaleX = 4096;      // stored X is X * 2^12, at most
+constexpr double kScaleS = 1024;      // stored S and P are times 2^10, at most
 constexpr int kBK = 64;               // contracted elements per stage: one 128-byte line a row
 constexpr int kPitchPad = 64;         // elements between rows: see pitch_of
 constexpr int kMaxMats = 24;          // matrices per launch (kernel arguments < 4 KB)
@@ -637,7 +639,7 @@ __global__ __launch_bounds__(256) void k_ortho_start(SourceArgs args) {
   // The scale as mantissa and exponent: it passes fp32's range where norm + eps is below
   // 2^-116, and is subnormal far above 2^127. Where both are 0 it is infinite and X NaN.
   const double norm = sqrt(sq) + args.eps;
-  double scale = double(kScaleX) / norm;
+  double scale = kScaleX / norm;
   if (norm > 0.0 && scale > 0x1p1000) scale = 0x1p1000;      // zeros only, and an eps below 2^-988
   const float mantissa = float(__builtin_amdgcn_frexp_mant(scale));
   const int exponent = __builtin_amdgcn_frexp_exp(scale);
@@ -903,9 +905,45 @@ fsdp_status launch(const std::vector<const Prod*>& now, int pad, float* part, hi
   return FSDP_OK;
 }
 
+// What the coefficients let a step's matrices reach. A singular value x of X becomes
+// x p(x^2), p(s) = a + b s + c s^2, and starts at 1 or less; with S's eigenvalues
+// s = x^2 in [0, top^2] nothing in S, p(S) or X passes the largest value of s, |p(s)| or
+// |x p(x^2)| there, which lie at an end or where a derivative is zero. Past kMostX and
+// kMostS the bounds end: the scales would push ordinary values below fp16's range.
+constexpr double kMostX = 1024, kMostS = 1 << 20;
+struct Reach {
+  const double* k;
+  double p(double s) const { return std::fabs(k[0] + s * (k[1] + s * k[2])); }
+  template <typename F>
+  static double most(std::initializer_list<double> at, double end, double cap, F&& f) {
+    double m = f(end);
+    for (double s : at)
+      if (s >= 0 && s < end) m = std::max(m, f(s));
+    return m < cap ? m : cap;         // the cap for NaN too
+  }
+  double poly(double top) const {
+    return most({0.0, -k[1] / (2 * k[2])}, top * top, kMostS, [&](double s) { return p(s); });
+  }
+  // and 1% for the roundings of X and S
+  double step(double top) const {
+    const double b = 3 * k[1], c = 5 * k[2];        // a + b s + c s^2 = 0
+    const double q = -0.5 * (b + std::copysign(std::sqrt(b * b - 4 * k[0] * c), b));
+    return most({q / c, k[0] / q}, top * top, kMostX, [&](double s) { return 1.01 * std::sqrt(s) * p(s); });
+  }
+};
+// The power of two for values up to `most`: the usual one where it leaves an eighth of fp16's range.
+double scale_for(double most, double usual) {
+  while (most * usual > 57344) usual /= 2;
+  return usual;
+}
+
 // The products of one matrix, in order; the n-th of every matrix go into one launch.
 void list_products(const Plan& q, char* ws, int steps, const double* coeffs,
                    void* out, int64_t out_ld, std::vector<Prod>* list) {
+  struct Sym {                                  // a symmetric matrix and its scale
+    f16* at;
+    double scale;
+  };
   auto at = [&](int64_t offset) { return reinterpret_cast<f16*>(ws + offset); };
   f16 *x = at(q.x), *xt = at(q.xt0), *xt_next = at(q.xt1);
   f16 *s0 = at(q.sym0), *s1 = at(q.sym1), *s2 = at(q.sym2);
@@ -928,30 +966,40 @@ void list_products(const Plan& q, char* ws, int steps, const double* coeffs,
     p.ldc = p.ldct = int32_t(pitch_of(q.mp));
     return p;
   };
-  auto poly = [&](const f16* a, f16* to) {
-    Prod& p = symmetric(kPoly, a, a, to, q.mp, coeffs[2] / kScaleS);
-    p.beta = float(coeffs[1]);
-    p.delta = float(coeffs[0]) * kScaleS;
+  auto poly = [&](Sym s, f16* to, double most) {
+    const double scale = scale_for(most, kScaleS);
+    Prod& p = symmetric(kPoly, s.at, s.at, to, q.mp, coeffs[2] * scale / (s.scale * s.scale));
+    p.beta = float(coeffs[1] * scale / s.scale);
+    p.delta = float(coeffs[0] * scale);
+    return Sym{to, scale};
   };
-  auto multiply = [&](const f16* a, const f16* b, f16* to) {
-    symmetric(kSym, a, b, to, q.mp, 1.0 / kScaleS);
+  auto multiply = [&](Sym a, Sym b, f16* to, double most) {
+    const double scale = scale_for(most, kScaleS);
+    symmetric(kSym, a.at, b.at, to, q.mp, scale / (a.scale * b.scale));
+    return Sym{to, scale};
   };
+  const Reach reach{coeffs};
+  double top = 1, scale = kScaleX;              // of X
   for (int step = 0, group = 0; step < steps; ++group) {
     const int n = q.pairs && group % 2 == 0 && step + 2 <= steps ? 2 : 1;
     step += n;
-    symmetric(kSym, x, x, s0, q.np, double(kScaleS) / (double(kScaleX) * kScaleX));
-    poly(s0, s1);                               // P_1
-    f16* p = s1;
+    const Sym s = {s0, scale_for(top * top, kScaleS)};
+    symmetric(kSym, x, x, s0, q.np, s.scale / (scale * scale));
+    double most = reach.poly(top), next = reach.step(top);
+    Sym p = poly(s, s1, most);                  // P_1
     if (n == 2) {
-      multiply(s1, s0, s2);                     // P_1 S_1
-      multiply(s1, s2, s0);                     // S_2 = P_1 P_1 S_1
-      poly(s0, s2);                             // P_2
-      multiply(s2, s1, s0);                     // P_2 P_1
-      p = s0;
+      const Sym ps = multiply(p, s, s2, top * next);        // P_1 S_1
+      const Sym second = multiply(p, ps, s0, next * next);  // S_2 = P_1 P_1 S_1
+      const double most2 = reach.poly(next);
+      const Sym p2 = poly(second, s2, most2);               // P_2
+      p = multiply(p2, p, s0, std::min(most * most2, kMostS));   // P_2 P_1
+      next = reach.step(next);
     }
+    top = next;
     const bool last = step == steps;
-    Prod& u = add(last ? kFinal : kUpdate, xt, p, q.mp,
-                  last ? 1.0 / (double(kScaleS) * kScaleX) : 1.0 / kScaleS);
+    const double next_scale = last ? 1.0 : scale_for(top, kScaleX);
+    Prod& u = add(last ? kFinal : kUpdate, xt, p.at, q.mp, next_scale / (p.scale * scale));
+    scale = next_scale;
     u.side_i = int32_t(q.np);
     u.out_i = q.n;
     u.out_j = q.m;

@@ -36,3 +36,38 @@ def test_norms_at_the_ends_of_fp32(lib, scale, dtype):
 def test_zero_matrix_with_a_tiny_eps_is_zero(lib, eps):
     (o,) = ortho(lib, [torch.zeros(30, 50, device="cuda")], eps=eps)
     assert bool((o == 0).all())
+
+
+# Every value of these is exact in the operands' format, so the results are the formula's bits: one
+# row of 2^-5 or so in absolute value whose norm is a power of two, among rows of zeros.
+@pytest.mark.parametrize("shape", [(1, 1), (64, 4096), (4096, 64), (1024, 1024)])
+@pytest.mark.parametrize("steps,coeffs", [
+    (5, (3.0, 0.0, 0.0)),            # 3^k: 243 in the end
+    (2, (8.5, -14.0, 6.0)),          # below 4 on [0, 1.3], and the polynomials' product 72.25 where X is 0
+    (3, (-60.0, 30.0, 31.0)), (2, (100.0, -200.0, 101.0)), (7, (2.0, 0.0, 0.0)),
+])
+def test_coefficients_that_grow(lib, steps, coeffs, shape):
+    m = torch.zeros(*shape, device="cuda")
+    line = m[0] if shape[0] <= shape[1] else m[:, 0]
+    line.copy_(torch.randn(line.numel(), generator=torch.Generator().manual_seed(2)).sign())
+    (o,) = ortho(lib, [m], steps=steps, coeffs=coeffs, eps=0.0)
+    x = 1.0
+    for _ in range(steps):
+        x = coeffs[0] * x + coeffs[1] * x ** 3 + coeffs[2] * x ** 5
+    want = (m.double() / line.numel() ** 0.5 * x).to(BF)
+    assert torch.equal(o, want)
+
+
+def test_coefficients_that_grow_on_any_matrix(lib):
+    """Singular values that pass 16: powers of 2 are taken out of X, S and P."""
+    gen = torch.Generator().manual_seed(3)
+    for shape in ((90, 130), (300, 2000), (700, 500)):
+        m = torch.randn(*shape, generator=gen).cuda()
+        for steps, coeffs in ((5, (4.0, 0.0, 0.0)), (4, (3.0, 1.0, 0.0))):
+            (o,) = ortho(lib, [m], steps=steps, coeffs=coeffs)
+            want = M.polar(m, steps=steps, coeffs=coeffs)
+            assert want.norm() > 20
+            # as for polar_tolerance, each rounding amplified by the steps after it: relative to X
+            # by 1 where p is a number, by less than 3 for 3 x + x^3
+            tol = M.BF16 + (M.polar_tolerance(steps) - M.BF16) * (1 if coeffs[1] == 0 else 3 ** (steps - 1))
+            assert (o.double().cpu() - want).norm() <= tol * want.norm()
