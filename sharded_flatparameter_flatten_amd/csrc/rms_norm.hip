@@ -33,8 +33,8 @@ constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.1754943508222875e-38f;   // 2^-126: a row of zeros divides by this
 constexpr int64_t kStreamBytes = int64_t(32) << 20;    // outputs from here on are streamed past L2
 
-// Two fp32 values to bf16 (nearest, ties to even; a NaN stays one) in one instruction: the
-// same bits as to_bf16 for every value that is not NaN.
+// Two fp32 values to bf16 (nearest, ties to even) in one instruction: the same bits as
+// to_bf16 for every value that is not NaN. A NaN keeps bits of its own here.
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t round_bf16(float a, float b) {
@@ -100,6 +100,13 @@ __device__ __forceinline__ void store_vector(T* p, I c, I dim, V x) {
   else st_loose<V, sizeof(T)>(p + c, x);
 }
 // N values to column c of a row; elements at or past `dim` are left alone.
+template <int N>
+__device__ __forceinline__ bool has_nan(const float (&x)[N]) {   // one comparison for two values
+  bool nan = false;
+#pragma unroll
+  for (int e = 0; e < N; e += 2) nan |= __builtin_isunordered(x[e], x[e + 1]);
+  return nan;
+}
 template <Way WAY, int N, typename I>
 __device__ __forceinline__ void store_as(float* p, I c, I dim, const float (&x)[N]) {
 #pragma unroll
@@ -114,16 +121,33 @@ __device__ __forceinline__ void store_as(float* p, I c, I dim, const float (&x)[
     }
   }
 }
+// Every NaN is to_bf16's, in a row's whole vectors as in its ragged end; `nan` says whether
+// this lane may have one. The comparisons and the branch cost up to 1% (2% at 16384
+// columns); a sum of squares that is at hand is one comparison for all of its values.
 template <Way WAY, typename I>
-__device__ __forceinline__ void store_as(uint16_t* p, I c, I dim, const float (&x)[8]) {
+__device__ __forceinline__ void store_as(uint16_t* p, I c, I dim, const float (&x)[8], bool nan) {
   if (c + 8 <= dim) {
-    store_vector<WAY>(p, c, dim, u32x4{round_bf16(x[0], x[1]), round_bf16(x[2], x[3]),
-                                       round_bf16(x[4], x[5]), round_bf16(x[6], x[7])});
+    u32x4 q;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = round_bf16(x[2 * e], x[2 * e + 1]);
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(nan) != 0, 0)) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+    }
+    store_vector<WAY>(p, c, dim, q);
   } else if (c < dim) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (c + e < dim) store1(p + c + e, x[e]);
   }
+}
+template <Way WAY, typename I>
+__device__ __forceinline__ void store_as(uint16_t* p, I c, I dim, const float (&x)[8]) {
+  store_as<WAY>(p, c, dim, x, has_nan(x));
+}
+template <Way WAY, typename I>
+__device__ __forceinline__ void store_as(float* p, I c, I dim, const float (&x)[4], bool) {
+  store_as<WAY>(p, c, dim, x);
 }
 // N values in e4m3 (nearest, ties to even), whose magnitudes round to 448 at most.
 template <Way WAY, int N, typename I>
@@ -258,10 +282,10 @@ __global__ __launch_bounds__(L * kNormRows<L>) void k_norm(NormArgs<T> a, int64_
 #pragma unroll
       for (int e = 0; e < E; ++e) h[k][e] += y[e];
       round_to(h[k]);
-      store_as<WAY>(a.sum + row * a.sum_ld, col(k), dim, h[k]);
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) sq += h[k][e] * h[k][e];
+    if constexpr (RES) store_as<WAY>(a.sum + row * a.sum_ld, col(k), dim, h[k], sq != sq);
   }
   const float rstd = rstd_of(row_sum<L>(sq, lds), dim, a.eps);
   if (a.rstd && t == 0) a.rstd[row] = rstd;

@@ -71,3 +71,37 @@ def test_coefficients_that_grow_on_any_matrix(lib):
             # by 1 where p is a number, by less than 3 for 3 x + x^3
             tol = M.BF16 + (M.polar_tolerance(steps) - M.BF16) * (1 if coeffs[1] == 0 else 3 ** (steps - 1))
             assert (o.double().cpu() - want).norm() <= tol * want.norm()
+
+
+@pytest.mark.parametrize("rows,dim,shift", [(3, 21, 0), (2, 4099, 1), (2, 16390, 0), (9000, 2049, 7)])
+def test_norm_writes_one_nan(lib, rows, dim, shift):
+    """Every NaN rounds to 0x7FC0, in a row's whole vectors and in its ragged end, in each way of storing."""
+    payloads = torch.tensor([0x7FC1, -0x40, 0x7F81, -1, -0x7F], dtype=torch.int16).view(BF).cuda()   # both signs, quiet and not
+    assert bool(torch.isnan(payloads).all())
+    wide = torch.zeros(rows, dim + shift, dtype=BF, device="cuda")
+    w, x = torch.ones(dim, dtype=BF, device="cuda"), torch.ones(rows, dim + shift, dtype=BF, device="cuda")[:, :dim]
+    at = torch.arange(0, dim, 3, device="cuda")
+    res = torch.zeros(rows, dim, dtype=BF, device="cuda")
+    res[:, at] = payloads[at % 5]
+    out, total, rstd = wide[:, :dim], torch.empty_like(wide)[:, :dim], torch.empty(rows, device="cuda")
+    lib.rms_norm(x, w, out, residual=res, residual_out=total, rstd=rstd)
+    dx, dw = torch.empty_like(wide)[:, :dim], torch.empty(dim, dtype=BF, device="cuda")
+    ws = torch.empty(lib.rms_norm_backward_workspace(rows, dim), dtype=torch.uint8, device="cuda")
+    lib.rms_norm_backward(res, x, w, torch.ones(rows, device="cuda"), dx, dw, ws, dresidual=res)
+    torch.cuda.synchronize()
+    for t in (out, total, dx, dw):
+        nan = torch.isnan(t)
+        assert bool((t.contiguous().view(torch.int16)[nan] == 0x7FC0).all())
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(dx).all())      # a row's sum holds them
+    here = torch.zeros(dim, dtype=torch.bool, device="cuda")
+    here[at] = True
+    assert torch.equal(torch.isnan(total), here.expand(rows, dim))
+    assert bool((total[:, ~here] == 1).all()) and torch.equal(torch.isnan(dw), here)
+    # a weight's NaN stays in its column
+    w[5] = payloads[1]
+    lib.rms_norm(x, w, out)
+    torch.cuda.synchronize()
+    here[:] = False
+    here[5] = True
+    assert torch.equal(torch.isnan(out), here.expand(rows, dim))
+    assert bool((out.contiguous().view(torch.int16)[:, 5] == 0x7FC0).all())
