@@ -481,18 +481,22 @@ def reduce_momentum_shard(unit: Unit, grads, momentum: torch.Tensor, update: tor
 def muon_apply_shard(unit: Unit, tensors, scales, master: torch.Tensor,
                      param_out: torch.Tensor | None, hp: MuonHparams, stream=None):
     """This rank's window of the whole update tensors, each times its scale, applied to its
-    master weights (and the bf16 parameter)."""
+    master weights (and the bf16 parameter). Tensors that do not reach into the window, and
+    their scales, may be None: a rank orthogonalises only what it applies."""
     status = _calls.muon_apply_shard(
-        unit._address, unit.numels, unit.shard_valid, tensors, scales, master, param_out, hp.lr,
-        hp.momentum, hp.weight_decay, hp.nesterov, stream if stream is None else _stream(stream))
+        unit._address, unit.numels, unit.shard_begin, unit.shard_valid, tensors, scales, master,
+        param_out, hp.lr, hp.momentum, hp.weight_decay, hp.nesterov,
+        stream if stream is None else _stream(stream))
     if status == 0:
         return
     if status is None:
         if len(tensors) != unit.n_tensors or len(scales) != unit.n_tensors:
             raise ValueError(f"need {unit.n_tensors} tensors and scales, got {len(tensors)} and "
                              f"{len(scales)}")
-        for i, (t, n) in enumerate(zip(tensors, unit.numels)):
-            _dev(t, torch.bfloat16, "tensors", n, i)
+        end = unit.shard_begin + unit.shard_valid
+        for i, (t, at, n) in enumerate(zip(tensors, unit.offsets, unit.numels)):
+            if t is not None or max(at, unit.shard_begin) < min(at + n, end):
+                _dev(t, torch.bfloat16, "tensors", n, i)
         _dev(master, torch.float32, "master", unit.shard_valid)
         if param_out is not None:
             _dev(param_out, torch.bfloat16, "param_out", unit.shard_valid)

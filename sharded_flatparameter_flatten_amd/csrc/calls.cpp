@@ -176,31 +176,35 @@ PyObject* reduce_momentum_shard(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return status_of([&] { return fsdp_reduce_momentum_shard(unit, int32_t(rows), g, m, u, &hp, s); });
 }
 
-// unit, its tensors' elements, its window's elements, tensors, scales, master, parameter,
-// lr, momentum, weight decay, nesterov, stream
+// unit, its tensors' elements, its window's begin and elements, tensors, scales, master,
+// parameter, lr, momentum, weight decay, nesterov, stream. A tensor and a scale that do not
+// reach into the window may be None.
 PyObject* muon_apply_shard(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!wants(n, 12)) return nullptr;
+  if (!wants(n, 13)) return nullptr;
   const fsdp_unit* unit = static_cast<const fsdp_unit*>(PyLong_AsVoidPtr(a[0]));
-  const int64_t valid = PyLong_AsLongLong(a[2]);
+  const int64_t begin = PyLong_AsLongLong(a[2]), valid = PyLong_AsLongLong(a[3]);
   fsdp_muon_hparams hp{};
-  if (PyErr_Occurred() || !hparams(a + 7, 0.0, &hp)) return nullptr;
-  const Items sizes(a[1]), tensors(a[3]), scales(a[4]);
+  if (PyErr_Occurred() || !hparams(a + 8, 0.0, &hp)) return nullptr;
+  const Items sizes(a[1]), tensors(a[4]), scales(a[5]);
   if (!sizes.seq || !tensors.seq || !scales.seq) return nullptr;
   const Py_ssize_t count = sizes.size();
   if (tensors.size() != count || scales.size() != count) Py_RETURN_NONE;
   std::vector<const void*> t(static_cast<size_t>(count) + 1);
   std::vector<double> k(static_cast<size_t>(count) + 1);
+  int64_t offset = 0;
   for (Py_ssize_t i = 0; i < count; ++i) {
     const int64_t need = PyLong_AsLongLong(sizes[i]);
-    k[i] = PyFloat_AsDouble(scales[i]);
+    const bool outside = offset + need <= begin || offset >= begin + valid || need == 0;
+    offset += need;
+    if (!outside || scales[i] != Py_None) k[i] = PyFloat_AsDouble(scales[i]);
     if (PyErr_Occurred()) return nullptr;
-    if (!flat(tensors[i], at::kBFloat16, need, false, &t[i])) Py_RETURN_NONE;
+    if (!flat(tensors[i], at::kBFloat16, need, outside, &t[i])) Py_RETURN_NONE;
   }
   float* p;
   void* w;
-  if (!flat(a[5], at::kFloat, valid, false, &p) || !flat(a[6], at::kBFloat16, valid, true, &w)) Py_RETURN_NONE;
+  if (!flat(a[6], at::kFloat, valid, false, &p) || !flat(a[7], at::kBFloat16, valid, true, &w)) Py_RETURN_NONE;
   hipStream_t s;
-  if (!stream_of(a[11], *tensor(a[5]), &s)) return nullptr;
+  if (!stream_of(a[12], *tensor(a[6]), &s)) return nullptr;
   return status_of([&] { return fsdp_muon_apply_shard(unit, t.data(), k.data(), p, w, &hp, s); });
 }
 

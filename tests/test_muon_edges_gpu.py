@@ -105,3 +105,27 @@ def test_norm_writes_one_nan(lib, rows, dim, shift):
     here[5] = True
     assert torch.equal(torch.isnan(out), here.expand(rows, dim))
     assert bool((out.contiguous().view(torch.int16)[:, 5] == 0x7FC0).all())
+
+
+def test_apply_takes_none_outside_the_window(lib):
+    """A rank needs the tensors that reach into its window, and no others."""
+    shapes, F_ = [(40, 100), (77,), (0, 3), (100, 40), (64, 64)], 4
+    gen = torch.Generator().manual_seed(4)
+    ts = [torch.randn(*s, generator=gen).to(BF).cuda() for s in shapes]
+    scales = [1.0, 2.0, 0.5, 1.5, 0.25]
+    hp = lib.MuonHparams(lr=0.1, weight_decay=0.05)
+    for rank in range(F_):
+        u = lib.Unit(shapes, F_, rank)
+        end = u.shard_begin + u.shard_valid
+        mine = [max(o, u.shard_begin) < min(o + n, end) for o, n in zip(u.offsets, u.numels)]
+        assert not all(mine)
+        p = torch.randn(u.shard_valid, generator=gen).cuda()
+        q = p.clone()
+        lib.muon_apply_shard(u, ts, scales, p, None, hp)
+        lib.muon_apply_shard(u, [t if m else None for t, m in zip(ts, mine)],
+                             [k if m else None for k, m in zip(scales, mine)], q, None, hp)
+        torch.cuda.synchronize()
+        assert M.same_bits(p, q)
+        first = mine.index(True)
+        with pytest.raises(TypeError, match=r"tensors\[%d\]" % first):
+            lib.muon_apply_shard(u, [None if i == first else t for i, t in enumerate(ts)], scales, q, None, hp)
