@@ -118,7 +118,7 @@ def library_path() -> str:
 
 def _load():
     path = library_path()
-    if not os.path.exists(path) or not os.path.exists(os.path.join(_HERE, "_calls.so")):
+    if not os.path.exists(path):
         raise ImportError(
             f"{path} is not built; run `python -c 'import __graft_entry__ as g; g.build()'` "
             "(or python sharded_flatparameter_flatten_amd/build.py) first")
@@ -171,8 +171,25 @@ def _load():
     return lib
 
 
+class _NoCalls:
+    """Stands for the extension module where it cannot be loaded (not built, or built for another
+    torch): the calls it marshals raise, the others, which need the library alone, work."""
+
+    def __init__(self, why: ImportError):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(
+            f"{name} needs the extension module _calls.so, which does not load ({self._why}); run "
+            "`python -c 'import __graft_entry__ as g; g.build()'` "
+            "(or python sharded_flatparameter_flatten_amd/build.py)") from self._why
+
+
 _lib = _load()
-from . import _calls  # noqa: E402  (links against the library that _load opened)
+try:
+    from . import _calls  # noqa: E402  (links against the library that _load opened)
+except ImportError as e:
+    _calls = _NoCalls(e)
 
 
 def abi_version() -> int:
@@ -194,7 +211,8 @@ def _ptr_array(ptrs):
 # The current stream's handle without a torch.cuda.Stream object around it (0.1 us
 # instead of 2 us a call, which shows in the calls whose kernels take 3 us).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_calls.set_current_stream(_raw_stream or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+if not isinstance(_calls, _NoCalls):
+    _calls.set_current_stream(_raw_stream or (lambda index: torch.cuda.current_stream(index).cuda_stream))
 
 
 def _stream(stream, device=None):
