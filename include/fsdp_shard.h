@@ -377,7 +377,7 @@ typedef struct {
   float* scales;              /* rows, or NULL: out in dtype */
   int64_t rows, dim;
   int64_t x_pitch, residual_pitch, residual_out_pitch, out_pitch;
-  double eps;                 /* finite, >= 0 */
+  double eps;                 /* finite, >= 0; fp32, a positive one 2^-149 at least */
   fsdp_dtype dtype;
   int32_t reserved;
 } fsdp_rms_norm_args;

@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <new>
 #include <type_traits>
 
@@ -706,6 +707,7 @@ fsdp_status launch_norm_as(const fsdp_rms_norm_args& n, hipStream_t stream) {
   a.sum_ld = n.residual_out_pitch;
   a.out_ld = n.out_pitch;
   a.eps = static_cast<float>(n.eps);
+  if (n.eps > 0.0 && a.eps == 0.f) a.eps = std::numeric_limits<float>::denorm_min();   // 0 / 0 otherwise
   if (a.res && a.scales) launch_norm<T, true, true>(a, n.rows, stream);
   else if (a.res) launch_norm<T, true, false>(a, n.rows, stream);
   else if (a.scales) launch_norm<T, false, true>(a, n.rows, stream);

@@ -129,3 +129,15 @@ def test_apply_takes_none_outside_the_window(lib):
         first = mine.index(True)
         with pytest.raises(TypeError, match=r"tensors\[%d\]" % first):
             lib.muon_apply_shard(u, [None if i == first else t for i, t in enumerate(ts)], scales, q, None, hp)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("dim", [40, 20000])
+def test_norm_of_zeros_with_a_tiny_eps_is_zero(lib, dim, dtype):
+    """A positive eps below fp32's least number is not taken for 0: rows of zeros stay zeros."""
+    x, w = torch.zeros(3, dim, dtype=dtype, device="cuda"), torch.ones(dim, dtype=dtype, device="cuda")
+    for eps in (1e-40, 1e-46, 1e-300):
+        out, rstd = torch.full_like(x, 3.0), torch.empty(3, device="cuda")
+        lib.rms_norm(x, w, out, eps=eps, rstd=rstd)
+        torch.cuda.synchronize()
+        assert bool((out == 0).all()) and bool(torch.isfinite(rstd).all())
