@@ -141,3 +141,64 @@ def test_norm_of_zeros_with_a_tiny_eps_is_zero(lib, dim, dtype):
         lib.rms_norm(x, w, out, eps=eps, rstd=rstd)
         torch.cuda.synchronize()
         assert bool((out == 0).all()) and bool(torch.isfinite(rstd).all())
+
+
+def test_offsets_past_32_bits_in_the_step(lib):
+    """A window of over 2^31 elements: every one of the momentum's, and of the master's."""
+    u = lib.Unit([((1 << 16) + 1, 1 << 15), (77,)], 1, 0)
+    n, hp = u.shard_valid, lib.MuonHparams(lr=0.5, momentum=0.5, nesterov=False, weight_decay=0.0)
+    grad = torch.empty(n, dtype=BF, device="cuda").random_(-100, 100)
+    m, upd = torch.ones(n, device="cuda"), torch.empty(n, dtype=BF, device="cuda")
+    lib.reduce_momentum_shard(u, [grad], m, upd, hp, grad_scale=1.0)
+    parts = [slice(a, min(a + (1 << 28), n)) for a in range(0, n, 1 << 28)]
+    for s in parts:                                       # halves of small whole numbers: exact
+        want = 0.5 + grad[s].float()
+        assert torch.equal(m[s], want) and torch.equal(upd[s], want.to(BF))
+    del m
+    tensors = list(grad.split(u.numels))
+    p, w = torch.full((n,), 3.0, device="cuda"), upd
+    lib.muon_apply_shard(u, tensors, [1.0, 2.0], p, w, hp)
+    for s in parts:
+        want = 3.0 - 0.5 * grad[s].float()
+        if s.stop == n:
+            want[-77:] = 3.0 - grad[s][-77:].float()
+        assert torch.equal(p[s], want) and torch.equal(w[s], want.to(BF))
+
+
+@pytest.mark.parametrize("rows,dim,pitch", [((1 << 22) - 1, 513, 513), (3, 70, (1 << 31) + 8), (3, 17000, (1 << 30) + 1)])
+def test_offsets_past_32_bits_in_the_norm(lib, rows, dim, pitch):
+    x = torch.empty((rows - 1) * pitch + dim, dtype=BF, device="cuda").as_strided((rows, dim), (pitch, 1))
+    out, dx = torch.empty_strided(x.shape, x.stride(), dtype=BF, device="cuda"), torch.empty(rows, dim, dtype=BF, device="cuda")
+    step = 1 << 16
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    for a in range(0, rows, step):
+        x[a:a + step] = torch.randn(min(step, rows - a), dim, generator=gen, device="cuda").to(BF)
+    w, rstd, dw = torch.ones(dim, dtype=BF, device="cuda"), torch.empty(rows, device="cuda"), torch.empty(dim, dtype=BF, device="cuda")
+    ws = torch.empty(lib.rms_norm_backward_workspace(rows, dim), dtype=torch.uint8, device="cuda")
+    lib.rms_norm(x, w, out, rstd=rstd)
+    lib.rms_norm_backward(x, x, w, rstd, dx, dw, ws)
+    sums = torch.zeros(dim, dtype=torch.float64, device="cuda")
+    for a in range(0, rows, step):
+        X = x[a:a + step].double()
+        y, r = M.norm_forward(X, w.double(), 1e-6)
+        # as for shorter rows: a lane's chunks, the joins and a few products in fp32, then bf16
+        fp32 = (128 + dim // 1024) * M.F32
+        assert bool(((out[a:a + step].double() - y).abs() <= (fp32 + M.BF16) * 1.01 * y.abs()).all())
+        want = M.norm_backward(X, X, w.double(), r)[0]
+        size = r * (X.abs() + (X * r).abs() * (X * X * r).mean(1, keepdim=True))
+        assert bool(((dx[a:a + step].double() - want).abs() <= 1.01 * fp32 * size + M.BF16 * want.abs()).all())
+        sums += (X * X * r).sum(0)
+    # a workgroup adds a 256th of the rows, then come the joins of its waves and of the workgroups
+    assert bool(((dw.double() - sums).abs() <= (rows // 256 + 300) * M.F32 * sums + M.BF16 * sums.abs()).all())
+
+
+def test_offsets_past_32_bits_in_a_matrix(lib):
+    pitch = (1 << 30) + 3
+    m = torch.empty(4 * pitch + 90, dtype=BF, device="cuda").as_strided((5, 90), (pitch, 1))
+    m.copy_(torch.randn(5, 90, generator=torch.Generator().manual_seed(7)).to(BF))
+    out = torch.empty_strided(m.shape, m.stride(), dtype=BF, device="cuda")
+    ws = torch.empty(lib.orthogonalize_workspace([m]), dtype=torch.uint8, device="cuda")
+    lib.orthogonalize([m], [out], ws)
+    torch.cuda.synchronize()
+    want = M.polar(m)
+    assert (out.double().cpu() - want).norm() <= M.polar_tolerance(5) * want.norm()
