@@ -294,7 +294,10 @@ fsdp_status fsdp_unflatten(const fsdp_unit* unit, fsdp_dtype src_dtype, fsdp_dty
  * bf16 update (fsdp_reduce_momentum_shard); the windows are gathered into whole
  * matrices (fsdp_cast_unflatten); the matrices are orthogonalised
  * (fsdp_orthogonalize); every rank applies its window of the result to its
- * master weights (fsdp_muon_apply_shard). Persistent state is fp32 master and
+ * master weights (fsdp_muon_apply_shard). The calls step the whole unit: vectors among
+ * its tensors take their update as it is, times their scale (and decay also where that is
+ * 0). Vectors that AdamW is to step belong in a unit of their own, for
+ * fsdp_reduce_adamw_shard. Persistent state is fp32 master and
  * momentum: 8 bytes a parameter of the window beside the bf16 parameter and
  * gradient, against AdamW's 12.
  * ------------------------------------------------------------------------- */
@@ -339,14 +342,21 @@ fsdp_status fsdp_muon_apply_shard(const fsdp_unit* unit, const void* const* tens
  * `mats` (of `dtype`) and `outs` (bf16): host arrays of device pointers to
  * row-major rows[i] x cols[i] matrices with row pitches mat_ld[i] and out_ld[i]
  * in elements; any element alignment. Matrices with no elements are skipped.
- * Products are of fp16 operands with fp32 sums: an element of X is held to 2^-11
- * relative (2^-36 absolute), so the result of the usual 5 steps is within about
- * 1.5e-3 (2-norm) of the exact polynomial's before its rounding to bf16. X,
- * S and a I + b S + c S S are held times powers of 2 that are chosen from what the
- * coefficients' polynomial reaches from [0, 1] step by step (and cost no accuracy):
- * coefficients may grow X up to 1024, S and a I + b S + c S S, for a pair of steps their
- * product, up to 2^20; past that the result holds infinities and NaN. A matrix
- * with a NaN or an infinity gives NaN. The same inputs give the same bits.
+ * Products are of fp16 operands with fp32 sums, for fp32 matrices too: an element of X
+ * is held to 2^-11 relative (2^-36 absolute), and so are those of S and its polynomial.
+ * Before its rounding to bf16 the result is about as far from the exact polynomial's as
+ * a change of 2^-11 in every element of the matrix would put it; the rounding of a
+ * gathered momentum to bf16 costs 6 times that. In the 2-norm, for 384 x 1536 and the
+ * usual 5 steps, that is 1.2e-3 with noise a third of the strong directions, 3.6e-3 with
+ * singular values 1/k, 2e-2 with 1/k^2, and more the faster they fall: each step raises
+ * the small ones by up to 3.4, and the roundings with them.
+ * X, S and a I + b S + c S S are held times powers of 2 that are chosen, at no cost in
+ * accuracy, from what the coefficients' polynomial reaches from [0, 1] step by step.
+ * Coefficients may grow X up to 1024, and S and a I + b S + c S S (for a pair of steps
+ * their product) up to 2^20; past that the result holds infinities and NaN. A matrix
+ * with a NaN or an infinity gives NaN.
+ * The same list of matrices gives the same bits. A matrix beside others may give other
+ * bits than alone, since a call takes one tile and one order of products for all.
  * `workspace`: device memory, 256-byte aligned, of fsdp_orthogonalize_workspace
  * bytes for the same sizes; its contents need not be kept from call to call.
  * 1 <= steps <= 64; sides up to 2^20. Per 24 matrices the call enqueues 2 launches
@@ -364,7 +374,9 @@ fsdp_status fsdp_orthogonalize(int32_t n_mats, fsdp_dtype dtype, const void* con
  *   rstd = 1/sqrt(mean(h*h) + eps);  y = h*rstd*weight   (fp32);
  *   out = y rounded to dtype; with `scales` instead
  *   scale = max(max|y| / 448, 2^-126),  out = e4m3_rne(y * (1 / scale)).
- * A NaN in a row gives a NaN scale and a row of NaN. Every row argument has its
+ * A NaN in a row gives a NaN scale and a row of NaN. The sum of squares is fp32: rows
+ * whose mean square passes its range (values from about 1e19) give zeros, and values whose
+ * squares fall below it (1e-22) count as zeros beside eps. Every row argument has its
  * own pitch in elements (>= dim); rows and pointers may have any element
  * alignment. rows < 2^22, dim <= 2^24. rows == 0 is a no-op. */
 typedef struct {
@@ -392,8 +404,9 @@ fsdp_status fsdp_rms_norm(const fsdp_rms_norm_args* args, hipStream_t stream);
  * elsewhere; dx is then the gradient of both x and residual. dweight may be
  * NULL; otherwise `workspace` (device memory, 16-byte aligned) has
  * fsdp_rms_norm_backward_workspace bytes. Sums are joined in a fixed order: the
- * same inputs give the same bits. rows == 0 gives a dweight of zeros. Two
- * launches (three for dim > 2^14); if the runtime refuses one, those before stay. */
+ * same inputs give the same bits. rows == 0 gives a dweight of zeros. One
+ * launch, with dweight two, or three for rows over 32 KB (dim over 2^14 in bf16, 2^13 in
+ * fp32); if the runtime refuses one, those before stay. */
 typedef struct {
   const void* dy;
   const void* x;

@@ -1,5 +1,6 @@
 """Python binding of libfsdpshard.so (argument marshalling only), through ctypes, and for the
-calls with the shortest kernels through the extension module ``_calls`` (csrc/calls.cpp).
+calls with the shortest kernels through the extension module ``_calls`` (csrc/calls.cpp), which
+nothing else needs.
 
 Every step of the path runs in the HIP library; this module only turns torch
 tensors into device pointers, picks the current HIP stream, and turns status

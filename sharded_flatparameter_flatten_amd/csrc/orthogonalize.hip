@@ -28,7 +28,10 @@
 // of X is amplified: the polynomial raises the small singular values (up to
 // 3.4 times a step) over rounding errors that are relative to the large ones.
 // With bf16 operands the result is about 1.1e-2 from the exact polynomial,
-// with fp16 ones 1.4e-3 (2-norm, matrices with a few strong directions). The
+// with fp16 ones 1.4e-3 (2-norm, matrices with a few strong directions over
+// noise). Both grow as the singular values fall faster: fp16 gives 3.6e-3 for
+// 1/k and 2e-2 for 1/k^2 (384 x 1536), half to all of what a change of 2^-11 in
+// each element of G makes, and a sixth of what G's own rounding to bf16 does. The
 // values are scaled by powers of two to sit in fp16's normal range: X by
 // 2^12, S and P by 2^10, so |X| < 16, |S| < 64 and |P| < 64 are representable;
 // singular values start at 1 or less and stay below 1.3 with the usual
@@ -191,11 +194,13 @@ __device__ __forceinline__ void static_for(F&& f) {
 // fragments in registers, so stage k + S may be loaded over stage k, and has
 // S - 1 stages' time to arrive.
 //
-// What bounds it: with full launches of 256 tiles the card's power (the 7B block's matrices,
-// 12.1 to 12.5 ms, 1.2 PFLOP/s of the formula's operations; with zeros for data 10.1 ms): a stage
-// takes 2500 cycles at 1.65 GHz, 2048 of them matrix instructions, and reading its fragments
-// keeps LDS as busy. With few tiles the latency of a launch: 5 us for a 64 tile of 4 stages,
-// 0.2 us for each further one (16 KB at the 64 bytes a cycle that a CU loads).
+// What bounds it, in full launches of 256 tiles (the 7B block's matrices, 11.9 to 12.5 ms, 13.2
+// TFLOP in whole tiles, 1.06 to 1.11 PFLOP/s): whole rounds of tiles on the CUs, which are busy
+// for 85% of a launch (2064, 2608 and 952 tiles on 256 of them), and the card's power (with zeros
+// for data 10.1 ms): a stage takes 2500 cycles at 1.65 GHz, 2048 of them matrix instructions, and
+// reading its fragments keeps LDS as busy. The library's fp16 products of 4096 x 4096 x 4096 and
+// x 11008 reach 1.42 and 1.50 PFLOP/s. With few tiles the latency of a launch: 5 us for a 64 tile
+// of 4 stages, 0.2 us for each further one (16 KB at the 64 bytes a cycle that a CU loads).
 //
 // Why these tiles: 256 on 8 waves (two a SIMD) hides the stage's wait for loads better than 4
 // waves of 128 x 128, which read a third less LDS (7B block 13.0 ms); half lines in twice as
@@ -858,7 +863,7 @@ void launch_products(const std::vector<const Prod*>& now, Shape shape, bool join
   int64_t all_tiles = 0;
   for (const Prod* p : now) all_tiles += tiles_of(*p, shape.tile);
   const int tile = join ? 64 : shape.tile;
-  // 256 tiles keep a share of each product an XCD (the 7B block: 11.95 ms, 12.4 in runs)
+  // 256 tiles keep a share of each product an XCD (the 7B block, both in turn: 12.05 ms, 12.42 in runs)
   bool even = tile < 256;
   for (const Prod* p : now) even = even && p->kt == now[0]->kt;
   int n = 0, groups = 0;
