@@ -425,6 +425,113 @@ typedef struct {
 fsdp_status fsdp_rms_norm_backward_workspace(int64_t rows, int64_t dim, int64_t* bytes);
 fsdp_status fsdp_rms_norm_backward(const fsdp_rms_norm_backward_args* args, hipStream_t stream);
 
+/* Rows of an embedding, looked up and scaled:
+ *   out[n] = weight[tokens[n]] * scale   rounded to dtype,
+ * a row of zeros where tokens[n] is outside [0, vocab). Row arguments have their own pitch in
+ * elements (>= dim) and any element alignment. rows < 2^22, vocab < 2^22, dim <= 2^24.
+ * rows == 0 is a no-op. One launch. */
+typedef struct {
+  const int64_t* tokens;      /* rows */
+  const void* weight;         /* vocab x dim of dtype */
+  void* out;                  /* rows x dim of dtype */
+  int64_t rows, vocab, dim;
+  int64_t weight_pitch, out_pitch;
+  double scale;               /* finite; rounded to fp32 */
+  fsdp_dtype dtype;
+  int32_t reserved;
+} fsdp_embedding_args;
+fsdp_status fsdp_embedding(const fsdp_embedding_args* args, hipStream_t stream);
+
+/* Its gradient, a row for each of the vocabulary:
+ *   dweight[v] = scale * sum over n with tokens[n] = v of dy[n]   (fp32, in the order of n)
+ *                [+ dweight[v], with accumulate]   rounded to dtype once.
+ * Tokens outside [0, vocab) and those equal to padding_idx (-1: none) add nothing. With accumulate
+ * the rows of absent tokens are neither read nor written: the gradient of an embedding
+ * that is also the head is the head's with this one added. The same inputs give the same bits.
+ * `workspace`: device memory, 16-byte aligned, of fsdp_embedding_backward_workspace bytes; its
+ * contents need not be kept from call to call. rows == 0 writes zeros (with accumulate: nothing).
+ * If the runtime refuses a launch, those before it stay. */
+typedef struct {
+  const int64_t* tokens;      /* rows */
+  const void* dy;             /* rows x dim of dtype */
+  void* dweight;              /* vocab x dim of dtype */
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t rows, vocab, dim;
+  int64_t dy_pitch, dweight_pitch;
+  int64_t padding_idx;
+  double scale;               /* finite; rounded to fp32 */
+  fsdp_dtype dtype;
+  int32_t accumulate;         /* 0 or 1 */
+} fsdp_embedding_backward_args;
+fsdp_status fsdp_embedding_backward_workspace(int64_t rows, int64_t vocab, int64_t dim, int64_t* bytes);
+fsdp_status fsdp_embedding_backward(const fsdp_embedding_backward_args* args, hipStream_t stream);
+
+/* Dropout of `rows` rows of `dim` elements, with the residual's addition:
+ *   t = p * 65536 rounded to the nearest integer (ties to even);
+ *   out = (kept ? x * (65536 / (65536 - t)) : 0) [+ residual]   (fp32, rounded to dtype once).
+ * An element is kept if its 16 random bits, as a number, are t or more; what is dropped is 0
+ * whatever it held. The bits are those of Philox 4 x 32 with 10 rounds, with key
+ * (seed low, seed high) and counter (column / 8, row, o low, o high): element (row, column) has
+ * half column % 2 (0: the low one) of word column / 2 % 4. o = offset + *counter, modulo 2^64;
+ * counter is a device value (or NULL: 0), so that replays of a captured graph can differ. Nothing
+ * is stored: the gradient is the same call on dy. A layer and step takes an offset of its own;
+ * the bits do not depend on pitches or sizes. p = 1 drops everything.
+ * out may be x or residual itself (same address and pitch). rows == 0 is a no-op. One launch. */
+typedef struct {
+  const void* x;
+  const void* residual;       /* NULL: none */
+  void* out;
+  const uint64_t* counter;    /* device memory, or NULL */
+  int64_t rows, dim;
+  int64_t x_pitch, residual_pitch, out_pitch;
+  uint64_t seed, offset;
+  double p;                   /* in [0, 1] */
+  fsdp_dtype dtype;
+  int32_t reserved;
+} fsdp_dropout_args;
+fsdp_status fsdp_dropout(const fsdp_dropout_args* args, hipStream_t stream);
+
+/* Softmax cross entropy of a head's logits z = hidden weight^T, which are never kept, with its
+ * gradients. A row counts if its target is in [0, vocab); with n counted rows, for those
+ *   loss_r = log(1 + sum over v != target of exp(z_v - z_target))   (fp32),
+ *   loss = sum of loss_r, divided by n with FSDP_MEAN (0 where no row counts),
+ *   k = grad_scale, divided by n with FSDP_MEAN,  G = k (softmax(z) - onehot(target)),
+ *   dhidden = G weight,  dweight = G^T hidden   rounded to bf16.
+ * Rows that do not count have a loss of 0, a dhidden of zeros and no part in dweight, whatever
+ * they hold. hidden and weight are bf16, the type of the gathered parameters; products are of bf16
+ * operands with fp32 sums, for which softmax(z) - onehot is rounded to bf16 (2^-8 of each value,
+ * the target's from a difference that does not cancel). A row with a NaN logit gives NaN, one
+ * with an infinite logit NaN or its limit. dhidden or dweight may be NULL; what is not asked for is not computed.
+ * Rows are worked off in pieces of `piece` (0: as many as a scratch of 1 GiB holds); with
+ * more than one piece dweight's sums are kept in fp32 in the workspace between them.
+ * `workspace`: device memory, 256-byte aligned, of as many bytes as
+ * fsdp_linear_cross_entropy_workspace says for the same arguments (of pointers only alignment
+ * counts, and whether dhidden and dweight are NULL); its contents need not be kept from call to call. The same
+ * inputs give the same bits. rows, vocab < 2^22, dim <= 2^20, and the product of any two (of the rows:
+ * those of a piece) at most 2^35. If the runtime refuses a launch,
+ * those before it stay. */
+typedef enum { FSDP_MEAN = 0, FSDP_SUM = 1 } fsdp_reduction;
+typedef struct {
+  const void* hidden;         /* rows x dim, bf16 */
+  const void* weight;         /* vocab x dim, bf16 */
+  const int64_t* targets;     /* rows */
+  float* loss;                /* one value */
+  float* losses;              /* rows, or NULL */
+  void* dhidden;              /* rows x dim, bf16, or NULL */
+  void* dweight;              /* vocab x dim, bf16, or NULL */
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t rows, vocab, dim;
+  int64_t hidden_pitch, weight_pitch, dhidden_pitch, dweight_pitch;
+  int64_t piece;
+  double grad_scale;          /* finite */
+  fsdp_reduction reduction;
+  int32_t reserved;
+} fsdp_linear_cross_entropy_args;
+fsdp_status fsdp_linear_cross_entropy_workspace(const fsdp_linear_cross_entropy_args* args, int64_t* bytes);
+fsdp_status fsdp_linear_cross_entropy(const fsdp_linear_cross_entropy_args* args, hipStream_t stream);
+
 const char* fsdp_status_string(fsdp_status status);
 const char* fsdp_last_error(void);
 

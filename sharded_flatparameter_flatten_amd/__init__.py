@@ -30,6 +30,12 @@ Names follow the C ABI in include/fsdp_shard.h:
 * ``rms_norm(x, weight, out, ...)``         -> fsdp_rms_norm
 * ``rms_norm_backward(dy, x, weight, rstd, dx, dweight, workspace, ...)``
                                             -> fsdp_rms_norm_backward
+* ``embedding(tokens, weight, out, scale)`` -> fsdp_embedding
+* ``embedding_backward(tokens, dy, dweight, workspace, ...)``
+                                            -> fsdp_embedding_backward
+* ``dropout(x, out, p, seed, offset, ...)`` -> fsdp_dropout
+* ``linear_cross_entropy(hidden, weight, targets, loss, workspace, ...)``
+                                            -> fsdp_linear_cross_entropy
 """
 
 from __future__ import annotations
@@ -46,7 +52,8 @@ __all__ = [
     "reduce_shard_hybrid", "reduce_adamw_shard_hybrid", "reduce_shard_bf16acc",
     "reduce_adamw_shard_bf16acc", "MuonHparams", "reduce_momentum_shard", "muon_apply_shard",
     "orthogonalize", "orthogonalize_workspace", "rms_norm", "rms_norm_backward",
-    "rms_norm_backward_workspace", "abi_version", "library_path",
+    "rms_norm_backward_workspace", "embedding", "embedding_backward", "embedding_backward_workspace",
+    "dropout", "linear_cross_entropy", "linear_cross_entropy_workspace", "abi_version", "library_path",
     "F32", "BF16",
 ]
 
@@ -113,6 +120,44 @@ class _NormBackwardArgs(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("reserved", ctypes.c_int32)]
 
 
+class _EmbeddingArgs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("weight_pitch", ctypes.c_int64), ("out_pitch", ctypes.c_int64),
+                ("scale", ctypes.c_double), ("dtype", ctypes.c_int), ("reserved", ctypes.c_int32)]
+
+
+class _EmbeddingBackwardArgs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("dweight", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("dy_pitch", ctypes.c_int64), ("dweight_pitch", ctypes.c_int64),
+                ("padding_idx", ctypes.c_int64), ("scale", ctypes.c_double),
+                ("dtype", ctypes.c_int), ("accumulate", ctypes.c_int32)]
+
+
+class _DropoutArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("counter", ctypes.c_void_p), ("rows", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("x_pitch", ctypes.c_int64), ("residual_pitch", ctypes.c_int64),
+                ("out_pitch", ctypes.c_int64), ("seed", ctypes.c_uint64),
+                ("offset", ctypes.c_uint64), ("p", ctypes.c_double), ("dtype", ctypes.c_int),
+                ("reserved", ctypes.c_int32)]
+
+
+class _LossArgs(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("targets", ctypes.c_void_p), ("loss", ctypes.c_void_p),
+                ("losses", ctypes.c_void_p), ("dhidden", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("hidden_pitch", ctypes.c_int64), ("weight_pitch", ctypes.c_int64),
+                ("dhidden_pitch", ctypes.c_int64), ("dweight_pitch", ctypes.c_int64),
+                ("piece", ctypes.c_int64), ("grad_scale", ctypes.c_double),
+                ("reduction", ctypes.c_int), ("reserved", ctypes.c_int32)]
+
+
 def library_path() -> str:
     return os.path.join(_HERE, _LIB_NAME)
 
@@ -164,6 +209,12 @@ def _load():
         "fsdp_rms_norm": (st, [ctypes.POINTER(_NormArgs), vp]),
         "fsdp_rms_norm_backward_workspace": (st, [i64, i64, ctypes.POINTER(i64)]),
         "fsdp_rms_norm_backward": (st, [ctypes.POINTER(_NormBackwardArgs), vp]),
+        "fsdp_embedding": (st, [ctypes.POINTER(_EmbeddingArgs), vp]),
+        "fsdp_embedding_backward_workspace": (st, [i64, i64, i64, ctypes.POINTER(i64)]),
+        "fsdp_embedding_backward": (st, [ctypes.POINTER(_EmbeddingBackwardArgs), vp]),
+        "fsdp_dropout": (st, [ctypes.POINTER(_DropoutArgs), vp]),
+        "fsdp_linear_cross_entropy_workspace": (st, [ctypes.POINTER(_LossArgs), ctypes.POINTER(i64)]),
+        "fsdp_linear_cross_entropy": (st, [ctypes.POINTER(_LossArgs), vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -585,11 +636,11 @@ def orthogonalize(mats, outs, workspace: torch.Tensor, steps: int = 5,
 # --- RMS norm -------------------------------------------------------------------------------
 
 
-def _check_norm_type(x: torch.Tensor):
+def _check_norm_type(x: torch.Tensor, name: str = "x"):
     if not isinstance(x, torch.Tensor) or x.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("x must be a float32 or bfloat16 tensor")
+        raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
     if x.dim() != 2:
-        raise ValueError(f"x must be 2-d (rows, dim), got {tuple(x.shape)}")
+        raise ValueError(f"{name} must be 2-d (rows, dim), got {tuple(x.shape)}")
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, eps: float = 1e-6,
@@ -648,4 +699,143 @@ def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
             _dev(dweight, dtype, "dweight", size[1])
             if workspace is not None:
                 _dev(workspace, torch.uint8, "workspace")
+    _check(status)
+
+
+# --- the ends of a model: embedding, dropout, the head's loss --------------------------------
+
+
+def _same_device(*tensors):
+    """``tensors``: those of a call, None for one that is not given."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) > 1:
+        raise ValueError(f"the tensors of a call must be on one device, got {sorted(map(str, devices))}")
+
+
+def embedding(tokens: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, scale: float = 1.0,
+              stream=None):
+    """``out[n]`` = ``weight[tokens[n]] * scale``, zeros where the token is outside the vocabulary.
+
+    ``tokens``: int64, of any shape; ``out`` has a row for each."""
+    status = _calls.embedding(tokens, weight, out, scale, stream if stream is None else _stream(stream))
+    if status == 0:
+        return
+    if status is None:
+        _check_norm_type(weight, "weight")
+        _dev(tokens, torch.int64, "tokens")
+        _dev_rows(weight, weight.dtype, "weight")
+        _dev_rows(out, weight.dtype, "out", (tokens.numel(), weight.shape[1]))
+        _same_device(tokens, weight, out)
+    _check(status)
+
+
+def embedding_backward_workspace(rows: int, vocab: int, dim: int) -> int:
+    """Bytes of device workspace that ``embedding_backward`` needs."""
+    need = ctypes.c_int64()
+    _check(_lib.fsdp_embedding_backward_workspace(int(rows), int(vocab), int(dim), ctypes.byref(need)))
+    return need.value
+
+
+def embedding_backward(tokens: torch.Tensor, dy: torch.Tensor, dweight: torch.Tensor,
+                       workspace: torch.Tensor, scale: float = 1.0, accumulate: bool = False,
+                       padding_idx: int = -1, stream=None):
+    """The gradient of ``embedding`` for its weight: written, or added to what ``dweight`` holds
+    (``accumulate``, which leaves the rows of absent tokens alone). Tokens outside the vocabulary
+    and those equal to ``padding_idx`` add nothing."""
+    status = _calls.embedding_backward(tokens, dy, dweight, workspace, scale, accumulate, padding_idx,
+                                       stream if stream is None else _stream(stream))
+    if status == 0:
+        return
+    if status is None:
+        _check_norm_type(dweight, "dweight")
+        _dev(tokens, torch.int64, "tokens")
+        _dev_rows(dy, dweight.dtype, "dy", (tokens.numel(), dweight.shape[1]))
+        _dev_rows(dweight, dweight.dtype, "dweight")
+        _dev(workspace, torch.uint8, "workspace")
+        _same_device(tokens, dy, dweight, workspace)
+    _check(status)
+
+
+def dropout(x: torch.Tensor, out: torch.Tensor, p: float, seed: int, offset: int = 0,
+            residual: torch.Tensor | None = None, counter: torch.Tensor | None = None, stream=None):
+    """``out`` = dropout of ``x`` (2-d) with probability ``p`` (a multiple of 2^-16 after rounding),
+    plus ``residual``. The mask is a function of ``seed``, ``offset`` (plus ``counter``, an int64
+    on the device, for captured graphs), row and column: the gradient is the same call on dy, and
+    each layer and step takes an offset of its own. ``out`` may be ``x`` or ``residual`` itself."""
+    status = _calls.dropout(x, out, p, seed, offset, residual, counter,
+                            stream if stream is None else _stream(stream))
+    if status == 0:
+        return
+    if status is None:
+        _check_norm_type(x)
+        _dev_rows(x, x.dtype, "x")
+        _dev_rows(out, x.dtype, "out", x.shape)
+        if residual is not None:
+            _dev_rows(residual, x.dtype, "residual", x.shape)
+        if counter is not None:
+            _dev(counter, torch.int64, "counter", 1)
+        _same_device(x, out, residual, counter)
+    _check(status)
+
+
+def _check_loss_inputs(hidden: torch.Tensor, weight: torch.Tensor):
+    for t, name in ((hidden, "hidden"), (weight, "weight")):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be a bfloat16 tensor")
+        if t.dim() != 2:
+            raise ValueError(f"{name} must be 2-d, got {tuple(t.shape)}")
+    if hidden.shape[1] != weight.shape[1]:
+        raise ValueError(f"hidden and weight differ in their rows' length: {hidden.shape[1]} and {weight.shape[1]}")
+
+
+def linear_cross_entropy_workspace(hidden: torch.Tensor, weight: torch.Tensor, dhidden: bool = True,
+                                   dweight: bool = True, piece: int = 0) -> int:
+    """Bytes of device workspace that ``linear_cross_entropy`` needs for these inputs, with the
+    gradients that are asked for."""
+    _check_loss_inputs(hidden, weight)
+    pitch = lambda t: t.stride(0) if t.shape[0] > 1 else t.shape[1]  # noqa: E731
+    a = _LossArgs(hidden=hidden.data_ptr(), weight=weight.data_ptr(), rows=hidden.shape[0],
+                  vocab=weight.shape[0], dim=weight.shape[1], hidden_pitch=pitch(hidden),
+                  weight_pitch=pitch(weight), dhidden=256 if dhidden else None,
+                  dweight=256 if dweight else None, piece=int(piece))
+    need = ctypes.c_int64()
+    _check(_lib.fsdp_linear_cross_entropy_workspace(ctypes.byref(a), ctypes.byref(need)))
+    return need.value
+
+
+def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                         loss: torch.Tensor, workspace: torch.Tensor,
+                         losses: torch.Tensor | None = None, dhidden: torch.Tensor | None = None,
+                         dweight: torch.Tensor | None = None, reduction: str = "mean",
+                         grad_scale: float = 1.0, piece: int = 0, stream=None):
+    """``loss`` (one fp32 value) = the mean or sum of the softmax cross entropy of the logits
+    ``hidden weight^T``, which are never kept, over the rows whose target (int64) is inside the
+    vocabulary; ``losses``: a value a row, 0 for the others. ``dhidden`` and ``dweight``: its
+    gradients times ``grad_scale``, each only if it is given. bf16 inputs and gradients.
+
+    ``workspace``: a device byte tensor of ``linear_cross_entropy_workspace`` bytes for the same
+    inputs, gradients and ``piece`` (rows worked off at a time; 0: chosen)."""
+    if reduction not in ("mean", "sum"):
+        raise ValueError(f"reduction must be 'mean' or 'sum', got {reduction!r}")
+    status = _calls.linear_cross_entropy(hidden, weight, targets, loss, workspace, losses, dhidden, dweight,
+                                         reduction == "sum", grad_scale, piece,
+                                         stream if stream is None else _stream(stream))
+    if status == 0:
+        return
+    if status is None:
+        _check_loss_inputs(hidden, weight)
+        _dev_rows(hidden, torch.bfloat16, "hidden")
+        _dev_rows(weight, torch.bfloat16, "weight")
+        _dev(targets, torch.int64, "targets")
+        if targets.numel() != hidden.shape[0]:
+            raise ValueError(f"need {hidden.shape[0]} targets, got {targets.numel()}")
+        _dev(loss, torch.float32, "loss", 1)
+        _dev(workspace, torch.uint8, "workspace")
+        if losses is not None:
+            _dev(losses, torch.float32, "losses", hidden.shape[0])
+        if dhidden is not None:
+            _dev_rows(dhidden, torch.bfloat16, "dhidden", hidden.shape)
+        if dweight is not None:
+            _dev_rows(dweight, torch.bfloat16, "dweight", weight.shape)
+        _same_device(hidden, weight, targets, loss, workspace, losses, dhidden, dweight)
     _check(status)

@@ -2,7 +2,8 @@
 
 The host indexer (csrc/unit.cpp) is plain C++; the kernels and their entry
 points are HIP: csrc/kernels.hip (the shard step), csrc/muon_step.hip,
-csrc/orthogonalize.hip and csrc/rms_norm.hip, compiled side by side. csrc/calls.cpp
+csrc/orthogonalize.hip, csrc/rms_norm.hip, csrc/embedding.hip, csrc/dropout.hip and
+csrc/linear_cross_entropy.hip, compiled side by side. csrc/calls.cpp
 becomes _calls.so, the extension module that marshals the shortest calls' tensors;
 it links against the library beside it. Flags that fix the numerics:
 -ffp-contract=off (no fused multiply-add anywhere on the path), the default
@@ -26,7 +27,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfsdpshard.so"
 CALLS_NAME = "_calls.so"
-SOURCES = ["unit.cpp", "kernels.hip", "muon_step.hip", "orthogonalize.hip", "rms_norm.hip"]
+SOURCES = ["unit.cpp", "kernels.hip", "muon_step.hip", "orthogonalize.hip", "rms_norm.hip", "embedding.hip",
+           "dropout.hip", "linear_cross_entropy.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -74,7 +76,7 @@ def build(out_dir: str | None = None, defines=(), verbose: bool = False) -> str:
         _run([HIPCC, "-x", "c++", *COMMON, "-fvisibility=hidden", *[x for i in includes for x in ("-isystem", i)],
               "-c", os.path.join(CSRC, "calls.cpp"), "-o", calls], verbose)
 
-    with ThreadPoolExecutor(5) as pool:
+    with ThreadPoolExecutor(8) as pool:
         binding = pool.submit(compile_calls)
         objects = list(pool.map(compile_one, SOURCES))
         binding.result()

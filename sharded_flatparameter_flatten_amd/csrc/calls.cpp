@@ -1,4 +1,4 @@
-// The binding's calls whose kernels take a few microseconds, marshalled in C++:
+// The binding's calls whose kernels may take a few microseconds, marshalled in C++:
 // a call of several tensors costs 4 us of the caller's time through ctypes
 // (attribute by attribute, then a structure), 0.5 us here.
 //
@@ -9,8 +9,10 @@
 
 #include <Python.h>
 
+#include <initializer_list>
 #include <vector>
 
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "fsdp_shard.h"
@@ -208,6 +210,126 @@ PyObject* muon_apply_shard(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return status_of([&] { return fsdp_muon_apply_shard(unit, t.data(), k.data(), p, w, &hp, s); });
 }
 
+// Every tensor of a call is on the first one's device.
+bool one_device(PyObject* const* a, std::initializer_list<int> at) {
+  const at::Tensor* first = nullptr;
+  for (int i : at) {
+    const at::Tensor* t = tensor(a[i]);
+    if (!t) continue;                 // None
+    if (first && t->device() != first->device()) return false;
+    if (!first) first = t;
+  }
+  return true;
+}
+
+// A contiguous device tensor of int64 of any shape: its elements are the rows.
+bool indices(PyObject* o, const int64_t** p, int64_t* rows) {
+  const at::Tensor* t = tensor(o);
+  if (!t) return false;
+  *rows = t->numel();
+  return flat(o, at::kLong, 0, false, p);
+}
+
+bool whole_number(PyObject* o, int64_t* v) {
+  *v = PyLong_AsLongLong(o);
+  return !PyErr_Occurred();
+}
+
+// tokens, weight, out, scale, stream
+PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!wants(n, 5)) return nullptr;
+  fsdp_embedding_args c{};
+  c.scale = PyFloat_AsDouble(a[3]);
+  if (PyErr_Occurred()) return nullptr;
+  const at::Tensor* w = tensor(a[1]);
+  if (!w || !element_type(*w, &c.dtype) || !indices(a[0], &c.tokens, &c.rows)) Py_RETURN_NONE;
+  const at::ScalarType type = w->scalar_type();
+  c.vocab = w->size(0);
+  c.dim = w->size(1);
+  if (!matrix(a[1], type, c.vocab, c.dim, false, &c.weight, &c.weight_pitch) ||
+      !matrix(a[2], type, c.rows, c.dim, false, &c.out, &c.out_pitch) || !one_device(a, {0, 1, 2}))
+    Py_RETURN_NONE;
+  const c10::DeviceGuard guard(w->device());
+  hipStream_t s;
+  if (!stream_of(a[4], *w, &s)) return nullptr;
+  return status_of([&] { return fsdp_embedding(&c, s); });
+}
+
+// tokens, dy, dweight, workspace, scale, accumulate, padding, stream
+PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!wants(n, 8)) return nullptr;
+  fsdp_embedding_backward_args c{};
+  c.scale = PyFloat_AsDouble(a[4]);
+  if (PyErr_Occurred() || !whole_number(a[6], &c.padding_idx)) return nullptr;
+  c.accumulate = PyObject_IsTrue(a[5]);
+  const at::Tensor* dw = tensor(a[2]);
+  if (!dw || !element_type(*dw, &c.dtype) || !indices(a[0], &c.tokens, &c.rows)) Py_RETURN_NONE;
+  const at::ScalarType type = dw->scalar_type();
+  c.vocab = dw->size(0);
+  c.dim = dw->size(1);
+  if (!matrix(a[1], type, c.rows, c.dim, false, &c.dy, &c.dy_pitch) ||
+      !matrix(a[2], type, c.vocab, c.dim, false, &c.dweight, &c.dweight_pitch) ||
+      !flat(a[3], at::kByte, 0, false, &c.workspace) || !one_device(a, {0, 1, 2, 3}))
+    Py_RETURN_NONE;
+  c.workspace_bytes = tensor(a[3])->numel();
+  const c10::DeviceGuard guard(dw->device());
+  hipStream_t s;
+  if (!stream_of(a[7], *dw, &s)) return nullptr;
+  return status_of([&] { return fsdp_embedding_backward(&c, s); });
+}
+
+// x, out, p, seed, offset, residual, counter, stream
+PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!wants(n, 8)) return nullptr;
+  fsdp_dropout_args c{};
+  c.p = PyFloat_AsDouble(a[2]);
+  c.seed = PyLong_AsUnsignedLongLongMask(a[3]);
+  c.offset = PyLong_AsUnsignedLongLongMask(a[4]);
+  if (PyErr_Occurred()) return nullptr;
+  const at::Tensor* x = tensor(a[0]);
+  if (!x || !element_type(*x, &c.dtype)) Py_RETURN_NONE;
+  const at::ScalarType type = x->scalar_type();
+  c.rows = x->size(0);
+  c.dim = x->size(1);
+  if (!matrix(a[0], type, c.rows, c.dim, false, &c.x, &c.x_pitch) ||
+      !matrix(a[1], type, c.rows, c.dim, false, &c.out, &c.out_pitch) ||
+      !matrix(a[5], type, c.rows, c.dim, true, &c.residual, &c.residual_pitch) ||
+      !flat(a[6], at::kLong, 1, true, &c.counter) || !one_device(a, {0, 1, 5, 6}))
+    Py_RETURN_NONE;
+  const c10::DeviceGuard guard(x->device());
+  hipStream_t s;
+  if (!stream_of(a[7], *x, &s)) return nullptr;
+  return status_of([&] { return fsdp_dropout(&c, s); });
+}
+
+// hidden, weight, targets, loss, workspace, losses, dhidden, dweight, sum, grad_scale, piece, stream
+PyObject* linear_cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!wants(n, 12)) return nullptr;
+  fsdp_linear_cross_entropy_args c{};
+  c.reduction = PyObject_IsTrue(a[8]) ? FSDP_SUM : FSDP_MEAN;
+  c.grad_scale = PyFloat_AsDouble(a[9]);
+  if (PyErr_Occurred() || !whole_number(a[10], &c.piece)) return nullptr;
+  const at::Tensor *x = tensor(a[0]), *w = tensor(a[1]);
+  if (!x || !w || x->dim() != 2 || w->dim() != 2) Py_RETURN_NONE;
+  c.rows = x->size(0);
+  c.dim = x->size(1);
+  c.vocab = w->size(0);
+  int64_t rows = 0;
+  if (!matrix(a[0], at::kBFloat16, c.rows, c.dim, false, &c.hidden, &c.hidden_pitch) ||
+      !matrix(a[1], at::kBFloat16, c.vocab, c.dim, false, &c.weight, &c.weight_pitch) ||
+      !indices(a[2], &c.targets, &rows) || rows != c.rows || !flat(a[3], at::kFloat, 1, false, &c.loss) ||
+      !flat(a[4], at::kByte, 0, false, &c.workspace) || !flat(a[5], at::kFloat, c.rows, true, &c.losses) ||
+      !matrix(a[6], at::kBFloat16, c.rows, c.dim, true, &c.dhidden, &c.dhidden_pitch) ||
+      !matrix(a[7], at::kBFloat16, c.vocab, c.dim, true, &c.dweight, &c.dweight_pitch) ||
+      !one_device(a, {0, 1, 2, 3, 4, 5, 6, 7}))
+    Py_RETURN_NONE;
+  c.workspace_bytes = tensor(a[4])->numel();
+  const c10::DeviceGuard guard(x->device());
+  hipStream_t s;
+  if (!stream_of(a[11], *x, &s)) return nullptr;
+  return status_of([&] { return fsdp_linear_cross_entropy(&c, s); });
+}
+
 // The function that gives a device's current stream.
 PyObject* set_current_stream(PyObject*, PyObject* f) {
   Py_INCREF(f);
@@ -236,6 +358,10 @@ PyMethodDef g_methods[] = {
     method<rms_norm_backward>("rms_norm_backward"),
     method<reduce_momentum_shard>("reduce_momentum_shard"),
     method<muon_apply_shard>("muon_apply_shard"),
+    method<embedding>("embedding"),
+    method<embedding_backward>("embedding_backward"),
+    method<dropout>("dropout"),
+    method<linear_cross_entropy>("linear_cross_entropy"),
     {"set_current_stream", set_current_stream, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

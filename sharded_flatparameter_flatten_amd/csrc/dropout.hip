@@ -1,0 +1,135 @@
+// Dropout of rows on gfx950 with a mask that is never stored, and its entry point.
+//
+//   out = keep ? x * 65536 / (65536 - t) : 0   [+ residual],   t = round(p * 65536),
+// where an element is kept if its 16 random bits, as a number, are t or more: the expectation of
+// out is x exactly, for the p that t stands for. The gradient is the same call on dy.
+//
+// The bits are Philox 4 x 32 with 10 rounds (Salmon, Moraes, Dror, Shaw: Parallel random numbers,
+// as easy as 1, 2, 3; 2011): one block of 128 bits for 8 columns of a row, from the seed as key
+// and (group of 8 columns, row, offset) as counter, so that any lane makes its own, forward and
+// backward, whatever the pitch and the launch. 16 bits an element and not 32: a block is 20
+// multiplications of 32 x 32 bits, a quarter of the rate of other instructions.
+
+#include <cmath>
+
+#include "row_util.h"
+
+#pragma clang fp contract(off)
+
+using fsdp::fail;
+using namespace fsdp::dev;
+
+namespace {
+
+template <typename T>
+struct DropArgs {
+  const T* x;
+  const T* res;
+  T* out;
+  const uint64_t* counter;
+  int64_t rows, dim, x_ld, res_ld, out_ld;
+  uint64_t seed, offset;
+  uint32_t below;
+  float scale;
+};
+
+__device__ __forceinline__ u32x4 philox(uint32_t group, uint32_t row, uint64_t offset, uint64_t seed) {
+  u32x4 c{group, row, uint32_t(offset), uint32_t(offset >> 32)};
+  uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t p = uint64_t(0xD2511F53u) * c.x, q = uint64_t(0xCD9E8D57u) * c.z;
+    c = u32x4{uint32_t(q >> 32) ^ c.y ^ k0, uint32_t(q), uint32_t(p >> 32) ^ c.w ^ k1, uint32_t(p)};
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return c;
+}
+
+// `lanes` lanes a row, 256 / lanes rows a workgroup.
+template <typename T, bool RES>
+__global__ __launch_bounds__(256) void k_dropout(DropArgs<T> a, int lanes) {
+  const int64_t row = int64_t(blockIdx.x) * (256 / lanes) + threadIdx.x / lanes;
+  if (row >= a.rows) return;
+  const uint64_t offset = a.offset + (a.counter ? *a.counter : 0);
+  const T* x = a.x + row * a.x_ld;
+  const T* res = RES ? a.res + row * a.res_ld : nullptr;
+  T* out = a.out + row * a.out_ld;
+  for (int64_t c = threadIdx.x % lanes * 8; c < a.dim; c += lanes * 8) {
+    float v[8], r[8];
+    unpack(load_group(x, c, a.dim), v);
+    if (RES) unpack(load_group(res, c, a.dim), r);
+    const u32x4 bits = philox(uint32_t(c / 8), uint32_t(row), offset, a.seed);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t h = e & 1 ? bits[e / 2] >> 16 : bits[e / 2] & 0xFFFFu;
+      v[e] = h >= a.below ? v[e] * a.scale : 0.f;
+      if (RES) v[e] += r[e];
+    }
+    store_group(out, c, a.dim, v);
+  }
+}
+
+template <typename T>
+fsdp_status launch(const fsdp_dropout_args& n, uint32_t below, hipStream_t stream) {
+  DropArgs<T> a{};
+  a.x = static_cast<const T*>(n.x);
+  a.res = static_cast<const T*>(n.residual);
+  a.out = static_cast<T*>(n.out);
+  a.counter = reinterpret_cast<const uint64_t*>(n.counter);
+  a.rows = n.rows;
+  a.dim = n.dim;
+  a.x_ld = n.x_pitch;
+  a.res_ld = n.residual_pitch;
+  a.out_ld = n.out_pitch;
+  a.seed = n.seed;
+  a.offset = n.offset;
+  a.below = below;
+  a.scale = below < 65536 ? float(65536.0 / (65536 - below)) : 0.f;
+  const int lanes = fsdp::lanes_of_row(n.dim), per = 256 / lanes;
+  const unsigned blocks = unsigned((n.rows + per - 1) / per);
+  if (a.res) k_dropout<T, true><<<blocks, 256, 0, stream>>>(a, lanes);
+  else k_dropout<T, false><<<blocks, 256, 0, stream>>>(a, lanes);
+  return fsdp::after_launch("fsdp_dropout");
+}
+
+fsdp_status dropout(const fsdp_dropout_args* n, hipStream_t stream) {
+  if (!n) return fail(FSDP_ERR_INVALID_ARG, "arguments pointer is NULL");
+  if (fsdp_status st = fsdp::check_row_sizes(n->rows, n->dim)) return st;
+  if (fsdp_status st = fsdp::check_row_type(n->dtype)) return st;
+  if (!(n->p >= 0.0 && n->p <= 1.0)) return fail(FSDP_ERR_INVALID_ARG, "p must be in [0, 1]");
+  if (n->rows == 0) return FSDP_OK;
+  const int es = n->dtype == FSDP_F32 ? 4 : 2;
+  std::vector<fsdp::ByteRange> ranges;
+  // out may be x or residual itself: a lane reads its elements before it writes them
+  const bool over_x = n->out == n->x && n->out_pitch == n->x_pitch;
+  const bool over_res = n->residual && n->out == n->residual && n->out_pitch == n->residual_pitch;
+  if (fsdp_status st = fsdp::check_row_arg(n->x, n->x_pitch, n->rows, n->dim, es, false, "x", &ranges)) return st;
+  if (over_x) ranges.pop_back();
+  if (n->residual) {
+    if (fsdp_status st = fsdp::check_row_arg(n->residual, n->residual_pitch, n->rows, n->dim, es, false, "residual",
+                                             &ranges))
+      return st;
+    if (over_res) ranges.pop_back();
+  }
+  if (n->counter) {
+    if (fsdp_status st = fsdp::check_ptr(n->counter, "counter", 8)) return st;
+    ranges.push_back(fsdp::range_of(n->counter, 1, 8, false, "counter"));
+  }
+  if (fsdp_status st = fsdp::check_row_arg(n->out, n->out_pitch, n->rows, n->dim, es, true, "out", &ranges)) return st;
+  if (fsdp_status st = fsdp::check_alias(ranges)) return st;
+  if (fsdp_status st = fsdp::check_no_pending_error("fsdp_dropout")) return st;
+  const uint32_t below = uint32_t(std::nearbyint(n->p * 65536.0));
+  return n->dtype == FSDP_F32 ? launch<float>(*n, below, stream) : launch<uint16_t>(*n, below, stream);
+}
+
+}  // namespace
+
+extern "C" fsdp_status fsdp_dropout(const fsdp_dropout_args* args, hipStream_t stream) {
+  fsdp::clear_error();
+  try {
+    return dropout(args, stream);
+  } catch (const std::bad_alloc&) {
+    return fail(FSDP_ERR_INVALID_ARG, "out of host memory");
+  }
+}
