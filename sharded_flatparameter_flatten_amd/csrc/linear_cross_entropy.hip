@@ -23,6 +23,7 @@
 #include <cmath>
 
 #include "row_util.h"
+#include "tile_util.h"
 
 #pragma clang fp contract(off)
 
@@ -32,10 +33,12 @@ using namespace fsdp::dev;
 namespace {
 
 typedef _Float16 f16;
+typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kT = 64;                // tile
+constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kGatherRows = 32;       // rows a workgroup gathers
 constexpr int64_t kScratch = int64_t(1) << 30;
 constexpr int64_t kMaxProduct = int64_t(1) << 35;   // elements of an operand or a result: grids stay below 2^32 lanes
@@ -43,8 +46,8 @@ constexpr int64_t kMaxProduct = int64_t(1) << 35;   // elements of an operand or
 // What the kernels of one call share.
 struct Loss {
   const uint16_t* x;                  // the caller's hidden
-  const uint16_t* w;
   const int64_t* targets;
+  const uint16_t* wt;                 // weight, the caller's or a copy (wt_dim: dim, or padded by zeros)
   int32_t* count;                     // rows that count
   int32_t* map;                       // their places among the caller's
   int32_t* target;                    // and targets
@@ -55,12 +58,13 @@ struct Loss {
   uint16_t* dx;
   uint16_t* dw;
   uint16_t* g;                        // P, then G: piece rows, g_ld apart
-  f32x2* stats;                       // m and S of a piece's rows, tile by tile
+  f32x2* stats;                       // m and S of a piece's rows, chunk by chunk of the vocabulary
   float* right;                       // the targets' logits of a piece's rows
+  float* part;                        // sums of a split dhidden
   float* acc;                         // dweight's sums of the pieces before
-  int64_t rows, vocab, dim, x_ld, xc_ld, w_ld, dx_ld, dw_ld, g_ld;
+  int64_t rows, vocab, dim, x_ld, xc_ld, wt_ld, wt_dim, dx_ld, dw_ld, g_ld;
   int64_t piece;
-  int32_t tiles;                      // of the vocabulary
+  int32_t chunks, chunk_bits;         // of the vocabulary
   int32_t mean;
   int32_t grads;                      // dx or dw is wanted
   float scale;
@@ -114,119 +118,411 @@ __global__ __launch_bounds__(256) void k_loss_gather(Loss a) {
   }
 }
 
+// weight with rows that the products' loads can take: 16-byte pieces, zeros past dim.
+__global__ __launch_bounds__(256) void k_loss_copy(const uint16_t* w, int64_t w_ld, uint16_t* to, int64_t ld, int64_t dim) {
+  for (int64_t k = threadIdx.x * 8; k < ld - 64; k += 256 * 8)
+    *reinterpret_cast<u32x4*>(to + blockIdx.x * ld + k) = load_group(w + blockIdx.x * w_ld, k, dim).v[0];
+}
+
+// ---------------------------------------------------------------------------
+// the products
+// ---------------------------------------------------------------------------
+
+// C[i][j] = sum over k of A[i][k] B[j][k]:
+//   kLogits  i: vocabulary, j: row, k: dim;         A = weight, B = the gathered rows
+//   kHidden  i: dim, j: row, k: vocabulary;         A = weight^T, B = G
+//   kWeight  i: dim, j: vocabulary, k: row.         A = the gathered rows^T, B = G^T
+// Operands lie in memory as they are: `along` the contracted axis, or `across` it (^T).
 enum Kind { kLogits, kHidden, kWeight };
 
-// C[i][j] = sum over k of A[i][k] B[j][k], 64 x 64 by 4 waves:
-//   kLogits  i: vocabulary, j: row, k: dim;
-//   kHidden  i: dim, j: row, k: vocabulary;
-//   kWeight  i: dim, j: vocabulary, k: row.
-template <Kind KIND>
-__global__ __launch_bounds__(256) void k_loss_product(Loss a, int64_t row0, int tiles_i) {
-  constexpr int kPitch = 72;
-  __shared__ __attribute__((aligned(16))) uint16_t la[kT * kPitch], lb[kT * kPitch];
-  __shared__ float z[kT][kT + 1];
-  const int64_t left = *a.count - row0;
-  const int64_t n = left < 0 ? 0 : left < a.piece ? left : a.piece;
-  const int64_t i0 = int64_t(blockIdx.x) % tiles_i * kT, j0 = int64_t(blockIdx.x) / tiles_i * kT;
-  const int64_t side_i = KIND == kLogits ? a.vocab : a.dim;
-  const int64_t side_j = KIND == kWeight ? a.vocab : n;
-  const int64_t depth = KIND == kLogits ? a.dim : KIND == kHidden ? a.vocab : n;
-  if (j0 >= side_j || (KIND == kWeight && row0 > 0 && n == 0)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wi = wave / 2 * 32, wj = wave % 2 * 32;
-  const uint16_t* xc = a.xc + row0 * a.xc_ld;
-  f32x16 acc;
+// An operand's tile of T rows (i or j) and all of the contracted axis, 64 of it a stage.
+//
+// LDS holds a stage of either layout in 128 T bytes, filled by loads of 1 KB that go straight
+// there, 16 bytes a lane.
+// Along: T rows of 128 bytes; chunk c (16 bytes) of row r sits at c ^ (r / 2 % 8), so that the
+// fragment reads (32 rows, one chunk each) touch each bank once per 16 lanes.
+// Across: 64 rows (of the contracted axis) of 2 T bytes; a fragment is read through the
+// transposing reads of LDS, where 16 lanes take 4 rows x 16 columns and each gets a column's 4
+// values. 32 lanes read 64 bytes of each of 4 rows: the 64-byte blocks of row r are moved by
+// r % 4 (T = 64, whose rows are half as long: by r / 2 % 2), so that they touch each bank once.
+template <bool ACROSS, int T, int PER>
+struct Operand {
+  static constexpr int kRowBytes = ACROSS ? 2 * T : 128, kRows = 1024 / kRowBytes;   // rows a load fills
+  const char* base;
+  int64_t ld;                   // bytes from row to row
+  int64_t bytes;                // from base to the operand's end
+  int32_t v[2], tail;           // a lane's offsets in loads of even and odd number
+  int32_t first;                // this wave's first load
+  int32_t last, columns;        // along: the last stage and the bytes of a row in it
+  static constexpr int32_t kMaxBytes = 0x7FFFFF00;   // a descriptor's, past every offset within a stage
+
+  // PER loads a wave, an even number where T = 256 or the operand is along.
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t pitch, int64_t elements, int wave, int lane) {
+    base = reinterpret_cast<const char*>(p);
+    ld = pitch * 2;
+    bytes = elements * 2;
+    first = wave * PER;
+    const int row = lane / (kRowBytes / 16), c = lane % (kRowBytes / 16);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-  for (int64_t k0 = 0; k0 < depth; k0 += kT) {
-    __syncthreads();
-    for (int q = threadIdx.x; q < kT * kT; q += 256) {
-      const int in = q % kT, out = q / kT;            // `in` runs along memory
-      uint16_t u = 0, v = 0;
-      if (KIND == kLogits) {
-        if (i0 + out < side_i && k0 + in < depth) u = a.w[(i0 + out) * a.w_ld + k0 + in];
-        la[out * kPitch + in] = u;
-      } else if (KIND == kHidden) {
-        if (k0 + out < depth && i0 + in < side_i) u = a.w[(k0 + out) * a.w_ld + i0 + in];
-        la[in * kPitch + out] = u;
-      } else {
-        if (k0 + out < depth && i0 + in < side_i) u = xc[(k0 + out) * a.xc_ld + i0 + in];
-        la[in * kPitch + out] = u;
-      }
-      if (KIND == kWeight) {
-        if (k0 + out < depth && j0 + in < side_j) v = a.g[(k0 + out) * a.g_ld + j0 + in];
-        lb[in * kPitch + out] = v;
-      } else {
-        const uint16_t* b = KIND == kLogits ? xc : a.g;
-        const int64_t ld = KIND == kLogits ? a.xc_ld : a.g_ld;
-        if (j0 + out < side_j && k0 + in < depth) v = b[(j0 + out) * ld + k0 + in];
-        lb[out * kPitch + in] = v;
-      }
+    for (int odd = 0; odd < 2; ++odd) {
+      const int r = odd * kRows + row;
+      const int moved = !ACROSS ? c ^ (r >> 1 & 7) : T == 64 ? c ^ (r >> 1 & 1) << 2 : c ^ (r & 3) << 2;
+      v[odd] = row * int32_t(ld) + moved * 16;
     }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < kT / 16; ++q) {
-      const bf16x8 fa = *reinterpret_cast<const bf16x8*>(la + (wi + (lane & 31)) * kPitch + q * 16 + lane / 32 * 8);
-      const bf16x8 fb = *reinterpret_cast<const bf16x8*>(lb + (wj + (lane & 31)) * kPitch + q * 16 + lane / 32 * 8);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb, acc, 0, 0, 0);
+    last = columns = 0x7FFFFFFF;
+  }
+  // Along, where a row does not fill its last stage: what lies past it is not read.
+  __device__ __forceinline__ void end_at(int64_t elements, int stages) {
+    last = stages - 1;
+    columns = int32_t(elements - int64_t(last) * 64) * 2;
+  }
+  __device__ __forceinline__ void load(int k, int q, char* stage) const {
+    const int64_t at = ACROSS ? int64_t(k) * 64 * ld : int64_t(k) * 128;
+    const int64_t left = bytes - at;
+    const __amdgpu_buffer_rsrc_t r = rsrc(base + at, left < 0 ? 0 : left < kMaxBytes ? left : kMaxBytes);
+    int32_t offset = v[q & 1] + (first + q) * kRows * int32_t(ld);
+    if constexpr (!ACROSS) {
+      // chunks at or past `columns` of the last stage: out of bounds, which loads zeros
+      const int32_t c = (threadIdx.x & 7) ^ ((((q & 1) * 8 + (threadIdx.x & 63) / 8) >> 1) & 7);
+      if (k == last && c * 16 >= columns) offset = kMaxBytes;
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(stage + (first + q) * 1024), 16,
+                                             offset, 0, 0, 0);
+  }
+};
+
+// Where a lane's part of a fragment lies in a stage: 32 rows (i or j) from row0, k from 16 q.
+template <bool ACROSS, int T>
+struct Fragment {
+  int32_t at;
+  __device__ __forceinline__ void init(int row0, int lane) {
+    if (!ACROSS) {
+      at = (row0 + (lane & 31)) * 128 + (((lane >> 5) ^ ((lane >> 1) & 7)) * 16);
+    } else {
+      const int in = lane & 15, k = (lane >> 5) * 8 + (in >> 2);
+      const int moved = T == 64 ? (in >> 3) & 1 : in >> 2;
+      at = k * 2 * T + (((row0 >> 5) ^ moved) << 6) + ((lane >> 4) & 1) * 32 + (in & 3) * 8;
     }
   }
-  // a lane holds i = 8 g + 4 (lane / 32) + e, j = lane % 32 in element 4 g + e
-#pragma unroll
-  for (int e = 0; e < 16; ++e) z[wj + (lane & 31)][wi + e / 4 * 8 + lane / 32 * 4 + e % 4] = acc[e];
-  __syncthreads();
-  if (KIND == kLogits) {
-    const int r = threadIdx.x / 4, c0 = threadIdx.x % 4 * 16;
-    const int64_t row = j0 + r;
-    const int64_t t = row < n ? a.target[row0 + row] - i0 : -1;
-    float m = -INFINITY, s = 0.f;
-    for (int c = c0; c < c0 + 16; ++c)
-      if (i0 + c < side_i && c != t) m = fmaxf(m, z[r][c]);
-    m = fmaxf(m, __shfl_xor(m, 1));
-    m = fmaxf(m, __shfl_xor(m, 2));
-    const float from = m == -INFINITY ? 0.f : m;
-    for (int c = c0; c < c0 + 16; ++c) {
-      const float p = i0 + c < side_i && c != t ? expf(z[r][c] - from) : 0.f;
-      s += p;
-      if (row < n && a.grads) reinterpret_cast<f16*>(a.g)[row * a.g_ld + i0 + c] = f16(p);
-      if (c == t) a.right[row] = z[r][c];
+  // Fragment w (32 w rows on) at k = 16 q of a stage.
+  __device__ __forceinline__ bf16x8 read(const char* stage, int w, int q) const {
+    if constexpr (!ACROSS) {
+      return *reinterpret_cast<const bf16x8*>(stage + (at ^ (q * 32)) + w * 4096);
+    } else {
+      const char* p = stage + (at ^ (w << 6)) + q * 32 * T;
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * T));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
-    s += __shfl_xor(s, 1);
-    s += __shfl_xor(s, 2);
-    if (row < n && c0 == 0) a.stats[row * a.tiles + i0 / kT] = f32x2{m, s};
+  }
+};
+
+// A TI x TJ tile by WI x WJ waves on 32 x 32 x 16 matrix instructions, S stages of 64 in LDS.
+//
+// A stage is worked off in two halves, and the fragments of the next half are read while the
+// matrix instructions of this one run. The stage's one barrier stands between the halves: by then
+// every wave holds the second half's fragments in registers, so stage k + S may be loaded over
+// stage k, and has S - 1 stages' time to arrive.
+template <int TI_, int TJ_, int WI_, int WJ_, int S_>
+struct Shape {
+  static constexpr int TI = TI_, TJ = TJ_, WI = WI_, WJ = WJ_, S = S_;
+  static constexpr int kThreads = 64 * WI * WJ;
+};
+
+template <Kind KIND, typename SH>
+__global__ __launch_bounds__(SH::kThreads) void k_loss_product(Loss a, int64_t row0, int splits) {
+  constexpr int TI = SH::TI, TJ = SH::TJ, WI = SH::WI, WJ = SH::WJ, S = SH::S, kWaves = WI * WJ;
+  constexpr bool kAcrossA = KIND != kLogits, kAcrossB = KIND == kWeight;
+  constexpr int MI = TI / WI / 32, NI = TJ / WJ / 32;
+  constexpr int kPerA = TI / 8 / kWaves, kPerB = TJ / 8 / kWaves, kPer = kPerA + kPerB;
+  static_assert(kPerA % 2 == 0 && kPerB % 2 == 0, "a wave's first load is of an even number");
+  static_assert(S >= 2 && (S & (S - 1)) == 0 && (S - 1) * kPer < 64, "stages");
+  constexpr int kStageA = TI * 128, kStage = (TI + TJ) * 128;
+  constexpr int kRowJ = 2 * TI + 16;              // a result's row in LDS
+  __shared__ __attribute__((aligned(1024))) char lds[std::max(S * kStage, TJ * kRowJ)];
+
+  // The rows that count are known here only: the grid is for all of them.
+  const int64_t left = *a.count - row0;
+  const int n = int(left < 0 ? 0 : left < a.piece ? left : a.piece);
+  const int side_i = int(KIND == kLogits ? a.vocab : a.dim), side_j = KIND == kWeight ? int(a.vocab) : n;
+  const int depth = KIND == kLogits ? int(a.dim) : KIND == kHidden ? int(a.vocab) : n;
+  const int tiles_i = (side_i + TI - 1) / TI, tiles_j = (side_j + TJ - 1) / TJ;
+  if (KIND == kWeight && row0 > 0 && n == 0) return;
+  // Workgroup b runs on XCD b % 8, and tiles that share operands should share its L2: each XCD
+  // takes one run of the tiles, in bands of 8.
+  const int total = tiles_i * tiles_j * splits, run = (total + 7) / 8;
+  int local = int(blockIdx.x / 8);
+  if (local >= run) return;
+  local += int(blockIdx.x % 8) * run;
+  if (local >= total) return;
+  int k0 = 0, kt = (depth + 63) / 64, z = 0, ti, tj;
+  if (KIND == kHidden && splits > 1) {
+    z = divide(local, tiles_i * tiles_j);
+    local -= z * tiles_i * tiles_j;
+    k0 = int(int64_t(kt) * z / splits);
+    kt = int(int64_t(kt) * (z + 1) / splits) - k0;
+  }
+  tile_of(local, tiles_i, tiles_j, ti, tj);
+  const int i0 = ti * TI, j0 = tj * TJ;
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = wave / WJ, wj = wave % WJ;
+  Operand<kAcrossA, TI, kPerA> oa;
+  Operand<kAcrossB, TJ, kPerB> ob;
+  const uint16_t* xc = a.xc + row0 * a.xc_ld;
+  if constexpr (KIND == kLogits) {
+    oa.init(a.wt + int64_t(i0) * a.wt_ld, a.wt_ld, (a.vocab - 1 - i0) * a.wt_ld + a.wt_dim, wave, lane);
+    oa.end_at(a.wt_dim, kt);
+    ob.init(xc + int64_t(j0) * a.xc_ld, a.xc_ld, int64_t(n - j0) * a.xc_ld, wave, lane);
+  } else if constexpr (KIND == kHidden) {
+    oa.init(a.wt + int64_t(k0) * 64 * a.wt_ld + i0, a.wt_ld, (a.vocab - 1 - int64_t(k0) * 64) * a.wt_ld + a.wt_dim - i0, wave, lane);
+    ob.init(a.g + int64_t(j0) * a.g_ld + k0 * 64, a.g_ld, int64_t(n - j0) * a.g_ld - k0 * 64, wave, lane);
+  } else {
+    oa.init(xc + i0, a.xc_ld, int64_t(n) * a.xc_ld - i0, wave, lane);
+    ob.init(a.g + j0, a.g_ld, int64_t(n) * a.g_ld - j0, wave, lane);
+  }
+  auto load_one = [&](int k, int q) {
+    char* to = lds + (k & (S - 1)) * kStage;
+    if (q < kPerA) oa.load(k, q, to);
+    else ob.load(k, q - kPerA, to + kStageA);
+  };
+  auto load = [&](int k) {
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) load_one(k, q);
+  };
+
+  f32x16 acc[MI][NI];
+#pragma unroll
+  for (int x = 0; x < MI; ++x)
+#pragma unroll
+    for (int y = 0; y < NI; ++y)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.f;
+
+  Fragment<kAcrossA, TI> ra;
+  Fragment<kAcrossB, TJ> rb;
+  ra.init(wi * (TI / WI), lane);
+  rb.init(wj * (TJ / WJ), lane);
+  constexpr int kReads = 2 * (MI + NI), kMuls = 2 * MI * NI;
+  constexpr int kAhead = (kReads + kMuls - 1) / kMuls;   // reads before and after each multiply
+  bf16x8 fa[2][2][MI], fb[2][2][NI];              // [half][q][fragment]
+  auto read_one = [&](int k, int h, auto at) {    // the at-th fragment of a half
+    constexpr int q = at.value / (MI + NI), w = at.value % (MI + NI);
+    const char* st = lds + (k & (S - 1)) * kStage;
+    if constexpr (w < NI) {
+      fb[h][q][w] = rb.read(st + kStageA, w, h * 2 + q);
+      __builtin_amdgcn_sched_group_barrier(0x100, kAcrossB ? 2 : 1, 0);
+    } else {
+      fa[h][q][w - NI] = ra.read(st, w - NI, h * 2 + q);
+      __builtin_amdgcn_sched_group_barrier(0x100, kAcrossA ? 2 : 1, 0);
+    }
+  };
+  // The multiplies of half h of stage k, each followed by a share of the next half's fragment
+  // reads and, in the second half, of the loads of stage k + S.
+  auto half = [&](int k, auto of, auto load_next, auto read_next) {
+    static_for<kMuls>([&](auto at) {
+      constexpr int h = of.value, i = at.value;
+      constexpr int r0 = i ? std::min(kReads, i * kAhead + 1) : 0, r1 = std::min(kReads, (i + 1) * kAhead + 1);
+      constexpr int l0 = std::min(kPer, (i * kPer * 2 + kMuls - 1) / kMuls);
+      constexpr int l1 = std::min(kPer, ((i + 1) * kPer * 2 + kMuls - 1) / kMuls);
+      if constexpr (read_next.value)
+        static_for<r1 - r0>([&](auto y) { read_one(h ? k + 1 : k, 1 - h, std::integral_constant<int, r0 + y.value>{}); });
+      constexpr int q = i / (MI * NI), x = i % (MI * NI) / NI, y = i % NI;
+      acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[h][q][x], fb[h][q][y], acc[x][y], 0, 0, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if constexpr (load_next.value)
+        static_for<l1 - l0>([&](auto y) {
+          load_one(k + S, l0 + y.value);
+          __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+        });
+    });
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const std::integral_constant<int, 0> lower;
+  const std::integral_constant<int, 1> upper;
+  using std::false_type;
+  using std::true_type;
+
+  if (kt > 0) {
+    if (kt >= S) {
+#pragma unroll
+      for (int k = 0; k < S; ++k) load(k);
+      wait_loads<(S - 1) * kPer>();
+    } else {
+      for (int k = 0; k < kt; ++k) load(k);
+      wait_loads<0>();
+    }
+    meet();
+    static_for<kReads>([&](auto at) { read_one(0, 0, at); });
+    int k = 0;
+    for (; k + S < kt; ++k) {                     // stages k + 2 to k + S - 1 may be under way
+      half(k, lower, false_type{}, true_type{});
+      wait_loads<(S - 2) * kPer>();
+      meet();
+      half(k, upper, true_type{}, true_type{});
+    }
+    for (; k + 1 < kt; ++k) {
+      half(k, lower, false_type{}, true_type{});
+      wait_loads<0>();
+      meet();
+      half(k, upper, false_type{}, true_type{});
+    }
+    half(k, lower, false_type{}, true_type{});
+    wait_loads<0>();
+    meet();
+    half(k, upper, false_type{}, false_type{});
+  }
+
+  // A lane holds, of column j = jl + 32 y, the rows i = il + 32 x + 8 g + e in acc[x][y][4 g + e].
+  const int il = wi * (TI / WI) + (lane >> 5) * 4, jl = wj * (TJ / WJ) + (lane & 31);
+  auto place = [&](int i, int j) { return reinterpret_cast<u32x2*>(lds + j * kRowJ + i * 2); };
+  constexpr int kCols = TI / 8, kStep = SH::kThreads / kCols, kSteps = TJ / kStep;   // 16 bytes a lane
+  const int row_of = threadIdx.x / kCols, col_of = threadIdx.x % kCols * 8;
+
+  if constexpr (KIND == kLogits) {
+    // What is not in the vocabulary, and the target, leave the sums as -infinity.
+    const int from = i0 + wi * (TI / WI), ends = side_i - i0 - il;
+#pragma unroll
+    for (int y = 0; y < NI; ++y) {
+      const int j = j0 + jl + 32 * y;
+      const int t = j < n ? a.target[row0 + j] - i0 - il : -1;
+      if (__builtin_amdgcn_ballot_w64(t >= 0 && t < TI / WI) != 0 || i0 + TI > side_i) {
+#pragma unroll
+        for (int x = 0; x < MI; ++x)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int at = x * 32 + e / 4 * 8 + e % 4;
+            if (at == t) a.right[j] = acc[x][y][e];
+            if (at == t || at >= ends) acc[x][y][e] = -INFINITY;
+          }
+      }
+      float m = -INFINITY, s = 0.f;
+#pragma unroll
+      for (int x = 0; x < MI; ++x)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[x][y][e]);
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float off = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int x = 0; x < MI; ++x)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          f32x4 p;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = __builtin_amdgcn_exp2f((acc[x][y][4 * g + e] - off) * kLog2e);
+            s += p[e];
+          }
+          if (a.grads) *place(il + x * 32 + g * 8, jl + 32 * y) = __builtin_bit_cast(u32x2, __builtin_convertvector(p, f16x4));
+        }
+      s += __shfl_xor(s, 32);
+      if (lane < 32 && j < n && from < side_i) a.stats[int64_t(from / (TI / WI)) * a.piece + j] = f32x2{m, s};
+    }
+    if (!a.grads) return;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      const int row = row_of + q * kStep;
+      if (j0 + row < n)
+        *reinterpret_cast<u32x4*>(a.g + int64_t(j0 + row) * a.g_ld + i0 + col_of) =
+            *reinterpret_cast<const u32x4*>(lds + row * kRowJ + col_of * 2);
+    }
     return;
   }
-  const float k = factor(a);
-  for (int q = threadIdx.x; q < kT * kT; q += 256) {
-    const int in = q % kT, out = q / kT;
-    if (i0 + in >= side_i || j0 + out >= side_j) continue;
-    float v = z[out][in];
-    if (KIND == kHidden) {
-      a.dx[a.map[row0 + j0 + out] * a.dx_ld + i0 + in] = uint16_t(to_bf16(v * k));
-      continue;
+
+  auto each_four = [&](auto f) {
+#pragma unroll
+    for (int x = 0; x < MI; ++x)
+#pragma unroll
+      for (int y = 0; y < NI; ++y)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          f(f32x4{acc[x][y][4 * g], acc[x][y][4 * g + 1], acc[x][y][4 * g + 2], acc[x][y][4 * g + 3]},
+            (x * NI + y) * 4 + g, il + x * 32 + g * 8, jl + y * 32);
+  };
+  if (KIND == kHidden && splits > 1) {            // sums of a part of the vocabulary
+    float* part = a.part + (int64_t(z) * a.piece + j0) * a.xc_ld + i0;
+    each_four([&](f32x4 v, int, int i, int j) {
+      if (j0 + j < n && i0 + i < a.xc_ld) *reinterpret_cast<f32x4*>(part + j * a.xc_ld + i) = v;
+    });
+    return;
+  }
+  if (KIND == kWeight && a.acc) {                 // the pieces before and after
+    f32x4* sum = reinterpret_cast<f32x4*>(a.acc) + int64_t(ti * tiles_j + tj) * (TI * TJ / 4) + threadIdx.x;
+    if (row0 > 0)
+#pragma unroll
+      for (int x = 0; x < MI; ++x)
+#pragma unroll
+        for (int y = 0; y < NI; ++y)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const f32x4 v = sum[((x * NI + y) * 4 + g) * SH::kThreads];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[x][y][4 * g + e] = v[e] + acc[x][y][4 * g + e];
+          }
+    if (left > a.piece) {
+      each_four([&](f32x4 v, int at, int, int) { sum[at * SH::kThreads] = v; });
+      return;
     }
-    float* sum = a.acc ? a.acc + (j0 + out) * a.xc_ld + i0 + in : nullptr;
-    if (row0 > 0) v += *sum;
-    if (left <= a.piece) a.dw[(j0 + out) * a.dw_ld + i0 + in] = uint16_t(to_bf16(v * k));
-    else *sum = v;
+  }
+  const float k = factor(a);
+  each_four([&](f32x4 v, int, int i, int j) { *place(i, j) = u32x2{pack_bf16(v.x * k, v.y * k), pack_bf16(v.z * k, v.w * k)}; });
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kSteps; ++q) {
+    const int row = row_of + q * kStep;
+    if (j0 + row >= side_j || i0 + col_of >= side_i) continue;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * kRowJ + col_of * 2);
+    uint16_t* o = (KIND == kHidden ? a.dx + a.map[row0 + j0 + row] * a.dx_ld : a.dw + int64_t(j0 + row) * a.dw_ld) + i0 + col_of;
+    if (i0 + col_of + 8 <= side_i) {
+      st_loose<u32x4, 2>(o, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (i0 + col_of + e < side_i) o[e] = uint16_t(v[e / 2] >> (16 * (e & 1)));
+    }
   }
 }
 
-// A row's loss from its tiles' m and S, and its row of G.
+// dhidden from the parts of a split product, added in their order: a row a workgroup.
+__global__ __launch_bounds__(256) void k_loss_join(Loss a, int64_t row0, int splits) {
+  const int64_t r = blockIdx.x;
+  if (row0 + r >= *a.count) return;
+  const float k = factor(a);
+  uint16_t* dx = a.dx + a.map[row0 + r] * a.dx_ld;
+  for (int64_t c = threadIdx.x * 8; c < a.dim; c += 256 * 8) {
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int z = 0; z < splits; ++z) {
+      const f32x4* p = reinterpret_cast<const f32x4*>(a.part + (int64_t(z) * a.piece + r) * a.xc_ld + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { sum[e] += p[0][e]; sum[4 + e] += p[1][e]; }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] *= k;
+    store_group(dx, c, a.dim, sum);
+  }
+}
+
+// A row's loss from its chunks' m and S, and its row of G from P.
 __global__ __launch_bounds__(256) void k_loss_rows(Loss a, int64_t row0) {
   __shared__ float part[8];
   const int64_t r = blockIdx.x;
   if (row0 + r >= *a.count) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const f32x2* stats = a.stats + r * a.tiles;
+  const f32x2* stats = a.stats + r;
   float m = -INFINITY, s = 0.f;
-  for (int t = threadIdx.x; t < a.tiles; t += 256) m = fmaxf(m, stats[t].x);
+  for (int t = threadIdx.x; t < a.chunks; t += 256) m = fmaxf(m, stats[t * a.piece].x);
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
   if (lane == 0) part[wave] = m;
   __syncthreads();
   m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
   const float from = m == -INFINITY ? 0.f : m;
-  for (int t = threadIdx.x; t < a.tiles; t += 256) s += stats[t].y * expf((stats[t].x == -INFINITY ? from : stats[t].x) - from);
+  for (int t = threadIdx.x; t < a.chunks; t += 256) {
+    const f32x2 q = stats[t * a.piece];
+    s += q.y * expf((q.x == -INFINITY ? from : q.x) - from);
+  }
   s = wave_sum(s);
   if (lane == 0) part[4 + wave] = s;
   __syncthreads();
@@ -238,13 +534,22 @@ __global__ __launch_bounds__(256) void k_loss_rows(Loss a, int64_t row0) {
     if (a.losses) a.losses[a.map[row0 + r]] = loss;
   }
   if (!a.grads) return;
-  const int32_t target = a.target[row0 + r];
+  const int target = a.target[row0 + r];
   uint16_t* g = a.g + r * a.g_ld;
-  for (int64_t c = threadIdx.x; c < int64_t(a.tiles) * kT; c += 256) {
-    const float mt = stats[c / kT].x;
+  for (int c = threadIdx.x * 8; c < a.vocab; c += 256 * 8) {
+    const float mt = stats[(c >> a.chunk_bits) * a.piece].x;
     const float f = mt == -INFINITY ? 0.f : expf(mt - right - loss);
-    const float p = float(reinterpret_cast<const f16*>(g)[c]) * f;
-    g[c] = uint16_t(to_bf16(c == target ? expm1f(-loss) : p));
+    const f16x8 p = *reinterpret_cast<const f16x8*>(g + c);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = float(p[e]) * f;
+    if (uint32_t(target - c) < 8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e == target) v[e] = expm1f(-loss);
+    }
+    *reinterpret_cast<u32x4*>(g + c) = u32x4{round_bf16(v[0], v[1]), round_bf16(v[2], v[3]), round_bf16(v[4], v[5]),
+                                             round_bf16(v[6], v[7])};
   }
 }
 
@@ -264,20 +569,51 @@ __global__ __launch_bounds__(1024) void k_loss_mean(Loss a) {
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
+using Large = Shape<256, 256, 2, 4, 2>;
+using Middle = Shape<128, 128, 2, 2, 4>;
+using Small = Shape<64, 64, 2, 2, 4>;
+
+// f(a tile's shape) for a tile of `side`.
+template <typename F>
+void with_shape(int side, F&& f) {
+  if (side == 256) f(Large{});
+  else if (side == 128) f(Middle{});
+  else f(Small{});
+}
+
+int64_t tiles_of(int64_t i, int64_t j, int side) { return ((i + side - 1) / side) * ((j + side - 1) / side); }
+
+// The tile of a product of i x j results: the largest that fills the card's 256 CUs.
+int choose_tile(int64_t i, int64_t j) {
+  for (int side : {256, 128})
+    if (tiles_of(i, j, side) >= 192) return side;
+  return 64;
+}
+
 struct Plan {
-  int64_t piece, pieces, tiles, g_ld, xc_ld;
-  int64_t count, map, target, xc, row_loss, g, stats, right, acc, bytes;   // workspace offsets
+  int64_t piece, pieces, g_ld, xc_ld;
+  int logits, hidden, weight;         // tiles
+  int splits;                         // of dhidden's product over the vocabulary
+  bool copy;
+  int64_t count, map, target, xc, wc, row_loss, g, stats, right, part, acc, bytes;   // workspace offsets
 };
 
 Plan make_plan(const fsdp_linear_cross_entropy_args& n) {
   Plan p{};
   const bool grads = n.dhidden || n.dweight;
-  p.tiles = (n.vocab + kT - 1) / kT;
-  p.g_ld = p.tiles * kT + 64;
+  p.g_ld = round_up(n.vocab, 256) + 64;
   p.xc_ld = round_up(n.dim, 64) + 64;
   p.piece = n.piece > 0 ? n.piece : std::max<int64_t>(256, kScratch / (2 * p.g_ld) / 256 * 256);
   p.piece = std::max<int64_t>(1, std::min(p.piece, n.rows));
   p.pieces = std::max<int64_t>(1, (n.rows + p.piece - 1) / p.piece);
+  // loads of 16 bytes at 32-bit offsets within a tile
+  p.copy = n.rows > 0 && (n.dim % 8 || n.weight_pitch % 8 || n.weight_pitch > (int64_t(1) << 20) ||
+                          reinterpret_cast<uintptr_t>(n.weight) % 16);
+  p.logits = choose_tile(n.vocab, p.piece);
+  p.weight = choose_tile(n.dim, n.vocab);
+  p.hidden = choose_tile(n.dim, p.piece);
+  const int64_t tiles = tiles_of(n.dim, p.piece, p.hidden), stages = (n.vocab + 63) / 64;
+  p.splits = int(std::max<int64_t>(1, std::min<int64_t>({256 / tiles, stages / 8, 16})));
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -289,10 +625,12 @@ Plan make_plan(const fsdp_linear_cross_entropy_args& n) {
   p.target = take(n.rows * 4);
   p.row_loss = take(n.rows * 4);
   p.right = take(p.piece * 4);
-  p.stats = take(p.piece * p.tiles * 8);
+  p.stats = take(p.piece * ((n.vocab + p.logits / 2 - 1) / (p.logits / 2)) * 8);
   p.xc = take(n.rows * p.xc_ld * 2);
+  p.wc = take(p.copy ? n.vocab * p.xc_ld * 2 : 0);
   p.g = take(grads ? p.piece * p.g_ld * 2 : 0);
-  p.acc = take(n.dweight && p.pieces > 1 ? n.vocab * p.xc_ld * 4 : 0);
+  p.part = take(n.dhidden && p.splits > 1 ? p.splits * p.piece * p.xc_ld * 4 : 0);
+  p.acc = take(n.dweight && p.pieces > 1 ? round_up(n.vocab, p.weight) * round_up(n.dim, p.weight) * 4 : 0);
   p.bytes = at;
   return p;
 }
@@ -341,7 +679,9 @@ fsdp_status run(const fsdp_linear_cross_entropy_args* n, hipStream_t stream) {
   char* ws = static_cast<char*>(n->workspace);
   Loss a{};
   a.x = static_cast<const uint16_t*>(n->hidden);
-  a.w = static_cast<const uint16_t*>(n->weight);
+  a.wt = p.copy ? reinterpret_cast<uint16_t*>(ws + p.wc) : static_cast<const uint16_t*>(n->weight);
+  a.wt_ld = p.copy ? p.xc_ld : n->weight_pitch;
+  a.wt_dim = p.copy ? p.xc_ld - 64 : n->dim;
   a.targets = n->targets;
   a.count = reinterpret_cast<int32_t*>(ws + p.count);
   a.map = reinterpret_cast<int32_t*>(ws + p.map);
@@ -355,33 +695,49 @@ fsdp_status run(const fsdp_linear_cross_entropy_args* n, hipStream_t stream) {
   a.g = reinterpret_cast<uint16_t*>(ws + p.g);
   a.stats = reinterpret_cast<f32x2*>(ws + p.stats);
   a.right = reinterpret_cast<float*>(ws + p.right);
+  a.part = reinterpret_cast<float*>(ws + p.part);
   a.acc = n->dweight && p.pieces > 1 ? reinterpret_cast<float*>(ws + p.acc) : nullptr;
   a.rows = n->rows;
   a.vocab = n->vocab;
   a.dim = n->dim;
   a.x_ld = n->hidden_pitch;
   a.xc_ld = p.xc_ld;
-  a.w_ld = n->weight_pitch;
   a.dx_ld = n->dhidden_pitch;
   a.dw_ld = n->dweight_pitch;
   a.g_ld = p.g_ld;
   a.piece = p.piece;
-  a.tiles = int32_t(p.tiles);
   a.mean = n->reduction == FSDP_MEAN;
   a.grads = a.dx || a.dw;
   a.scale = static_cast<float>(n->grad_scale);
 
-  auto tiles_of = [](int64_t side) { return int((side + kT - 1) / kT); };
   k_loss_gather<<<unsigned(std::max<int64_t>(1, (n->rows + kGatherRows - 1) / kGatherRows)), 256, 0, stream>>>(a);
+  if (p.copy)
+    k_loss_copy<<<unsigned(n->vocab), 256, 0, stream>>>(static_cast<const uint16_t*>(n->weight), n->weight_pitch,
+                                                         reinterpret_cast<uint16_t*>(ws + p.wc), p.xc_ld, n->dim);
+  auto blocks = [](int64_t i, int64_t j, int side, int splits) { return unsigned((tiles_of(i, j, side) * splits + 7) / 8 * 8); };
   for (int64_t i = 0; i < p.pieces; ++i) {
-    const int64_t row0 = i * p.piece;
-    const int in_dim = tiles_of(n->dim), in_rows = tiles_of(std::min(p.piece, n->rows - row0)), in_vocab = tiles_of(n->vocab);
-    if (in_rows > 0) {
-      k_loss_product<kLogits><<<in_vocab * in_rows, 256, 0, stream>>>(a, row0, in_vocab);
-      k_loss_rows<<<unsigned(std::min(p.piece, n->rows - row0)), 256, 0, stream>>>(a, row0);
-      if (a.dx) k_loss_product<kHidden><<<in_dim * in_rows, 256, 0, stream>>>(a, row0, in_dim);
+    const int64_t row0 = i * p.piece, rows = std::min(p.piece, n->rows - row0);
+    if (rows > 0) {
+      with_shape(p.logits, [&](auto sh) {
+        using SH = decltype(sh);
+        a.chunk_bits = __builtin_ctz(SH::TI / SH::WI);
+        a.chunks = int32_t((n->vocab - 1) >> a.chunk_bits) + 1;
+        k_loss_product<kLogits, SH><<<blocks(n->vocab, rows, SH::TI, 1), SH::kThreads, 0, stream>>>(a, row0, 1);
+      });
+      k_loss_rows<<<unsigned(rows), 256, 0, stream>>>(a, row0);
+      if (a.dx) {
+        with_shape(p.hidden, [&](auto sh) {
+          using SH = decltype(sh);
+          k_loss_product<kHidden, SH><<<blocks(n->dim, rows, SH::TI, p.splits), SH::kThreads, 0, stream>>>(a, row0, p.splits);
+        });
+        if (p.splits > 1) k_loss_join<<<unsigned(rows), 256, 0, stream>>>(a, row0, p.splits);
+      }
     }
-    if (a.dw) k_loss_product<kWeight><<<in_dim * in_vocab, 256, 0, stream>>>(a, row0, in_dim);
+    if (a.dw)
+      with_shape(p.weight, [&](auto sh) {
+        using SH = decltype(sh);
+        k_loss_product<kWeight, SH><<<blocks(n->dim, n->vocab, SH::TI, 1), SH::kThreads, 0, stream>>>(a, row0, 1);
+      });
     if (fsdp_status st = fsdp::after_launch("fsdp_linear_cross_entropy")) return st;
   }
   k_loss_mean<<<1, 1024, 0, stream>>>(a);

@@ -43,10 +43,8 @@
 #include <cmath>
 #include <initializer_list>
 #include <new>
-#include <type_traits>
-#include <utility>
 
-#include "device_util.h"
+#include "tile_util.h"
 
 #pragma clang fp contract(off)
 
@@ -59,7 +57,6 @@ typedef _Float16 f16;
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr double kScaleX = 4096;      // stored X is X * 2^12, at most
 constexpr double kScaleS = 1024;      // stored S and P are times 2^10, at most
@@ -115,19 +112,6 @@ struct ProdArgs {
 };
 constexpr int kFewMats = 4, kSomeMats = 8;
 
-// t / d for 0 <= t < 2^24, 0 < d and quotients below 2^20 (the estimate is then off by at most one): a few instructions, where a division takes 40 that wait for each other.
-__device__ __forceinline__ int divide(int t, int d) {
-  int q = int(float(t) * __builtin_amdgcn_rcpf(float(d)));
-  q -= q * d > t;
-  q += (q + 1) * d <= t;
-  return __builtin_amdgcn_readfirstlane(q);
-}
-// Tile t of a ti x tj grid, walked in bands of 8 tile rows.
-__device__ __forceinline__ void tile_of(int t, int ti, int tj, int& i, int& j) {
-  const int r0 = divide(t, 8 * tj) * 8, h = ti - r0 < 8 ? ti - r0 : 8, in = t - r0 * tj;
-  j = divide(in, h);
-  i = r0 + in - j * h;
-}
 // Tile t of the lower triangle of n rows, in bands of 4 rows walked by columns:
 // neighbours in this order share rows of both operands.
 __device__ __forceinline__ void tri_of(int t, int n, int& i, int& j) {
@@ -158,26 +142,6 @@ __device__ __forceinline__ int tri_index(int i, int j, int n) {
   const int r = i & ~3, h = n - r < 4 ? n - r : 4, c = j - r;
   if (c < 0) return r * (r + 1) / 2 + j * h + i - r;
   return r * (r + 1) / 2 + r * h + c * h - c * (c - 1) / 2 + i - j;
-}
-
-// At most N global loads of this wave are still under way, and no LDS read.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void meet() {
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-// f(0), ..., f(N - 1) with constants, whatever the compiler's limits on unrolling.
-template <int N, typename F, int... I>
-__device__ __forceinline__ void static_for_each(F&& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
-  static_for_each<N>(f, std::make_integer_sequence<int, N>{});
 }
 
 // T x T tile by WM x WN waves, on 32 x 32 x 16 matrix instructions.
