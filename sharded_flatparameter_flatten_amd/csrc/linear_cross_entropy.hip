@@ -191,6 +191,14 @@ struct Operand {
   }
 };
 
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+// A transposing read. As one through a pointer of its own (restrict) it is not taken to depend on
+// every load into LDS that is under way, each of which the compiler would wait for: what has to
+// have arrived is waited for where the stage changes.
+__device__ __forceinline__ s16x4 read_turned(lds_s16x4* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+}
+
 // Where a lane's part of a fragment lies in a stage: 32 rows (i or j) from row0, k from 16 q.
 template <bool ACROSS, int T>
 struct Fragment {
@@ -210,9 +218,7 @@ struct Fragment {
       return *reinterpret_cast<const bf16x8*>(stage + (at ^ (q * 32)) + w * 4096);
     } else {
       const char* p = stage + (at ^ (w << 6)) + q * 32 * T;
-      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * T));
+      const s16x4 lo = read_turned((lds_s16x4*)p), hi = read_turned((lds_s16x4*)(p + 8 * T));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
