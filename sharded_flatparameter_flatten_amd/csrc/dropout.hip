@@ -46,27 +46,45 @@ __device__ __forceinline__ u32x4 philox(uint32_t group, uint32_t row, uint64_t o
   return c;
 }
 
-// `lanes` lanes a row, 256 / lanes rows a workgroup.
-template <typename T, bool RES>
+// `lanes` lanes a row, 256 / lanes rows a workgroup, two pieces a lane under way; with STREAM a row
+// has whole waves. Bound by HBM: the random bits take no time beside it. An fp32 piece is half of
+// a block's 8 columns: two lanes then make the same block, on twice the bytes a column.
+template <typename T, bool RES, bool STREAM>
 __global__ __launch_bounds__(256) void k_dropout(DropArgs<T> a, int lanes) {
-  const int64_t row = int64_t(blockIdx.x) * (256 / lanes) + threadIdx.x / lanes;
+  constexpr int N = kElems<T>;
+  int in = threadIdx.x / lanes;
+  if (STREAM) in = __builtin_amdgcn_readfirstlane(in);
+  const int64_t row = int64_t(blockIdx.x) * (256 / lanes) + in;
   if (row >= a.rows) return;
   const uint64_t offset = a.offset + (a.counter ? *a.counter : 0);
   const T* x = a.x + row * a.x_ld;
   const T* res = RES ? a.res + row * a.res_ld : nullptr;
   T* out = a.out + row * a.out_ld;
-  for (int64_t c = threadIdx.x % lanes * 8; c < a.dim; c += lanes * 8) {
-    float v[8], r[8];
-    unpack(load_group(x, c, a.dim), v);
-    if (RES) unpack(load_group(res, c, a.dim), r);
-    const u32x4 bits = philox(uint32_t(c / 8), uint32_t(row), offset, a.seed);
+  auto write = [&](u32x4 q, u32x4 p, int64_t c) {
+    if (c >= a.dim) return;
+    float v[N], r[N];
+    unpack(q, v);
+    unpack(p, r);
+    u32x4 bits = philox(uint32_t(c / 8), uint32_t(row), offset, a.seed);
+    if (N == 4 && c & 4) bits = u32x4{bits.z, bits.w, 0, 0};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < N; ++e) {
       const uint32_t h = e & 1 ? bits[e / 2] >> 16 : bits[e / 2] & 0xFFFFu;
       v[e] = h >= a.below ? v[e] * a.scale : 0.f;
       if (RES) v[e] += r[e];
     }
-    store_group(out, c, a.dim, v);
+    store_piece<STREAM>(out, c, a.dim, v);
+  };
+  const int64_t step = lanes * N;
+  for (int64_t c = threadIdx.x % lanes * N; c < a.dim; c += 2 * step) {
+    const u32x4 q0 = load_piece(x, c, a.dim), q1 = load_piece(x, c + step, a.dim);
+    u32x4 p0{}, p1{};
+    if (RES) {
+      p0 = load_piece(res, c, a.dim);
+      p1 = load_piece(res, c + step, a.dim);
+    }
+    write(q0, p0, c);
+    write(q1, p1, c + step);
   }
 }
 
@@ -86,10 +104,13 @@ fsdp_status launch(const fsdp_dropout_args& n, uint32_t below, hipStream_t strea
   a.offset = n.offset;
   a.below = below;
   a.scale = below < 65536 ? float(65536.0 / (65536 - below)) : 0.f;
-  const int lanes = fsdp::lanes_of_row(n.dim), per = 256 / lanes;
+  const int lanes = fsdp::lanes_of_row((n.dim + kElems<T> - 1) / kElems<T>), per = 256 / lanes;
   const unsigned blocks = unsigned((n.rows + per - 1) / per);
-  if (a.res) k_dropout<T, true><<<blocks, 256, 0, stream>>>(a, lanes);
-  else k_dropout<T, false><<<blocks, 256, 0, stream>>>(a, lanes);
+  const bool stream_out = fsdp::streams(n.out, n.out_pitch, n.rows, n.dim, sizeof(T), lanes);
+  if (a.res && stream_out) k_dropout<T, true, true><<<blocks, 256, 0, stream>>>(a, lanes);
+  else if (a.res) k_dropout<T, true, false><<<blocks, 256, 0, stream>>>(a, lanes);
+  else if (stream_out) k_dropout<T, false, true><<<blocks, 256, 0, stream>>>(a, lanes);
+  else k_dropout<T, false, false><<<blocks, 256, 0, stream>>>(a, lanes);
   return fsdp::after_launch("fsdp_dropout");
 }
 

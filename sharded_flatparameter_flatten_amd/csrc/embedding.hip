@@ -21,7 +21,7 @@ using namespace fsdp::dev;
 namespace {
 
 constexpr int kSortWaves = 16;
-constexpr int kMaxRange = 512;       // rows of the vocabulary that a workgroup sorts, at most
+constexpr int kRangeBits = 9, kMaxRange = 1 << kRangeBits;   // rows of the vocabulary that a workgroup sorts, at most
 
 template <typename T>
 struct EmbedArgs {
@@ -32,21 +32,37 @@ struct EmbedArgs {
   float scale;
 };
 
-// `lanes` lanes a row, 256 / lanes rows a workgroup. Bound by HBM.
-template <typename T>
+// This lane's row: `lanes` lanes a row, 256 / lanes rows a workgroup. With whole waves a row it is
+// the same for all of a wave, which the compiler is told.
+template <bool WAVES>
+__device__ __forceinline__ int64_t own_row(int64_t block, int lanes) {
+  int in = threadIdx.x / lanes;
+  if (WAVES) in = __builtin_amdgcn_readfirstlane(in);
+  return block * (256 / lanes) + in;
+}
+
+// Bound by HBM; two pieces a lane under way.
+template <typename T, bool STREAM>
 __global__ __launch_bounds__(256) void k_embedding(EmbedArgs<T> a, int lanes) {
-  const int64_t row = int64_t(blockIdx.x) * (256 / lanes) + threadIdx.x / lanes;
+  constexpr int N = kElems<T>;
+  const int64_t row = own_row<STREAM>(blockIdx.x, lanes);
   if (row >= a.rows) return;
   const int64_t t = a.tokens[row];
   const bool inside = uint64_t(t) < uint64_t(a.vocab);
   const T* w = a.w + (inside ? t : 0) * a.w_ld;
   T* out = a.out + row * a.out_ld;
-  for (int64_t c = threadIdx.x % lanes * 8; c < a.dim; c += lanes * 8) {
-    float v[8];
-    unpack(load_group(w, c, a.dim), v);
+  auto write = [&](u32x4 q, int64_t c) {
+    float v[N];
+    unpack(q, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = inside ? v[e] * a.scale : 0.f;
-    store_group(out, c, a.dim, v);
+    for (int e = 0; e < N; ++e) v[e] = inside ? v[e] * a.scale : 0.f;
+    store_piece<STREAM>(out, c, a.dim, v);
+  };
+  const int64_t step = lanes * N;
+  for (int64_t c = threadIdx.x % lanes * N; c < a.dim; c += 2 * step) {
+    const u32x4 p = load_piece(w, c, a.dim), q = load_piece(w, c + step, a.dim);
+    write(p, c);
+    write(q, c + step);
   }
 }
 
@@ -57,6 +73,11 @@ __global__ __launch_bounds__(256) void k_embedding(EmbedArgs<T> a, int lanes) {
 // workgroup reads all tokens, so it also counts how many fall before its range, which is where
 // its part of `order` begins. Each wave has a stretch of the tokens and counts, then places, its
 // own; between the two the counts of the waves before it become its first places.
+//
+// Bound by latency: 8 loads of 64 tokens are under way at a time, and lanes with the same row
+// find each other by 9 ballots, one for each bit of the row (a loop over the rows that a wave
+// holds took 39 us for 8192 tokens of a text, whose frequent ones all fall to one workgroup).
+constexpr int kTokenLoads = 8;
 __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const int64_t* tokens, int64_t n, int64_t vocab,
                                                                 int64_t padding, int range, int32_t* start,
                                                                 int32_t* order) {
@@ -67,14 +88,25 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const int64_t* t
   const int here = int(vocab - lo < range ? vocab - lo : range);
   const int64_t stretch = (n + 64 * kSortWaves - 1) / (64 * kSortWaves) * 64;
   const int64_t begin = wave * stretch, end = begin + stretch < n ? begin + stretch : n;
+  // A token's row within the range: negative before it and for none, `here` or more after it.
+  auto row_of = [&](int64_t t) {
+    return t < 0 || t >= vocab || t == padding ? INT32_MAX : int32_t(t - lo);
+  };
+  auto each = [&](auto f) {            // f(position, row) for 64 tokens at a time
+    for (int64_t i0 = begin; i0 < end; i0 += 64 * kTokenLoads) {
+      int64_t t[kTokenLoads];
+#pragma unroll
+      for (int u = 0; u < kTokenLoads; ++u) t[u] = i0 + u * 64 + lane < end ? tokens[i0 + u * 64 + lane] : -1;
+#pragma unroll
+      for (int u = 0; u < kTokenLoads; ++u) f(int32_t(i0 + u * 64 + lane), row_of(t[u]));
+    }
+  };
   for (int v = lane; v < here; v += 64) at[wave][v] = 0;
   int32_t less = 0;
-  for (int64_t i = begin + lane; i < end; i += 64) {
-    const int64_t t = tokens[i];
-    if (t < 0 || t >= vocab || t == padding) continue;
-    less += t < lo;
-    if (t >= lo && t < lo + here) atomicAdd(&at[wave][t - lo], 1);
-  }
+  each([&](int32_t, int32_t row) {
+    less += row < 0;
+    if (row >= 0 && row < here) atomicAdd(&at[wave][row], 1);
+  });
   less = wave_sum(less);
   if (lane == 0) before[wave] = less;
   __syncthreads();
@@ -114,57 +146,155 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const int64_t* t
     }
   }
   __syncthreads();
-  for (int64_t i0 = begin; i0 < end; i0 += 64) {
-    const int64_t i = i0 + lane;
-    const int64_t t = i < end ? tokens[i] : -1;
-    const bool mine = t >= lo && t < lo + here && t != padding;
-    uint64_t left = __builtin_amdgcn_ballot_w64(mine);
-    while (left) {                    // one token of the range at a time, all lanes that have it
-      const int first = __builtin_ctzll(left);
-      const int row = __builtin_amdgcn_readlane(int(t - lo), first);
-      const uint64_t same = __builtin_amdgcn_ballot_w64(mine && t - lo == row);
-      const int32_t place = at[wave][row];
-      if (same >> lane & 1) order[place + __builtin_popcountll(same & ((uint64_t(1) << lane) - 1))] = int32_t(i);
-      if (lane == first) at[wave][row] = place + __builtin_popcountll(same);
-      left &= ~same;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the next round reads what one lane wrote
+  each([&](int32_t i, int32_t row) {
+    const bool mine = row >= 0 && row < here;
+    uint64_t same = __builtin_amdgcn_ballot_w64(mine);
+    if (!same) return;
+#pragma unroll
+    for (int b = 0; b < kRangeBits; ++b) {
+      const uint64_t set = __builtin_amdgcn_ballot_w64(row >> b & 1);
+      same &= row >> b & 1 ? set : ~set;
     }
-  }
+    const int earlier = __builtin_popcountll(same & ((uint64_t(1) << lane) - 1));
+    int32_t place = 0;
+    if (mine) {
+      place = at[wave][row];
+      order[place + earlier] = i;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // every lane has read
+    if (mine && earlier == 0) at[wave][row] = place + __builtin_popcountll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the next round reads what one lane wrote
+  });
 }
+
+// Lists of more than kWindow tokens are summed in parts: those within each window of kWindow
+// places of `order`, for which a workgroup (and 256 pieces of columns) is responsible, and which at most
+// two long lists reach into: the one at its first place (its part goes to row 2 w of `part`) and
+// one that begins inside (row 2 w + 1). At most one long list begins in a window, so a second
+// launch gives each window the joining of that one, in the order of its parts.
+//
+// With 32 a text's 8192 tokens of 4096 columns take ... us; without parts the rows of the few
+// most frequent tokens, summed one after the other, took 925 us.
+constexpr int kWindow = 32;
 
 template <typename T>
 struct EmbedBackArgs {
+  const int64_t* tokens;
   const T* dy;
   T* dw;
   const int32_t* start;
   const int32_t* order;
-  int64_t vocab, dim, dy_ld, dw_ld;
+  float* part;
+  int64_t vocab, dim, dy_ld, dw_ld, part_ld;
+  int32_t windows;
   float scale;
 };
 
-// `lanes` lanes a row of the vocabulary, 256 / lanes rows a workgroup. Bound by HBM: most rows
-// are absent, and zeros are written.
-template <typename T, bool ADD>
-__global__ __launch_bounds__(256) void k_embed_back(EmbedBackArgs<T> a, int lanes) {
-  const int64_t v = int64_t(blockIdx.x) * (256 / lanes) + threadIdx.x / lanes;
+// sum of dy's rows order[begin] to order[end - 1], columns from c on; 4 rows under way
+template <typename T>
+__device__ __forceinline__ void sum_rows(const EmbedBackArgs<T>& a, int32_t begin, int32_t end, int64_t c,
+                                         float (&sum)[kElems<T>]) {
+  constexpr int N = kElems<T>;
+#pragma unroll
+  for (int e = 0; e < N; ++e) sum[e] = 0.f;
+  auto add = [&](u32x4 q) {
+    float x[N];
+    unpack(q, x);
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum[e] += x[e];
+  };
+  int32_t i = begin;
+  for (; i + 4 <= end; i += 4) {
+    u32x4 q[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) q[u] = load_piece(a.dy + a.order[i + u] * a.dy_ld, c, a.dim);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) add(q[u]);
+  }
+  for (; i < end; ++i) add(load_piece(a.dy + a.order[i] * a.dy_ld, c, a.dim));
+}
+
+template <bool ADD, bool STREAM, typename T>
+__device__ __forceinline__ void write_row(const EmbedBackArgs<T>& a, int64_t v, int64_t c, float (&sum)[kElems<T>]) {
+  constexpr int N = kElems<T>;
+  T* dw = a.dw + v * a.dw_ld;
+  float old[N] = {};
+  if (ADD) unpack(load_piece(dw, c, a.dim), old);
+#pragma unroll
+  for (int e = 0; e < N; ++e) sum[e] = ADD ? old[e] + sum[e] * a.scale : sum[e] * a.scale;
+  store_piece<STREAM>(dw, c, a.dim, sum);
+}
+
+template <int N>
+__device__ __forceinline__ void keep(float* p, const float (&x)[N]) {
+#pragma unroll
+  for (int h = 0; h < N; h += 4) *reinterpret_cast<f32x4*>(p + h) = f32x4{x[h], x[h + 1], x[h + 2], x[h + 3]};
+}
+
+// The windows' parts first (`parts` workgroups of 256 lanes), then the short lists: `lanes` lanes
+// a list, 256 / lanes lists a workgroup. Those are the rows of the vocabulary, absent ones
+// (written as zeros) included, or with ADD, which leaves absent rows alone, the places of `order`
+// where a list begins. Bound by HBM: most rows are absent.
+template <typename T, bool ADD, bool STREAM>
+__global__ __launch_bounds__(256) void k_embed_back(EmbedBackArgs<T> a, int lanes, int parts) {
+  constexpr int N = kElems<T>;
+  const int32_t all = a.start[a.vocab];
+  if (int(blockIdx.x) < parts) {
+    const int w = blockIdx.x % a.windows;
+    const int64_t c = (int64_t(blockIdx.x / a.windows) * 256 + threadIdx.x) * N;
+    const int32_t first = w * kWindow, last = (first + kWindow < all ? first + kWindow : all) - 1;
+    if (first > last) return;
+    const int64_t v = a.tokens[a.order[first]], u = a.tokens[a.order[last]];
+    float sum[N];
+    if (a.start[v + 1] - a.start[v] > kWindow && c < a.dim) {
+      const int32_t end = a.start[v + 1];
+      sum_rows(a, first, end <= last ? end : last + 1, c, sum);
+      keep(a.part + int64_t(2 * w) * a.part_ld + c, sum);
+    }
+    if (u != v && a.start[u + 1] - a.start[u] > kWindow && c < a.dim) {
+      sum_rows(a, a.start[u], last + 1, c, sum);
+      keep(a.part + int64_t(2 * w + 1) * a.part_ld + c, sum);
+    }
+    return;
+  }
+  int64_t v = own_row<STREAM>(blockIdx.x - parts, lanes);
+  if (ADD) {
+    if (v >= all) return;
+    const int64_t place = v;
+    v = a.tokens[a.order[place]];
+    if (a.start[v] != place) return;
+  }
   if (v >= a.vocab) return;
   const int32_t begin = a.start[v], end = a.start[v + 1];
-  if (ADD && begin == end) return;
-  T* dw = a.dw + v * a.dw_ld;
-  for (int64_t c = threadIdx.x % lanes * 8; c < a.dim; c += lanes * 8) {
-    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int32_t i = begin; i < end; ++i) {
-      float x[8];
-      unpack(load_group(a.dy + int64_t(a.order[i]) * a.dy_ld, c, a.dim), x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += x[e];
-    }
-    float old[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (ADD) unpack(load_group(dw, c, a.dim), old);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] = ADD ? old[e] + sum[e] * a.scale : sum[e] * a.scale;
-    store_group(dw, c, a.dim, sum);
+  if (end - begin > kWindow) return;
+  for (int64_t c = threadIdx.x % lanes * N; c < a.dim; c += lanes * N) {
+    float sum[N];
+    sum_rows(a, begin, end, c, sum);
+    write_row<ADD, STREAM>(a, v, c, sum);
   }
+}
+
+template <typename T, bool ADD>
+__global__ __launch_bounds__(256) void k_embed_join(EmbedBackArgs<T> a) {
+  constexpr int N = kElems<T>;
+  const int w = blockIdx.x % a.windows;
+  const int64_t c = (int64_t(blockIdx.x / a.windows) * 256 + threadIdx.x) * N;
+  const int32_t all = a.start[a.vocab], first = w * kWindow, last = (first + kWindow < all ? first + kWindow : all) - 1;
+  if (first > last || c >= a.dim) return;
+  const int64_t v = a.tokens[a.order[last]];
+  const int32_t begin = a.start[v], end = a.start[v + 1];
+  if (begin < first || end - begin <= kWindow) return;       // begins elsewhere, or is no long list
+  float sum[N] = {};
+  for (int x = w; x <= (end - 1) / kWindow; ++x) {
+    const float* p = a.part + int64_t(2 * x + (x == w && begin > first)) * a.part_ld + c;
+#pragma unroll
+    for (int h = 0; h < N; h += 4) {
+      const f32x4 q = *reinterpret_cast<const f32x4*>(p + h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[h + e] += q[e];
+    }
+  }
+  write_row<ADD, false>(a, v, c, sum);
 }
 
 int range_of_rows(int64_t vocab) {
@@ -172,12 +302,21 @@ int range_of_rows(int64_t vocab) {
   return int(range < kMaxRange ? range : kMaxRange);
 }
 
-int64_t back_workspace(int64_t rows, int64_t vocab) { return ((vocab + 1 + rows) * 4 + 15) / 16 * 16; }
+int64_t windows_of(int64_t rows) { return rows > kWindow ? (rows + kWindow - 1) / kWindow : 0; }
+int64_t lists_bytes(int64_t rows, int64_t vocab) { return ((vocab + 1 + rows) * 4 + 15) / 16 * 16; }
+int64_t part_pitch(int64_t dim) { return (dim + 7) / 8 * 8; }
+
+int64_t back_workspace(int64_t rows, int64_t vocab, int64_t dim) {
+  return lists_bytes(rows, vocab) + 2 * windows_of(rows) * part_pitch(dim) * 4;
+}
 
 fsdp_status check_sizes(int64_t rows, int64_t vocab, int64_t dim) {
   if (fsdp_status st = fsdp::check_row_sizes(rows, dim)) return st;
   if (vocab < 1 || vocab >= (int64_t(1) << 22))
     return fail(FSDP_ERR_RANGE, "vocab must be in [1, 2^22) (got %lld)", static_cast<long long>(vocab));
+  if (rows * dim > (int64_t(1) << 38))         // the grid's lanes stay below 2^32
+    return fail(FSDP_ERR_RANGE, "rows %lld of dim %lld: over 2^38 elements", static_cast<long long>(rows),
+                static_cast<long long>(dim));
   return FSDP_OK;
 }
 
@@ -198,8 +337,10 @@ fsdp_status launch(const fsdp_embedding_args& n, hipStream_t stream) {
   a.w_ld = n.weight_pitch;
   a.out_ld = n.out_pitch;
   a.scale = static_cast<float>(n.scale);
-  const int lanes = fsdp::lanes_of_row(n.dim), per = 256 / lanes;
-  k_embedding<T><<<unsigned((n.rows + per - 1) / per), 256, 0, stream>>>(a, lanes);
+  const int lanes = fsdp::lanes_of_row((n.dim + kElems<T> - 1) / kElems<T>), per = 256 / lanes;
+  const unsigned blocks = unsigned((n.rows + per - 1) / per);
+  if (fsdp::streams(n.out, n.out_pitch, n.rows, n.dim, sizeof(T), lanes)) k_embedding<T, true><<<blocks, 256, 0, stream>>>(a, lanes);
+  else k_embedding<T, false><<<blocks, 256, 0, stream>>>(a, lanes);
   return fsdp::after_launch("fsdp_embedding");
 }
 
@@ -229,19 +370,31 @@ fsdp_status launch_back(const fsdp_embedding_backward_args& n, hipStream_t strea
       n.tokens, n.rows, n.vocab, n.padding_idx, range, start, order);
   if (fsdp_status st = fsdp::after_launch("fsdp_embedding_backward")) return st;
   EmbedBackArgs<T> a{};
+  a.tokens = n.tokens;
   a.dy = static_cast<const T*>(n.dy);
   a.dw = static_cast<T*>(n.dweight);
   a.start = start;
   a.order = order;
+  a.part = reinterpret_cast<float*>(static_cast<char*>(n.workspace) + lists_bytes(n.rows, n.vocab));
   a.vocab = n.vocab;
   a.dim = n.dim;
   a.dy_ld = n.dy_pitch;
   a.dw_ld = n.dweight_pitch;
+  a.part_ld = part_pitch(n.dim);
+  a.windows = int32_t(windows_of(n.rows));
   a.scale = static_cast<float>(n.scale);
-  const int lanes = fsdp::lanes_of_row(n.dim), per = 256 / lanes;
-  const unsigned blocks = unsigned((n.vocab + per - 1) / per);
-  if (n.accumulate) k_embed_back<T, true><<<blocks, 256, 0, stream>>>(a, lanes);
-  else k_embed_back<T, false><<<blocks, 256, 0, stream>>>(a, lanes);
+  const int64_t pieces = (n.dim + kElems<T> - 1) / kElems<T>;
+  const int lanes = fsdp::lanes_of_row(pieces), per = 256 / lanes;
+  const int parts = a.windows * int((pieces + 255) / 256);
+  const unsigned blocks = parts + unsigned(((n.accumulate ? n.rows : n.vocab) + per - 1) / per);
+  if (n.accumulate) k_embed_back<T, true, false><<<blocks, 256, 0, stream>>>(a, lanes, parts);
+  else if (fsdp::streams(n.dweight, n.dweight_pitch, n.vocab, n.dim, sizeof(T), lanes))
+    k_embed_back<T, false, true><<<blocks, 256, 0, stream>>>(a, lanes, parts);
+  else k_embed_back<T, false, false><<<blocks, 256, 0, stream>>>(a, lanes, parts);
+  if (fsdp_status st = fsdp::after_launch("fsdp_embedding_backward")) return st;
+  if (!parts) return FSDP_OK;
+  if (n.accumulate) k_embed_join<T, true><<<parts, 256, 0, stream>>>(a);
+  else k_embed_join<T, false><<<parts, 256, 0, stream>>>(a);
   return fsdp::after_launch("fsdp_embedding_backward");
 }
 
@@ -261,7 +414,7 @@ fsdp_status backward(const fsdp_embedding_backward_args* n, hipStream_t stream) 
   }
   if (fsdp_status st = fsdp::check_row_arg(n->dweight, n->dweight_pitch, n->vocab, n->dim, es, true, "dweight", &ranges))
     return st;
-  if (fsdp_status st = fsdp::check_workspace(n->workspace, n->workspace_bytes, back_workspace(n->rows, n->vocab), 16,
+  if (fsdp_status st = fsdp::check_workspace(n->workspace, n->workspace_bytes, back_workspace(n->rows, n->vocab, n->dim), 16,
                                              &ranges))
     return st;
   if (fsdp_status st = fsdp::check_alias(ranges)) return st;
@@ -286,7 +439,7 @@ fsdp_status fsdp_embedding_backward_workspace(int64_t rows, int64_t vocab, int64
   fsdp::clear_error();
   if (!bytes) return fail(FSDP_ERR_INVALID_ARG, "bytes pointer is NULL");
   if (fsdp_status st = check_sizes(rows, vocab, dim)) return st;
-  *bytes = back_workspace(rows, vocab);
+  *bytes = back_workspace(rows, vocab, dim);
   return FSDP_OK;
 }
 

@@ -39,7 +39,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kGatherRows = 32;       // rows a workgroup gathers
+constexpr int kGatherRows = 8;        // rows a workgroup gathers
 constexpr int64_t kScratch = int64_t(1) << 30;
 constexpr int64_t kMaxProduct = int64_t(1) << 35;   // elements of an operand or a result: grids stay below 2^32 lanes
 
@@ -84,7 +84,13 @@ __global__ __launch_bounds__(256) void k_loss_gather(Loss a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row0 = int64_t(blockIdx.x) * kGatherRows;
   int32_t before = 0;
-  for (int64_t i = threadIdx.x; i < row0; i += 256) before += counts(a, a.targets[i]);
+  for (int64_t i = threadIdx.x; i < row0; i += 4 * 256) {
+    int64_t t[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) t[u] = i + u * 256 < row0 ? a.targets[i + u * 256] : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) before += counts(a, t[u]);
+  }
   before = wave_sum(before);
   if (lane == 0) part[wave] = before;
   __syncthreads();
@@ -110,18 +116,27 @@ __global__ __launch_bounds__(256) void k_loss_gather(Loss a) {
       if (a.losses && lane == 0) a.losses[row] = 0.f;
       if (!a.dx) continue;
       const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int64_t k = lane * 8; k < a.dim; k += 512) store_group(a.dx + row * a.dx_ld, k, a.dim, zero);
+      for (int64_t k = lane * 8; k < a.dim; k += 512) store_piece(a.dx + row * a.dx_ld, k, a.dim, zero);
       continue;
     }
-    for (int64_t k = lane * 8; k < a.xc_ld - 64; k += 512)
-      *reinterpret_cast<u32x4*>(a.xc + c * a.xc_ld + k) = load_group(a.x + row * a.x_ld, k, a.dim).v[0];
+    const uint16_t* x = a.x + row * a.x_ld;
+    uint16_t* xc = a.xc + c * a.xc_ld;
+    const int64_t end = a.xc_ld - 64;
+    for (int64_t k = lane * 8; k < end; k += 4 * 512) {
+      u32x4 q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) q[u] = load_piece(x, k + u * 512, a.dim);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (k + u * 512 < end) *reinterpret_cast<u32x4*>(xc + k + u * 512) = q[u];
+    }
   }
 }
 
 // weight with rows that the products' loads can take: 16-byte pieces, zeros past dim.
 __global__ __launch_bounds__(256) void k_loss_copy(const uint16_t* w, int64_t w_ld, uint16_t* to, int64_t ld, int64_t dim) {
   for (int64_t k = threadIdx.x * 8; k < ld - 64; k += 256 * 8)
-    *reinterpret_cast<u32x4*>(to + blockIdx.x * ld + k) = load_group(w + blockIdx.x * w_ld, k, dim).v[0];
+    *reinterpret_cast<u32x4*>(to + blockIdx.x * ld + k) = load_piece(w + blockIdx.x * w_ld, k, dim);
 }
 
 // ---------------------------------------------------------------------------
@@ -506,7 +521,7 @@ __global__ __launch_bounds__(256) void k_loss_join(Loss a, int64_t row0, int spl
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] *= k;
-    store_group(dx, c, a.dim, sum);
+    store_piece(dx, c, a.dim, sum);
   }
 }
 

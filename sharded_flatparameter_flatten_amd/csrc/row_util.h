@@ -1,4 +1,4 @@
-// Rows of bf16 or fp32 elements in groups of 8 columns, and the checks of row arguments:
+// Rows of bf16 or fp32 elements in pieces of 16 bytes, and the checks of row arguments:
 // what the embedding, the dropout and the head's loss share.
 #pragma once
 
@@ -20,40 +20,47 @@ __device__ __forceinline__ uint32_t round_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
-// Columns c to c + 7 of a row as they lie in memory, from element alignment; elements at or
-// past `dim` are zeros.
+// 16 bytes of a row, kElems<T> consecutive elements: what a lane holds. (With 32 bytes of fp32 a
+// lane the stores that stream past L2 would write half sectors.)
 template <typename T>
-struct Group {
-  u32x4 v[sizeof(T) / 2];
-};
-__device__ __forceinline__ Group<uint16_t> load_group(const uint16_t* p, int64_t c, int64_t dim) {
-  if (c + 8 <= dim) return {{ld_loose<u32x4, 2>(p + c)}};
-  Group<uint16_t> r{};
+constexpr int kElems = 16 / int(sizeof(T));
+
+// From element alignment; elements at or past `dim` are zeros.
+__device__ __forceinline__ u32x4 load_piece(const uint16_t* p, int64_t c, int64_t dim) {
+  if (c + 8 <= dim) return ld_loose<u32x4, 2>(p + c);
+  u32x4 r{};
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    if (c + e < dim) r.v[0][e / 2] |= uint32_t(p[c + e]) << (16 * (e & 1));
+    if (c + e < dim) r[e / 2] |= uint32_t(p[c + e]) << (16 * (e & 1));
   return r;
 }
-__device__ __forceinline__ Group<float> load_group(const float* p, int64_t c, int64_t dim) {
-  if (c + 8 <= dim) return {{ld_loose<u32x4, 4>(p + c), ld_loose<u32x4, 4>(p + c + 4)}};
-  Group<float> r{};
+__device__ __forceinline__ u32x4 load_piece(const float* p, int64_t c, int64_t dim) {
+  if (c + 4 <= dim) return ld_loose<u32x4, 4>(p + c);
+  u32x4 r{};
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (c + e < dim) r.v[e / 4][e % 4] = __float_as_uint(p[c + e]);
+  for (int e = 0; e < 4; ++e)
+    if (c + e < dim) r[e] = __float_as_uint(p[c + e]);
   return r;
 }
-__device__ __forceinline__ void unpack(const Group<uint16_t>& r, float (&x)[8]) {
+__device__ __forceinline__ void unpack(u32x4 r, float (&x)[8]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) { x[2 * e] = lo_bf16(r.v[0][e]); x[2 * e + 1] = hi_bf16(r.v[0][e]); }
+  for (int e = 0; e < 4; ++e) { x[2 * e] = lo_bf16(r[e]); x[2 * e + 1] = hi_bf16(r[e]); }
 }
-__device__ __forceinline__ void unpack(const Group<float>& r, float (&x)[8]) {
+__device__ __forceinline__ void unpack(u32x4 r, float (&x)[4]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(r.v[e / 4][e % 4]);
+  for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(r[e]);
 }
 
-// 8 values to columns c to c + 7, each rounded once; elements at or past `dim` are left alone.
+// STREAM: past L2, for a row that the whole wave is in, aligned to 16 bytes.
+template <bool STREAM, typename T>
+__device__ __forceinline__ void store_16(T* p, int64_t c, int64_t dim, u32x4 q) {
+  if constexpr (STREAM) st_stream(rsrc(p, dim * int(sizeof(T))), int(c) * int(sizeof(T)), q);
+  else st_loose<u32x4, sizeof(T)>(p + c, q);
+}
+// Values to the columns from c on, each rounded once; elements at or past `dim` are left alone.
 // Every NaN of a bf16 row is 0x7FC0.
-__device__ __forceinline__ void store_group(uint16_t* p, int64_t c, int64_t dim, const float (&x)[8]) {
+template <bool STREAM = false>
+__device__ __forceinline__ void store_piece(uint16_t* p, int64_t c, int64_t dim, const float (&x)[8]) {
   if (c + 8 <= dim) {
     bool nan = false;
     u32x4 q;
@@ -66,33 +73,40 @@ __device__ __forceinline__ void store_group(uint16_t* p, int64_t c, int64_t dim,
 #pragma unroll
       for (int e = 0; e < 4; ++e) q[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
     }
-    st_loose<u32x4, 2>(p + c, q);
+    store_16<STREAM>(p, c, dim, q);
     return;
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (c + e < dim) p[c + e] = uint16_t(to_bf16(x[e]));
 }
-__device__ __forceinline__ void store_group(float* p, int64_t c, int64_t dim, const float (&x)[8]) {
-  if (c + 8 <= dim) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      st_loose<f32x4, 4>(p + c + 4 * h, f32x4{x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]});
+template <bool STREAM = false>
+__device__ __forceinline__ void store_piece(float* p, int64_t c, int64_t dim, const float (&x)[4]) {
+  if (c + 4 <= dim) {
+    store_16<STREAM>(p, c, dim, u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])});
     return;
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
+  for (int e = 0; e < 4; ++e)
     if (c + e < dim) p[c + e] = x[e];
 }
 
 }  // namespace dev
 
-// Lanes that share a row of `dim` elements in a workgroup of 256, a power of 2: as many as the
-// row has groups of 8, so that short rows share a wave.
-inline int lanes_of_row(int64_t dim) {
+// Lanes that share a row of `pieces` pieces in a workgroup of 256, a power of 2: as many as the
+// row has pieces, so that short rows share a wave.
+inline int lanes_of_row(int64_t pieces) {
   int lanes = 1;
-  while (lanes < 256 && int64_t(lanes) * 8 < dim) lanes *= 2;
+  while (lanes < 256 && lanes < pieces) lanes *= 2;
   return lanes;
+}
+
+// Whether `rows` rows of output are streamed past L2: they are far larger than it, rows take
+// whole waves, and every piece is aligned.
+constexpr int64_t kStreamBytes = int64_t(32) << 20;
+inline bool streams(const void* out, int64_t ld, int64_t rows, int64_t dim, int elem, int lanes) {
+  return rows * dim * elem >= kStreamBytes && lanes >= 64 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
+         ld * elem % 16 == 0 && dim * elem < (int64_t(1) << 31);
 }
 
 // A rows x dim argument with a row pitch: checked, its byte range recorded.
