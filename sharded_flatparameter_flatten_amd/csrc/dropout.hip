@@ -18,6 +18,7 @@
 
 using fsdp::fail;
 using namespace fsdp::dev;
+using fsdp::Rows, fsdp::kShared, fsdp::kWhole, fsdp::kStreamed;
 
 namespace {
 
@@ -46,46 +47,33 @@ __device__ __forceinline__ u32x4 philox(uint32_t group, uint32_t row, uint64_t o
   return c;
 }
 
-// `lanes` lanes a row, 256 / lanes rows a workgroup, two pieces a lane under way; with STREAM a row
-// has whole waves. Bound by HBM: the random bits take no time beside it. An fp32 piece is half of
-// a block's 8 columns: two lanes then make the same block, on twice the bytes a column.
-template <typename T, bool RES, bool STREAM>
-__global__ __launch_bounds__(256) void k_dropout(DropArgs<T> a, int lanes) {
+// One piece a lane: with loops over a row, two or four pieces a lane, every size was slower (8192 rows
+// of 4096 with a residual: 35 us, 37 and 38). An fp32 piece is half of a block's 8 columns: two lanes
+// then make the same block, on twice the bytes a column.
+template <typename T, bool RES, Rows HOW>
+__global__ __launch_bounds__(256) void k_dropout(DropArgs<T> a, fsdp::RowGrid g) {
   constexpr int N = kElems<T>;
-  int in = threadIdx.x / lanes;
-  if (STREAM) in = __builtin_amdgcn_readfirstlane(in);
-  const int64_t row = int64_t(blockIdx.x) * (256 / lanes) + in;
-  if (row >= a.rows) return;
+  const int dim = int(a.dim);
+  int64_t row;
+  int c;
+  own_piece<T, HOW>(g, blockIdx.x, row, c);
+  if (row >= a.rows || c >= dim) return;
+  const u32x4 q = load_piece(a.x + row * a.x_ld, c, dim);
+  u32x4 p{};
+  if (RES) p = load_piece(a.res + row * a.res_ld, c, dim);
   const uint64_t offset = a.offset + (a.counter ? *a.counter : 0);
-  const T* x = a.x + row * a.x_ld;
-  const T* res = RES ? a.res + row * a.res_ld : nullptr;
-  T* out = a.out + row * a.out_ld;
-  auto write = [&](u32x4 q, u32x4 p, int64_t c) {
-    if (c >= a.dim) return;
-    float v[N], r[N];
-    unpack(q, v);
-    unpack(p, r);
-    u32x4 bits = philox(uint32_t(c / 8), uint32_t(row), offset, a.seed);
-    if (N == 4 && c & 4) bits = u32x4{bits.z, bits.w, 0, 0};
+  u32x4 random = philox(uint32_t(c) / 8, uint32_t(row), offset, a.seed);
+  if (N == 4 && c & 4) random = u32x4{random.z, random.w, 0, 0};
+  float v[N], r[N];
+  unpack(q, v);
+  unpack(p, r);
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const uint32_t h = e & 1 ? bits[e / 2] >> 16 : bits[e / 2] & 0xFFFFu;
-      v[e] = h >= a.below ? v[e] * a.scale : 0.f;
-      if (RES) v[e] += r[e];
-    }
-    store_piece<STREAM>(out, c, a.dim, v);
-  };
-  const int64_t step = lanes * N;
-  for (int64_t c = threadIdx.x % lanes * N; c < a.dim; c += 2 * step) {
-    const u32x4 q0 = load_piece(x, c, a.dim), q1 = load_piece(x, c + step, a.dim);
-    u32x4 p0{}, p1{};
-    if (RES) {
-      p0 = load_piece(res, c, a.dim);
-      p1 = load_piece(res, c + step, a.dim);
-    }
-    write(q0, p0, c);
-    write(q1, p1, c + step);
+  for (int e = 0; e < N; ++e) {
+    const uint32_t h = e & 1 ? random[e / 2] >> 16 : random[e / 2] & 0xFFFFu;
+    v[e] = h >= a.below ? v[e] * a.scale : 0.f;
+    if (RES) v[e] += r[e];
   }
+  store_piece<HOW == kStreamed>(a.out + row * a.out_ld, c, dim, v);
 }
 
 template <typename T>
@@ -104,13 +92,14 @@ fsdp_status launch(const fsdp_dropout_args& n, uint32_t below, hipStream_t strea
   a.offset = n.offset;
   a.below = below;
   a.scale = below < 65536 ? float(65536.0 / (65536 - below)) : 0.f;
-  const int lanes = fsdp::lanes_of_row((n.dim + kElems<T> - 1) / kElems<T>), per = 256 / lanes;
-  const unsigned blocks = unsigned((n.rows + per - 1) / per);
-  const bool stream_out = fsdp::streams(n.out, n.out_pitch, n.rows, n.dim, sizeof(T), lanes);
-  if (a.res && stream_out) k_dropout<T, true, true><<<blocks, 256, 0, stream>>>(a, lanes);
-  else if (a.res) k_dropout<T, true, false><<<blocks, 256, 0, stream>>>(a, lanes);
-  else if (stream_out) k_dropout<T, false, true><<<blocks, 256, 0, stream>>>(a, lanes);
-  else k_dropout<T, false, false><<<blocks, 256, 0, stream>>>(a, lanes);
+  const fsdp::RowGrid g = fsdp::row_grid(n.dim, sizeof(T));
+  const int64_t blocks = fsdp::row_blocks(g, n.rows);
+  if (fsdp_status st = fsdp::check_blocks(blocks)) return st;
+  fsdp::with_rows(g, n.out, n.out_pitch, n.rows, n.dim, sizeof(T), [&](auto how) {
+    constexpr Rows HOW = how.value;
+    if (a.res) k_dropout<T, true, HOW><<<unsigned(blocks), 256, 0, stream>>>(a, g);
+    else k_dropout<T, false, HOW><<<unsigned(blocks), 256, 0, stream>>>(a, g);
+  });
   return fsdp::after_launch("fsdp_dropout");
 }
 

@@ -9,6 +9,7 @@
 // positions are sorted by token first (one launch, no atomics on global memory), then each row of
 // the vocabulary is summed from its list.
 
+#include <algorithm>
 #include <cmath>
 
 #include "row_util.h"
@@ -17,6 +18,7 @@
 
 using fsdp::fail;
 using namespace fsdp::dev;
+using fsdp::Rows, fsdp::kShared, fsdp::kWhole, fsdp::kStreamed;
 
 namespace {
 
@@ -32,38 +34,22 @@ struct EmbedArgs {
   float scale;
 };
 
-// This lane's row: `lanes` lanes a row, 256 / lanes rows a workgroup. With whole waves a row it is
-// the same for all of a wave, which the compiler is told.
-template <bool WAVES>
-__device__ __forceinline__ int64_t own_row(int64_t block, int lanes) {
-  int in = threadIdx.x / lanes;
-  if (WAVES) in = __builtin_amdgcn_readfirstlane(in);
-  return block * (256 / lanes) + in;
-}
-
-// Bound by HBM; two pieces a lane under way.
-template <typename T, bool STREAM>
-__global__ __launch_bounds__(256) void k_embedding(EmbedArgs<T> a, int lanes) {
+// One piece a lane. Bound by HBM.
+template <typename T, Rows HOW>
+__global__ __launch_bounds__(256) void k_embedding(EmbedArgs<T> a, fsdp::RowGrid g) {
   constexpr int N = kElems<T>;
-  const int64_t row = own_row<STREAM>(blockIdx.x, lanes);
-  if (row >= a.rows) return;
+  const int dim = int(a.dim);
+  int64_t row;
+  int c;
+  own_piece<T, HOW>(g, blockIdx.x, row, c);
+  if (row >= a.rows || c >= dim) return;
   const int64_t t = a.tokens[row];
   const bool inside = uint64_t(t) < uint64_t(a.vocab);
-  const T* w = a.w + (inside ? t : 0) * a.w_ld;
-  T* out = a.out + row * a.out_ld;
-  auto write = [&](u32x4 q, int64_t c) {
-    float v[N];
-    unpack(q, v);
+  float v[N];
+  unpack(load_piece(a.w + (inside ? t : 0) * a.w_ld, c, dim), v);
 #pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = inside ? v[e] * a.scale : 0.f;
-    store_piece<STREAM>(out, c, a.dim, v);
-  };
-  const int64_t step = lanes * N;
-  for (int64_t c = threadIdx.x % lanes * N; c < a.dim; c += 2 * step) {
-    const u32x4 p = load_piece(w, c, a.dim), q = load_piece(w, c + step, a.dim);
-    write(p, c);
-    write(q, c + step);
-  }
+  for (int e = 0; e < N; ++e) v[e] = inside ? v[e] * a.scale : 0.f;
+  store_piece<HOW == kStreamed>(a.out + row * a.out_ld, c, dim, v);
 }
 
 // The positions of all tokens, sorted by token and, for equal ones, by position: `order`; the
@@ -192,7 +178,7 @@ struct EmbedBackArgs {
 
 // sum of dy's rows order[begin] to order[end - 1], columns from c on; 4 rows under way
 template <typename T>
-__device__ __forceinline__ void sum_rows(const EmbedBackArgs<T>& a, int32_t begin, int32_t end, int64_t c,
+__device__ __forceinline__ void sum_rows(const EmbedBackArgs<T>& a, int32_t begin, int32_t end, int c,
                                          float (&sum)[kElems<T>]) {
   constexpr int N = kElems<T>;
 #pragma unroll
@@ -207,22 +193,22 @@ __device__ __forceinline__ void sum_rows(const EmbedBackArgs<T>& a, int32_t begi
   for (; i + 4 <= end; i += 4) {
     u32x4 q[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) q[u] = load_piece(a.dy + a.order[i + u] * a.dy_ld, c, a.dim);
+    for (int u = 0; u < 4; ++u) q[u] = load_piece(a.dy + a.order[i + u] * a.dy_ld, c, int(a.dim));
 #pragma unroll
     for (int u = 0; u < 4; ++u) add(q[u]);
   }
-  for (; i < end; ++i) add(load_piece(a.dy + a.order[i] * a.dy_ld, c, a.dim));
+  for (; i < end; ++i) add(load_piece(a.dy + a.order[i] * a.dy_ld, c, int(a.dim)));
 }
 
 template <bool ADD, bool STREAM, typename T>
-__device__ __forceinline__ void write_row(const EmbedBackArgs<T>& a, int64_t v, int64_t c, float (&sum)[kElems<T>]) {
+__device__ __forceinline__ void write_row(const EmbedBackArgs<T>& a, int64_t v, int c, float (&sum)[kElems<T>]) {
   constexpr int N = kElems<T>;
   T* dw = a.dw + v * a.dw_ld;
   float old[N] = {};
-  if (ADD) unpack(load_piece(dw, c, a.dim), old);
+  if (ADD) unpack(load_piece(dw, c, int(a.dim)), old);
 #pragma unroll
   for (int e = 0; e < N; ++e) sum[e] = ADD ? old[e] + sum[e] * a.scale : sum[e] * a.scale;
-  store_piece<STREAM>(dw, c, a.dim, sum);
+  store_piece<STREAM>(dw, c, int(a.dim), sum);
 }
 
 template <int N>
@@ -231,33 +217,36 @@ __device__ __forceinline__ void keep(float* p, const float (&x)[N]) {
   for (int h = 0; h < N; h += 4) *reinterpret_cast<f32x4*>(p + h) = f32x4{x[h], x[h + 1], x[h + 2], x[h + 3]};
 }
 
-// The windows' parts first (`parts` workgroups of 256 lanes), then the short lists: `lanes` lanes
-// a list, 256 / lanes lists a workgroup. Those are the rows of the vocabulary, absent ones
-// (written as zeros) included, or with ADD, which leaves absent rows alone, the places of `order`
-// where a list begins. Bound by HBM: most rows are absent.
-template <typename T, bool ADD, bool STREAM>
-__global__ __launch_bounds__(256) void k_embed_back(EmbedBackArgs<T> a, int lanes, int parts) {
+// The windows' parts first (a workgroup each), then the short lists: those of the rows of the
+// vocabulary, absent ones (written as zeros) included, or with ADD, which leaves absent rows
+// alone, those that begin at the places of `order`. Bound by HBM: most rows are absent.
+template <typename T, bool ADD, Rows HOW>
+__global__ __launch_bounds__(256) void k_embed_back(EmbedBackArgs<T> a, fsdp::RowGrid g) {
   constexpr int N = kElems<T>;
   const int32_t all = a.start[a.vocab];
-  if (int(blockIdx.x) < parts) {
-    const int w = blockIdx.x % a.windows;
-    const int64_t c = (int64_t(blockIdx.x / a.windows) * 256 + threadIdx.x) * N;
-    const int32_t first = w * kWindow, last = (first + kWindow < all ? first + kWindow : all) - 1;
+  const uint32_t parts = uint32_t(a.windows) * g.chunks;
+  int64_t v;
+  int c;
+  own_piece<T, HOW>(g, blockIdx.x < parts ? blockIdx.x : blockIdx.x - parts, v, c);
+  if (c >= a.dim) return;
+  float sum[N];
+  if (blockIdx.x < parts) {
+    if (threadIdx.x >> g.bits) return;
+    const int w = blockIdx.x / uint32_t(g.chunks), first = w * kWindow, last = (first + kWindow < all ? first + kWindow : all) - 1;
     if (first > last) return;
-    const int64_t v = a.tokens[a.order[first]], u = a.tokens[a.order[last]];
-    float sum[N];
-    if (a.start[v + 1] - a.start[v] > kWindow && c < a.dim) {
-      const int32_t end = a.start[v + 1];
+    const int64_t u = a.tokens[a.order[last]];
+    v = a.tokens[a.order[first]];
+    const int32_t end = a.start[v + 1], begin = a.start[u];
+    if (end - a.start[v] > kWindow) {
       sum_rows(a, first, end <= last ? end : last + 1, c, sum);
       keep(a.part + int64_t(2 * w) * a.part_ld + c, sum);
     }
-    if (u != v && a.start[u + 1] - a.start[u] > kWindow && c < a.dim) {
-      sum_rows(a, a.start[u], last + 1, c, sum);
+    if (u != v && a.start[u + 1] - begin > kWindow) {
+      sum_rows(a, begin, last + 1, c, sum);
       keep(a.part + int64_t(2 * w + 1) * a.part_ld + c, sum);
     }
     return;
   }
-  int64_t v = own_row<STREAM>(blockIdx.x - parts, lanes);
   if (ADD) {
     if (v >= all) return;
     const int64_t place = v;
@@ -267,20 +256,19 @@ __global__ __launch_bounds__(256) void k_embed_back(EmbedBackArgs<T> a, int lane
   if (v >= a.vocab) return;
   const int32_t begin = a.start[v], end = a.start[v + 1];
   if (end - begin > kWindow) return;
-  for (int64_t c = threadIdx.x % lanes * N; c < a.dim; c += lanes * N) {
-    float sum[N];
-    sum_rows(a, begin, end, c, sum);
-    write_row<ADD, STREAM>(a, v, c, sum);
-  }
+  sum_rows(a, begin, end, c, sum);
+  write_row<ADD, HOW == kStreamed>(a, v, c, sum);
 }
 
 template <typename T, bool ADD>
-__global__ __launch_bounds__(256) void k_embed_join(EmbedBackArgs<T> a) {
+__global__ __launch_bounds__(256) void k_embed_join(EmbedBackArgs<T> a, fsdp::RowGrid g) {
   constexpr int N = kElems<T>;
-  const int w = blockIdx.x % a.windows;
-  const int64_t c = (int64_t(blockIdx.x / a.windows) * 256 + threadIdx.x) * N;
+  int64_t row;
+  int c;
+  own_piece<T, kShared>(g, blockIdx.x, row, c);
+  const int w = blockIdx.x / uint32_t(g.chunks);
   const int32_t all = a.start[a.vocab], first = w * kWindow, last = (first + kWindow < all ? first + kWindow : all) - 1;
-  if (first > last || c >= a.dim) return;
+  if (first > last || c >= a.dim || threadIdx.x >> g.bits) return;
   const int64_t v = a.tokens[a.order[last]];
   const int32_t begin = a.start[v], end = a.start[v + 1];
   if (begin < first || end - begin <= kWindow) return;       // begins elsewhere, or is no long list
@@ -314,9 +302,6 @@ fsdp_status check_sizes(int64_t rows, int64_t vocab, int64_t dim) {
   if (fsdp_status st = fsdp::check_row_sizes(rows, dim)) return st;
   if (vocab < 1 || vocab >= (int64_t(1) << 22))
     return fail(FSDP_ERR_RANGE, "vocab must be in [1, 2^22) (got %lld)", static_cast<long long>(vocab));
-  if (rows * dim > (int64_t(1) << 38))         // the grid's lanes stay below 2^32
-    return fail(FSDP_ERR_RANGE, "rows %lld of dim %lld: over 2^38 elements", static_cast<long long>(rows),
-                static_cast<long long>(dim));
   return FSDP_OK;
 }
 
@@ -337,10 +322,11 @@ fsdp_status launch(const fsdp_embedding_args& n, hipStream_t stream) {
   a.w_ld = n.weight_pitch;
   a.out_ld = n.out_pitch;
   a.scale = static_cast<float>(n.scale);
-  const int lanes = fsdp::lanes_of_row((n.dim + kElems<T> - 1) / kElems<T>), per = 256 / lanes;
-  const unsigned blocks = unsigned((n.rows + per - 1) / per);
-  if (fsdp::streams(n.out, n.out_pitch, n.rows, n.dim, sizeof(T), lanes)) k_embedding<T, true><<<blocks, 256, 0, stream>>>(a, lanes);
-  else k_embedding<T, false><<<blocks, 256, 0, stream>>>(a, lanes);
+  const fsdp::RowGrid g = fsdp::row_grid(n.dim, sizeof(T));
+  const int64_t blocks = fsdp::row_blocks(g, n.rows);
+  if (fsdp_status st = fsdp::check_blocks(blocks)) return st;
+  fsdp::with_rows(g, n.out, n.out_pitch, n.rows, n.dim, sizeof(T),
+                  [&](auto how) { k_embedding<T, how.value><<<unsigned(blocks), 256, 0, stream>>>(a, g); });
   return fsdp::after_launch("fsdp_embedding");
 }
 
@@ -363,6 +349,9 @@ fsdp_status embedding(const fsdp_embedding_args* n, hipStream_t stream) {
 
 template <typename T>
 fsdp_status launch_back(const fsdp_embedding_backward_args& n, hipStream_t stream) {
+  const fsdp::RowGrid g = fsdp::row_grid(n.dim, sizeof(T));
+  if (fsdp_status st = fsdp::check_blocks(windows_of(n.rows) * g.chunks + fsdp::row_blocks(g, std::max(n.rows, n.vocab))))
+    return st;
   int32_t* start = static_cast<int32_t*>(n.workspace);
   int32_t* order = start + n.vocab + 1;
   const int range = range_of_rows(n.vocab);
@@ -383,18 +372,17 @@ fsdp_status launch_back(const fsdp_embedding_backward_args& n, hipStream_t strea
   a.part_ld = part_pitch(n.dim);
   a.windows = int32_t(windows_of(n.rows));
   a.scale = static_cast<float>(n.scale);
-  const int64_t pieces = (n.dim + kElems<T> - 1) / kElems<T>;
-  const int lanes = fsdp::lanes_of_row(pieces), per = 256 / lanes;
-  const int parts = a.windows * int((pieces + 255) / 256);
-  const unsigned blocks = parts + unsigned(((n.accumulate ? n.rows : n.vocab) + per - 1) / per);
-  if (n.accumulate) k_embed_back<T, true, false><<<blocks, 256, 0, stream>>>(a, lanes, parts);
-  else if (fsdp::streams(n.dweight, n.dweight_pitch, n.vocab, n.dim, sizeof(T), lanes))
-    k_embed_back<T, false, true><<<blocks, 256, 0, stream>>>(a, lanes, parts);
-  else k_embed_back<T, false, false><<<blocks, 256, 0, stream>>>(a, lanes, parts);
-  if (fsdp_status st = fsdp::after_launch("fsdp_embedding_backward")) return st;
-  if (!parts) return FSDP_OK;
-  if (n.accumulate) k_embed_join<T, true><<<parts, 256, 0, stream>>>(a);
-  else k_embed_join<T, false><<<parts, 256, 0, stream>>>(a);
+  const int64_t lists = n.accumulate ? n.rows : n.vocab, parts = int64_t(a.windows) * g.chunks;
+  const int64_t blocks = parts + fsdp::row_blocks(g, lists);
+  fsdp::with_rows(g, n.dweight, n.dweight_pitch, lists, n.dim, sizeof(T), [&](auto how) {
+    constexpr Rows HOW = how.value;
+    if (n.accumulate) k_embed_back<T, true, HOW == kShared ? kShared : kWhole><<<unsigned(blocks), 256, 0, stream>>>(a, g);
+    else k_embed_back<T, false, HOW><<<unsigned(blocks), 256, 0, stream>>>(a, g);
+  });
+  if (a.windows) {
+    if (n.accumulate) k_embed_join<T, true><<<unsigned(parts), 256, 0, stream>>>(a, g);
+    else k_embed_join<T, false><<<unsigned(parts), 256, 0, stream>>>(a, g);
+  }
   return fsdp::after_launch("fsdp_embedding_backward");
 }
 

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <new>
+#include <type_traits>
 
 #include "device_util.h"
 
@@ -25,8 +26,10 @@ __device__ __forceinline__ uint32_t round_bf16(float a, float b) {
 template <typename T>
 constexpr int kElems = 16 / int(sizeof(T));
 
-// From element alignment; elements at or past `dim` are zeros.
-__device__ __forceinline__ u32x4 load_piece(const uint16_t* p, int64_t c, int64_t dim) {
+// From element alignment; elements at or past `dim` are zeros. I: int within a row, int64_t where
+// a row may pass 2^31 bytes.
+template <typename I>
+__device__ __forceinline__ u32x4 load_piece(const uint16_t* p, I c, I dim) {
   if (c + 8 <= dim) return ld_loose<u32x4, 2>(p + c);
   u32x4 r{};
 #pragma unroll
@@ -34,7 +37,8 @@ __device__ __forceinline__ u32x4 load_piece(const uint16_t* p, int64_t c, int64_
     if (c + e < dim) r[e / 2] |= uint32_t(p[c + e]) << (16 * (e & 1));
   return r;
 }
-__device__ __forceinline__ u32x4 load_piece(const float* p, int64_t c, int64_t dim) {
+template <typename I>
+__device__ __forceinline__ u32x4 load_piece(const float* p, I c, I dim) {
   if (c + 4 <= dim) return ld_loose<u32x4, 4>(p + c);
   u32x4 r{};
 #pragma unroll
@@ -52,15 +56,15 @@ __device__ __forceinline__ void unpack(u32x4 r, float (&x)[4]) {
 }
 
 // STREAM: past L2, for a row that the whole wave is in, aligned to 16 bytes.
-template <bool STREAM, typename T>
-__device__ __forceinline__ void store_16(T* p, int64_t c, int64_t dim, u32x4 q) {
-  if constexpr (STREAM) st_stream(rsrc(p, dim * int(sizeof(T))), int(c) * int(sizeof(T)), q);
+template <bool STREAM, typename T, typename I>
+__device__ __forceinline__ void store_16(T* p, I c, I dim, u32x4 q) {
+  if constexpr (STREAM) st_stream(rsrc(p, int64_t(dim) * int(sizeof(T))), int(c) * int(sizeof(T)), q);
   else st_loose<u32x4, sizeof(T)>(p + c, q);
 }
 // Values to the columns from c on, each rounded once; elements at or past `dim` are left alone.
 // Every NaN of a bf16 row is 0x7FC0.
-template <bool STREAM = false>
-__device__ __forceinline__ void store_piece(uint16_t* p, int64_t c, int64_t dim, const float (&x)[8]) {
+template <bool STREAM = false, typename I>
+__device__ __forceinline__ void store_piece(uint16_t* p, I c, I dim, const float (&x)[8]) {
   if (c + 8 <= dim) {
     bool nan = false;
     u32x4 q;
@@ -80,8 +84,8 @@ __device__ __forceinline__ void store_piece(uint16_t* p, int64_t c, int64_t dim,
   for (int e = 0; e < 8; ++e)
     if (c + e < dim) p[c + e] = uint16_t(to_bf16(x[e]));
 }
-template <bool STREAM = false>
-__device__ __forceinline__ void store_piece(float* p, int64_t c, int64_t dim, const float (&x)[4]) {
+template <bool STREAM = false, typename I>
+__device__ __forceinline__ void store_piece(float* p, I c, I dim, const float (&x)[4]) {
   if (c + 4 <= dim) {
     store_16<STREAM>(p, c, dim, u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])});
     return;
@@ -93,21 +97,56 @@ __device__ __forceinline__ void store_piece(float* p, int64_t c, int64_t dim, co
 
 }  // namespace dev
 
-// Lanes that share a row of `pieces` pieces in a workgroup of 256, a power of 2: as many as the
-// row has pieces, so that short rows share a wave.
-inline int lanes_of_row(int64_t pieces) {
-  int lanes = 1;
-  while (lanes < 256 && lanes < pieces) lanes *= 2;
-  return lanes;
+// How workgroups of 256 lanes take rows: 2^bits lanes a row, as many as the row has pieces, and
+// `chunks` workgroups a row if it has more than 256. Chunks of a row are neighbours in the grid
+// (8192 rows of 11008 bf16 elements through the dropout: 61.5 us; with the rows of one chunk as
+// neighbours 82 us).
+struct RowGrid {
+  int32_t bits, chunks;
+};
+enum Rows {
+  kShared,      // rows share a wave
+  kWhole,       // a row has whole waves
+  kStreamed     // and its output goes past L2: far larger than it, every piece aligned
+};
+constexpr int64_t kStreamBytes = int64_t(32) << 20;
+
+inline RowGrid row_grid(int64_t dim, int elem) {
+  const int64_t pieces = (dim * elem + 15) / 16;
+  RowGrid g{0, int32_t((pieces + 255) / 256)};
+  while (g.bits < 8 && (int64_t(1) << g.bits) < pieces) ++g.bits;
+  return g;
+}
+inline int64_t row_blocks(RowGrid g, int64_t rows) { return ((rows + (256 >> g.bits) - 1) >> (8 - g.bits)) * g.chunks; }
+
+// A grid has fewer than 2^32 lanes.
+inline fsdp_status check_blocks(int64_t blocks) {
+  if (blocks >= int64_t(1) << 24)
+    return fail(FSDP_ERR_RANGE, "rows and dim make %lld workgroups of 256 pieces of 16 bytes: over 2^24",
+                static_cast<long long>(blocks));
+  return FSDP_OK;
 }
 
-// Whether `rows` rows of output are streamed past L2: they are far larger than it, rows take
-// whole waves, and every piece is aligned.
-constexpr int64_t kStreamBytes = int64_t(32) << 20;
-inline bool streams(const void* out, int64_t ld, int64_t rows, int64_t dim, int elem, int lanes) {
-  return rows * dim * elem >= kStreamBytes && lanes >= 64 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
-         ld * elem % 16 == 0 && dim * elem < (int64_t(1) << 31);
+// f(Rows constant) for an output's rows.
+template <typename F>
+void with_rows(RowGrid g, const void* out, int64_t ld, int64_t rows, int64_t dim, int elem, F&& f) {
+  if (g.bits < 6) f(std::integral_constant<Rows, kShared>{});
+  else if (rows * dim * elem >= kStreamBytes && reinterpret_cast<uintptr_t>(out) % 16 == 0 && ld * elem % 16 == 0)
+    f(std::integral_constant<Rows, kStreamed>{});
+  else f(std::integral_constant<Rows, kWhole>{});
 }
+
+namespace dev {
+// This lane's row (the same for all of a wave where rows have whole ones) and first column.
+template <typename T, Rows HOW>
+__device__ __forceinline__ void own_piece(RowGrid g, uint32_t block, int64_t& row, int& c) {
+  const uint32_t band = g.chunks == 1 ? block : block / uint32_t(g.chunks), chunk = block - band * g.chunks;
+  int in = threadIdx.x >> g.bits;
+  if (HOW != kShared) in = __builtin_amdgcn_readfirstlane(in);
+  row = (int64_t(band) << (8 - g.bits)) + in;
+  c = int((chunk << g.bits) + (threadIdx.x & ((1 << g.bits) - 1))) * kElems<T>;
+}
+}  // namespace dev
 
 // A rows x dim argument with a row pitch: checked, its byte range recorded.
 inline fsdp_status check_row_arg(const void* p, int64_t ld, int64_t rows, int64_t dim, int elem, bool write,
