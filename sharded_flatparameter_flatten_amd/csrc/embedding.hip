@@ -52,6 +52,26 @@ __global__ __launch_bounds__(256) void k_embedding(EmbedArgs<T> a, fsdp::RowGrid
   store_piece<HOW == kStreamed>(a.out + row * a.out_ld, c, dim, v);
 }
 
+// Rows begin to end - 1 of dweight as zeros, those that `absent` says, in blocks of 256 lanes. The
+// sort and the joining of parts leave most of the memory's bandwidth free, so they share their
+// launches with a part of the zeros that the gradient consists of mostly.
+template <typename T>
+struct Zeros {
+  T* dw;
+  int64_t begin, end, dim, ld;
+  fsdp::RowGrid g;
+  template <Rows HOW, typename F>
+  __device__ __forceinline__ void write(uint32_t block, F&& absent) const {
+    int64_t row;
+    int c;
+    own_piece<T, HOW>(g, HOW == kShared ? block : __builtin_amdgcn_readfirstlane(block), row, c);
+    row += begin;
+    if (row >= end || c >= dim || !absent(row)) return;
+    const float zero[kElems<T>] = {};
+    store_piece<HOW == kStreamed>(dw + row * ld, c, int(dim), zero);
+  }
+};
+
 // The positions of all tokens, sorted by token and, for equal ones, by position: `order`; the
 // list of row v is order[start[v]] to order[start[v + 1] - 1].
 //
@@ -64,9 +84,15 @@ __global__ __launch_bounds__(256) void k_embedding(EmbedArgs<T> a, fsdp::RowGrid
 // find each other by 9 ballots, one for each bit of the row (a loop over the rows that a wave
 // holds took 39 us for 8192 tokens of a text, whose frequent ones all fall to one workgroup).
 constexpr int kTokenLoads = 8;
+template <typename T, Rows HOW>
 __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const int64_t* tokens, int64_t n, int64_t vocab,
                                                                 int64_t padding, int range, int32_t* start,
-                                                                int32_t* order) {
+                                                                int32_t* order, Zeros<T> zeros) {
+  const int sorting = int((vocab + range - 1) / range);
+  if (int(blockIdx.x) >= sorting) {
+    zeros.template write<HOW>((blockIdx.x - sorting) * (64 * kSortWaves / 256) + threadIdx.x / 256, [](int64_t) { return true; });
+    return;
+  }
   __shared__ int32_t at[kSortWaves][kMaxRange];
   __shared__ int32_t total[kMaxRange], before[kSortWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -159,9 +185,12 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const int64_t* t
 // one that begins inside (row 2 w + 1). At most one long list begins in a window, so a second
 // launch gives each window the joining of that one, in the order of its parts.
 //
-// With 32 a text's 8192 tokens of 4096 columns take ... us; without parts the rows of the few
+// With 32 a text's 8192 tokens of 4096 columns take 35 us; without parts the rows of the few
 // most frequent tokens, summed one after the other, took 925 us.
-constexpr int kWindow = 32;
+constexpr int kWindow = 32, kDeep = 8;
+template <bool ADD>
+constexpr int kListsOf = ADD ? 1 : 4;
+constexpr int64_t kBesideSort = int64_t(48) << 20, kBesideJoin = int64_t(24) << 20;   // bytes of zeros
 
 template <typename T>
 struct EmbedBackArgs {
@@ -172,11 +201,13 @@ struct EmbedBackArgs {
   const int32_t* order;
   float* part;
   int64_t vocab, dim, dy_ld, dw_ld, part_ld;
+  int64_t dense;                      // absent rows from here on are written elsewhere
+  int64_t stride;                     // between the lists of a lane
   int32_t windows;
   float scale;
 };
 
-// sum of dy's rows order[begin] to order[end - 1], columns from c on; 4 rows under way
+// sum of dy's rows order[begin] to order[end - 1], columns from c on; 8 rows under way
 template <typename T>
 __device__ __forceinline__ void sum_rows(const EmbedBackArgs<T>& a, int32_t begin, int32_t end, int c,
                                          float (&sum)[kElems<T>]) {
@@ -190,14 +221,19 @@ __device__ __forceinline__ void sum_rows(const EmbedBackArgs<T>& a, int32_t begi
     for (int e = 0; e < N; ++e) sum[e] += x[e];
   };
   int32_t i = begin;
-  for (; i + 4 <= end; i += 4) {
-    u32x4 q[4];
+  auto batch = [&](auto many) {
+    constexpr int M = many.value;
+    u32x4 q[M];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) q[u] = load_piece(a.dy + a.order[i + u] * a.dy_ld, c, int(a.dim));
+    for (int u = 0; u < M; ++u) q[u] = load_piece(a.dy + a.order[i + u] * a.dy_ld, c, int(a.dim));
 #pragma unroll
-    for (int u = 0; u < 4; ++u) add(q[u]);
-  }
-  for (; i < end; ++i) add(load_piece(a.dy + a.order[i] * a.dy_ld, c, int(a.dim)));
+    for (int u = 0; u < M; ++u) add(q[u]);
+    i += M;
+  };
+  while (i + 8 <= end) batch(std::integral_constant<int, 8>{});
+  if (i + 4 <= end) batch(std::integral_constant<int, 4>{});
+  if (i + 2 <= end) batch(std::integral_constant<int, 2>{});
+  if (i < end) batch(std::integral_constant<int, 1>{});
 }
 
 template <bool ADD, bool STREAM, typename T>
@@ -247,22 +283,44 @@ __global__ __launch_bounds__(256) void k_embed_back(EmbedBackArgs<T> a, fsdp::Ro
     }
     return;
   }
-  if (ADD) {
-    if (v >= all) return;
-    const int64_t place = v;
-    v = a.tokens[a.order[place]];
-    if (a.start[v] != place) return;
+  // Lists a grid's length apart, 4 where absent rows are written: what bounds those is the wait for
+  // where their list begins, one for all four (a text's 8192 tokens, 32000 x 4096: 44 us with one list
+  // a lane, 35 with four).
+  constexpr int kLists = kListsOf<ADD>;
+  int32_t begin[kLists], end[kLists];
+  int64_t at[kLists];
+#pragma unroll
+  for (int u = 0; u < kLists; ++u) {
+    at[u] = v + u * a.stride;
+    begin[u] = end[u] = 0;
+    if (ADD) {
+      if (at[u] >= all) continue;
+      const int64_t place = at[u];
+      at[u] = a.tokens[a.order[place]];
+      begin[u] = a.start[at[u]];
+      end[u] = begin[u] == place ? a.start[at[u] + 1] : begin[u];
+    } else if (at[u] < a.vocab) {
+      begin[u] = a.start[at[u]];
+      end[u] = a.start[at[u] + 1];
+    }
   }
-  if (v >= a.vocab) return;
-  const int32_t begin = a.start[v], end = a.start[v + 1];
-  if (end - begin > kWindow) return;
-  sum_rows(a, begin, end, c, sum);
-  write_row<ADD, HOW == kStreamed>(a, v, c, sum);
+#pragma unroll
+  for (int u = 0; u < kLists; ++u) {
+    const int32_t n = end[u] - begin[u];
+    if (n > kWindow || (n == 0 && (ADD || at[u] >= a.dense))) continue;
+    sum_rows(a, begin[u], end[u], c, sum);
+    write_row<ADD, HOW == kStreamed>(a, at[u], c, sum);
+  }
 }
 
-template <typename T, bool ADD>
-__global__ __launch_bounds__(256) void k_embed_join(EmbedBackArgs<T> a, fsdp::RowGrid g) {
+template <typename T, bool ADD, Rows HOW>
+__global__ __launch_bounds__(256) void k_embed_join(EmbedBackArgs<T> a, fsdp::RowGrid g, Zeros<T> zeros) {
   constexpr int N = kElems<T>;
+  const uint32_t parts = uint32_t(a.windows) * g.chunks;
+  if (blockIdx.x >= parts) {
+    zeros.template write<HOW>(blockIdx.x - parts, [&](int64_t v) { return a.start[v] == a.start[v + 1]; });
+    return;
+  }
   int64_t row;
   int c;
   own_piece<T, kShared>(g, blockIdx.x, row, c);
@@ -273,14 +331,21 @@ __global__ __launch_bounds__(256) void k_embed_join(EmbedBackArgs<T> a, fsdp::Ro
   const int32_t begin = a.start[v], end = a.start[v + 1];
   if (begin < first || end - begin <= kWindow) return;       // begins elsewhere, or is no long list
   float sum[N] = {};
-  for (int x = w; x <= (end - 1) / kWindow; ++x) {
-    const float* p = a.part + int64_t(2 * x + (x == w && begin > first)) * a.part_ld + c;
+  const int end_w = (end - 1) / kWindow + 1;
+  for (int x = w; x < end_w; x += kDeep) {
+    f32x4 q[kDeep][N / 4];
 #pragma unroll
-    for (int h = 0; h < N; h += 4) {
-      const f32x4 q = *reinterpret_cast<const f32x4*>(p + h);
+    for (int u = 0; u < kDeep; ++u) {
+      const float* p = a.part + int64_t(2 * (x + u) + (x + u == w && begin > first)) * a.part_ld + c;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum[h + e] += q[e];
+      for (int h = 0; h < N / 4; ++h)
+        if (x + u < end_w) q[u][h] = *reinterpret_cast<const f32x4*>(p + 4 * h);
     }
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u)
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (x + u < end_w) sum[e] += q[u][e / 4][e % 4];
   }
   write_row<ADD, false>(a, v, c, sum);
 }
@@ -355,9 +420,6 @@ fsdp_status launch_back(const fsdp_embedding_backward_args& n, hipStream_t strea
   int32_t* start = static_cast<int32_t*>(n.workspace);
   int32_t* order = start + n.vocab + 1;
   const int range = range_of_rows(n.vocab);
-  k_embed_sort<<<unsigned((n.vocab + range - 1) / range), 64 * kSortWaves, 0, stream>>>(
-      n.tokens, n.rows, n.vocab, n.padding_idx, range, start, order);
-  if (fsdp_status st = fsdp::after_launch("fsdp_embedding_backward")) return st;
   EmbedBackArgs<T> a{};
   a.tokens = n.tokens;
   a.dy = static_cast<const T*>(n.dy);
@@ -373,16 +435,31 @@ fsdp_status launch_back(const fsdp_embedding_backward_args& n, hipStream_t strea
   a.windows = int32_t(windows_of(n.rows));
   a.scale = static_cast<float>(n.scale);
   const int64_t lists = n.accumulate ? n.rows : n.vocab, parts = int64_t(a.windows) * g.chunks;
-  const int64_t blocks = parts + fsdp::row_blocks(g, lists);
   fsdp::with_rows(g, n.dweight, n.dweight_pitch, lists, n.dim, sizeof(T), [&](auto how) {
     constexpr Rows HOW = how.value;
-    if (n.accumulate) k_embed_back<T, true, HOW == kShared ? kShared : kWhole><<<unsigned(blocks), 256, 0, stream>>>(a, g);
-    else k_embed_back<T, false, HOW><<<unsigned(blocks), 256, 0, stream>>>(a, g);
+    // zeros written beside the sort (of the last rows of the vocabulary) and the joins (of those before)
+    const int64_t row_bytes = n.dim * int64_t(sizeof(T));
+    const int64_t beside_sort = HOW == kStreamed && !n.accumulate ? std::min(n.vocab / 4, kBesideSort / row_bytes) : 0;
+    const int64_t beside_join = HOW == kStreamed && !n.accumulate && parts ? std::min(n.vocab / 4, kBesideJoin / row_bytes) : 0;
+    Zeros<T> sort{a.dw, n.vocab - beside_sort, n.vocab, n.dim, n.dweight_pitch, g}, join = sort;
+    join.end = sort.begin;
+    a.dense = join.begin = join.end - beside_join;
+    const int64_t sorting = (n.vocab + range - 1) / range + (fsdp::row_blocks(g, beside_sort) + 3) / 4;
+    k_embed_sort<T, HOW><<<unsigned(sorting), 64 * kSortWaves, 0, stream>>>(n.tokens, n.rows, n.vocab, n.padding_idx, range,
+                                                                          start, order, sort);
+    const int per_lane = n.accumulate ? kListsOf<true> : kListsOf<false>;
+    const int64_t bands = (fsdp::row_blocks(g, lists) / g.chunks + per_lane - 1) / per_lane;
+    a.stride = bands << (8 - g.bits);
+    const unsigned blocks = unsigned(parts + bands * g.chunks), joins = unsigned(parts + fsdp::row_blocks(g, beside_join));
+    if (n.accumulate) {
+      constexpr Rows ADD = HOW == kShared ? kShared : kWhole;
+      k_embed_back<T, true, ADD><<<blocks, 256, 0, stream>>>(a, g);
+      if (parts) k_embed_join<T, true, ADD><<<joins, 256, 0, stream>>>(a, g, join);
+    } else {
+      k_embed_back<T, false, HOW><<<blocks, 256, 0, stream>>>(a, g);
+      if (parts) k_embed_join<T, false, HOW><<<joins, 256, 0, stream>>>(a, g, join);
+    }
   });
-  if (a.windows) {
-    if (n.accumulate) k_embed_join<T, true><<<unsigned(parts), 256, 0, stream>>>(a, g);
-    else k_embed_join<T, false><<<unsigned(parts), 256, 0, stream>>>(a, g);
-  }
   return fsdp::after_launch("fsdp_embedding_backward");
 }
 

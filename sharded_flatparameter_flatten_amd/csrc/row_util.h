@@ -141,7 +141,7 @@ namespace dev {
 template <typename T, Rows HOW>
 __device__ __forceinline__ void own_piece(RowGrid g, uint32_t block, int64_t& row, int& c) {
   const uint32_t band = g.chunks == 1 ? block : block / uint32_t(g.chunks), chunk = block - band * g.chunks;
-  int in = threadIdx.x >> g.bits;
+  int in = (threadIdx.x & 255) >> g.bits;
   if (HOW != kShared) in = __builtin_amdgcn_readfirstlane(in);
   row = (int64_t(band) << (8 - g.bits)) + in;
   c = int((chunk << g.bits) + (threadIdx.x & ((1 << g.bits) - 1))) * kElems<T>;
