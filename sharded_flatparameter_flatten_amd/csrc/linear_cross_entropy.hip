@@ -61,11 +61,13 @@ struct Loss {
   f32x2* stats;                       // m and S of a piece's rows, chunk by chunk of the vocabulary
   float* right;                       // the targets' logits of a piece's rows
   float* part;                        // sums of a split dhidden
+  float* part_w;                      // and dweight
   float* acc;                         // dweight's sums of the pieces before
   int64_t rows, vocab, dim, x_ld, xc_ld, wt_ld, wt_dim, dx_ld, dw_ld, g_ld;
   int64_t piece;
   int32_t chunks, chunk_bits;         // of the vocabulary
   int32_t mean;
+  int32_t last;                       // no piece follows
   int32_t grads;                      // dx or dw is wanted
   float scale;
 };
@@ -77,8 +79,16 @@ __device__ __forceinline__ float factor(const Loss& a) {
   return a.mean ? a.scale / float(*a.count > 1 ? *a.count : 1) : a.scale;
 }
 
-// Every workgroup counts the rows that count before its own, so it knows where they go.
-__global__ __launch_bounds__(256) void k_loss_gather(Loss a) {
+// Every workgroup counts the rows that count before its own, so it knows where they go. The
+// workgroups past `gathers`, if weight is to be copied, give it rows that the products' loads can
+// take: 16-byte pieces, zeros past dim.
+__global__ __launch_bounds__(256) void k_loss_gather(Loss a, int gathers, const uint16_t* w, int64_t w_ld, uint16_t* wc) {
+  if (int(blockIdx.x) >= gathers) {
+    const int64_t row = blockIdx.x - gathers;
+    for (int64_t k = threadIdx.x * 8; k < a.xc_ld - 64; k += 256 * 8)
+      *reinterpret_cast<u32x4*>(wc + row * a.xc_ld + k) = load_piece(w + row * w_ld, k, a.dim);
+    return;
+  }
   __shared__ int32_t part[4];
   __shared__ int32_t to[kGatherRows];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -131,12 +141,6 @@ __global__ __launch_bounds__(256) void k_loss_gather(Loss a) {
         if (k + u * 512 < end) *reinterpret_cast<u32x4*>(xc + k + u * 512) = q[u];
     }
   }
-}
-
-// weight with rows that the products' loads can take: 16-byte pieces, zeros past dim.
-__global__ __launch_bounds__(256) void k_loss_copy(const uint16_t* w, int64_t w_ld, uint16_t* to, int64_t ld, int64_t dim) {
-  for (int64_t k = threadIdx.x * 8; k < ld - 64; k += 256 * 8)
-    *reinterpret_cast<u32x4*>(to + blockIdx.x * ld + k) = load_piece(w + blockIdx.x * w_ld, k, dim);
 }
 
 // ---------------------------------------------------------------------------
@@ -249,36 +253,48 @@ template <int TI_, int TJ_, int WI_, int WJ_, int S_>
 struct Shape {
   static constexpr int TI = TI_, TJ = TJ_, WI = WI_, WJ = WJ_, S = S_;
   static constexpr int kThreads = 64 * WI * WJ;
+  static constexpr int kRowJ = 2 * TI + 16;       // a result's row in LDS
+  static constexpr int kLds = std::max(S * (TI + TJ) * 128, TJ * kRowJ);
 };
 
+// Rows of a piece that count. They are known on the device only: grids are for all rows.
+__device__ __forceinline__ int rows_here(const Loss& a, int64_t row0) {
+  const int64_t left = *a.count - row0;
+  return int(left < 0 ? 0 : left < a.piece ? left : a.piece);
+}
 template <Kind KIND, typename SH>
-__global__ __launch_bounds__(SH::kThreads) void k_loss_product(Loss a, int64_t row0, int splits) {
+__device__ __forceinline__ int tiles_i_of(const Loss& a) {
+  return (int(KIND == kLogits ? a.vocab : a.dim) + SH::TI - 1) / SH::TI;
+}
+template <Kind KIND, typename SH>
+__device__ __forceinline__ int tiles_j_of(const Loss& a, int n) {
+  return ((KIND == kWeight ? int(a.vocab) : n) + SH::TJ - 1) / SH::TJ;
+}
+
+// Workgroup b runs on XCD b % 8, and tiles that share operands should share its L2: each XCD takes
+// one run of a product's tiles, in bands of 8; `slot` is the place in it. Past the run's end there
+// is nothing to do.
+template <Kind KIND, typename SH>
+__device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits, int slot, char* lds) {
   constexpr int TI = SH::TI, TJ = SH::TJ, WI = SH::WI, WJ = SH::WJ, S = SH::S, kWaves = WI * WJ;
   constexpr bool kAcrossA = KIND != kLogits, kAcrossB = KIND == kWeight;
   constexpr int MI = TI / WI / 32, NI = TJ / WJ / 32;
   constexpr int kPerA = TI / 8 / kWaves, kPerB = TJ / 8 / kWaves, kPer = kPerA + kPerB;
   static_assert(kPerA % 2 == 0 && kPerB % 2 == 0, "a wave's first load is of an even number");
   static_assert(S >= 2 && (S & (S - 1)) == 0 && (S - 1) * kPer < 64, "stages");
-  constexpr int kStageA = TI * 128, kStage = (TI + TJ) * 128;
-  constexpr int kRowJ = 2 * TI + 16;              // a result's row in LDS
-  __shared__ __attribute__((aligned(1024))) char lds[std::max(S * kStage, TJ * kRowJ)];
+  constexpr int kStageA = TI * 128, kStage = (TI + TJ) * 128, kRowJ = SH::kRowJ;
 
-  // The rows that count are known here only: the grid is for all of them.
-  const int64_t left = *a.count - row0;
-  const int n = int(left < 0 ? 0 : left < a.piece ? left : a.piece);
+  const int n = rows_here(a, row0);
+  const bool more = *a.count - row0 > a.piece;   // pieces follow
   const int side_i = int(KIND == kLogits ? a.vocab : a.dim), side_j = KIND == kWeight ? int(a.vocab) : n;
   const int depth = KIND == kLogits ? int(a.dim) : KIND == kHidden ? int(a.vocab) : n;
-  const int tiles_i = (side_i + TI - 1) / TI, tiles_j = (side_j + TJ - 1) / TJ;
+  const int tiles_i = tiles_i_of<KIND, SH>(a), tiles_j = tiles_j_of<KIND, SH>(a, n);
   if (KIND == kWeight && row0 > 0 && n == 0) return;
-  // Workgroup b runs on XCD b % 8, and tiles that share operands should share its L2: each XCD
-  // takes one run of the tiles, in bands of 8.
   const int total = tiles_i * tiles_j * splits, run = (total + 7) / 8;
-  int local = int(blockIdx.x / 8);
-  if (local >= run) return;
-  local += int(blockIdx.x % 8) * run;
-  if (local >= total) return;
+  int local = int(blockIdx.x % 8) * run + slot;
+  if (slot >= run || local >= total) return;
   int k0 = 0, kt = (depth + 63) / 64, z = 0, ti, tj;
-  if (KIND == kHidden && splits > 1) {
+  if (KIND != kLogits && splits > 1) {
     z = divide(local, tiles_i * tiles_j);
     local -= z * tiles_i * tiles_j;
     k0 = int(int64_t(kt) * z / splits);
@@ -300,8 +316,8 @@ __global__ __launch_bounds__(SH::kThreads) void k_loss_product(Loss a, int64_t r
     oa.init(a.wt + int64_t(k0) * 64 * a.wt_ld + i0, a.wt_ld, (a.vocab - 1 - int64_t(k0) * 64) * a.wt_ld + a.wt_dim - i0, wave, lane);
     ob.init(a.g + int64_t(j0) * a.g_ld + k0 * 64, a.g_ld, int64_t(n - j0) * a.g_ld - k0 * 64, wave, lane);
   } else {
-    oa.init(xc + i0, a.xc_ld, int64_t(n) * a.xc_ld - i0, wave, lane);
-    ob.init(a.g + j0, a.g_ld, int64_t(n) * a.g_ld - j0, wave, lane);
+    oa.init(xc + int64_t(k0) * 64 * a.xc_ld + i0, a.xc_ld, int64_t(n - k0 * 64) * a.xc_ld - i0, wave, lane);
+    ob.init(a.g + int64_t(k0) * 64 * a.g_ld + j0, a.g_ld, int64_t(n - k0 * 64) * a.g_ld - j0, wave, lane);
   }
   auto load_one = [&](int k, int q) {
     char* to = lds + (k & (S - 1)) * kStage;
@@ -320,6 +336,22 @@ __global__ __launch_bounds__(SH::kThreads) void k_loss_product(Loss a, int64_t r
     for (int y = 0; y < NI; ++y)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.f;
+  // dweight's sums go on from piece to piece: registers as they are, a tile's in one place.
+  const __amdgpu_buffer_rsrc_t sums = rsrc(a.acc + int64_t(ti * tiles_j + tj) * (TI * TJ), TI * TJ * 4);
+  const int own_sums = threadIdx.x * 16;
+  if (KIND == kWeight && a.acc && row0 > 0) {
+#pragma unroll
+    for (int x = 0; x < MI; ++x)
+#pragma unroll
+      for (int y = 0; y < NI; ++y)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                        sums, own_sums + ((x * NI + y) * 4 + g) * SH::kThreads * 16, 0, 0));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[x][y][4 * g + e] = v[e];
+        }
+  }
 
   Fragment<kAcrossA, TI> ra;
   Fragment<kAcrossB, TJ> rb;
@@ -409,14 +441,16 @@ __global__ __launch_bounds__(SH::kThreads) void k_loss_product(Loss a, int64_t r
       const int j = j0 + jl + 32 * y;
       const int t = j < n ? a.target[row0 + j] - i0 - il : -1;
       if (__builtin_amdgcn_ballot_w64(t >= 0 && t < TI / WI) != 0 || i0 + TI > side_i) {
+        float right = 0.f;
 #pragma unroll
         for (int x = 0; x < MI; ++x)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int at = x * 32 + e / 4 * 8 + e % 4;
-            if (at == t) a.right[j] = acc[x][y][e];
-            if (at == t || at >= ends) acc[x][y][e] = -INFINITY;
+            right = at == t ? acc[x][y][e] : right;
+            acc[x][y][e] = at == t || at >= ends ? -INFINITY : acc[x][y][e];
           }
+        if (t >= 0 && t < TI / WI && (t & 4) == 0) a.right[j] = right;   // t counts from this lane's first row
       }
       float m = -INFINITY, s = 0.f;
 #pragma unroll
@@ -462,30 +496,18 @@ __global__ __launch_bounds__(SH::kThreads) void k_loss_product(Loss a, int64_t r
           f(f32x4{acc[x][y][4 * g], acc[x][y][4 * g + 1], acc[x][y][4 * g + 2], acc[x][y][4 * g + 3]},
             (x * NI + y) * 4 + g, il + x * 32 + g * 8, jl + y * 32);
   };
-  if (KIND == kHidden && splits > 1) {            // sums of a part of the vocabulary
-    float* part = a.part + (int64_t(z) * a.piece + j0) * a.xc_ld + i0;
+  if (splits > 1) {                               // sums of a part of the contracted axis
+    float* part = (KIND == kHidden ? a.part + (z * a.piece + j0) * a.xc_ld : a.part_w + (z * a.vocab + j0) * a.xc_ld) + i0;
     each_four([&](f32x4 v, int, int i, int j) {
-      if (j0 + j < n && i0 + i < a.xc_ld) *reinterpret_cast<f32x4*>(part + j * a.xc_ld + i) = v;
+      if (j0 + j < side_j && i0 + i < a.xc_ld) *reinterpret_cast<f32x4*>(part + j * a.xc_ld + i) = v;
     });
     return;
   }
-  if (KIND == kWeight && a.acc) {                 // the pieces before and after
-    f32x4* sum = reinterpret_cast<f32x4*>(a.acc) + int64_t(ti * tiles_j + tj) * (TI * TJ / 4) + threadIdx.x;
-    if (row0 > 0)
-#pragma unroll
-      for (int x = 0; x < MI; ++x)
-#pragma unroll
-        for (int y = 0; y < NI; ++y)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f32x4 v = sum[((x * NI + y) * 4 + g) * SH::kThreads];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[x][y][4 * g + e] = v[e] + acc[x][y][4 * g + e];
-          }
-    if (left > a.piece) {
-      each_four([&](f32x4 v, int at, int, int) { sum[at * SH::kThreads] = v; });
-      return;
-    }
+  if (KIND == kWeight && a.acc && more) {
+    each_four([&](f32x4 v, int at, int, int) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), sums, own_sums + at * SH::kThreads * 16, 0, 0);
+    });
+    return;
   }
   const float k = factor(a);
   each_four([&](f32x4 v, int, int i, int j) { *place(i, j) = u32x2{pack_bf16(v.x * k, v.y * k), pack_bf16(v.z * k, v.w * k)}; });
@@ -506,22 +528,72 @@ __global__ __launch_bounds__(SH::kThreads) void k_loss_product(Loss a, int64_t r
   }
 }
 
-// dhidden from the parts of a split product, added in their order: a row a workgroup.
-__global__ __launch_bounds__(256) void k_loss_join(Loss a, int64_t row0, int splits) {
-  const int64_t r = blockIdx.x;
-  if (row0 + r >= *a.count) return;
+// The logits' tiles.
+template <typename SH>
+__global__ __launch_bounds__(SH::kThreads) void k_loss_logits(Loss a, int64_t row0) {
+  __shared__ __attribute__((aligned(1024))) char lds[SH::kLds];
+  product<kLogits, SH>(a, row0, 1, blockIdx.x / 8, lds);
+}
+
+// The mean, or sum, of the rows' losses, in the order that the workgroup's lanes make; 64 bits.
+__device__ __forceinline__ void mean_of_rows(const Loss& a, double* part) {
+  const int n = *a.count, waves = blockDim.x / 64;
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) sum += double(a.row_loss[i]);
+  sum = wave_sum(sum);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x) return;
+  sum = 0.0;
+  for (int w = 0; w < waves; ++w) sum += part[w];
+  *a.loss = float(a.mean ? sum / double(n > 1 ? n : 1) : sum);
+}
+__global__ __launch_bounds__(1024) void k_loss_mean(Loss a) {
+  __shared__ double part[16];
+  mean_of_rows(a, part);
+}
+
+// The gradients' products, those that are wanted, in one launch: the one with the longer tiles
+// first. The last workgroup makes the mean.
+template <typename SH>
+__global__ __launch_bounds__(SH::kThreads) void k_loss_grads(Loss a, int64_t row0, int splits, int splits_w, int weight_first) {
+  __shared__ __attribute__((aligned(1024))) char lds[SH::kLds];
+  if (blockIdx.x == gridDim.x - 1) {
+    if (a.last) mean_of_rows(a, reinterpret_cast<double*>(lds));
+    return;
+  }
+  const int n = rows_here(a, row0);
+  const int hidden = a.dx ? (tiles_i_of<kHidden, SH>(a) * tiles_j_of<kHidden, SH>(a, n) * splits + 7) / 8 : 0;
+  const int weight = a.dw ? (tiles_i_of<kWeight, SH>(a) * tiles_j_of<kWeight, SH>(a, n) * splits_w + 7) / 8 : 0;
+  int slot = blockIdx.x / 8;
+  const int first = weight_first ? weight : hidden;
+  const bool of_weight = (slot < first) == bool(weight_first);
+  if (slot >= first) slot -= first;
+  if (slot >= (of_weight ? weight : hidden)) return;   // rows that do not count, a product not wanted
+  if (of_weight) product<kWeight, SH>(a, row0, splits_w, slot, lds);
+  else product<kHidden, SH>(a, row0, splits, slot, lds);
+}
+
+// The gradients from the parts of split products, added in their order: a row a workgroup, the
+// first `rows` of them of dhidden.
+__global__ __launch_bounds__(256) void k_loss_join(Loss a, int64_t row0, int64_t rows, int splits, int splits_w) {
+  const bool of_weight = blockIdx.x >= rows;
+  const int64_t r = of_weight ? blockIdx.x - rows : blockIdx.x, stride = (of_weight ? a.vocab : a.piece) * a.xc_ld;
+  if (!of_weight && row0 + r >= *a.count) return;
   const float k = factor(a);
-  uint16_t* dx = a.dx + a.map[row0 + r] * a.dx_ld;
+  uint16_t* out = of_weight ? a.dw + r * a.dw_ld : a.dx + a.map[row0 + r] * a.dx_ld;
+  const float* part = (of_weight ? a.part_w : a.part) + r * a.xc_ld;
+  const int n = of_weight ? splits_w : splits;
   for (int64_t c = threadIdx.x * 8; c < a.dim; c += 256 * 8) {
-    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int z = 0; z < splits; ++z) {
-      const f32x4* p = reinterpret_cast<const f32x4*>(a.part + (int64_t(z) * a.piece + r) * a.xc_ld + c);
+    float sum[8] = {};
+    for (int z = 0; z < n; ++z) {
+      const f32x4* p = reinterpret_cast<const f32x4*>(part + z * stride + c);
 #pragma unroll
       for (int e = 0; e < 4; ++e) { sum[e] += p[0][e]; sum[4 + e] += p[1][e]; }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] *= k;
-    store_piece(dx, c, a.dim, sum);
+    store_piece(out, c, a.dim, sum);
   }
 }
 
@@ -574,20 +646,6 @@ __global__ __launch_bounds__(256) void k_loss_rows(Loss a, int64_t row0) {
   }
 }
 
-__global__ __launch_bounds__(1024) void k_loss_mean(Loss a) {
-  __shared__ double part[16];
-  const int n = *a.count;
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < n; i += 1024) sum += double(a.row_loss[i]);
-  sum = wave_sum(sum);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  if (threadIdx.x) return;
-  sum = 0.0;
-  for (int w = 0; w < 16; ++w) sum += part[w];
-  *a.loss = float(a.mean ? sum / double(n > 1 ? n : 1) : sum);
-}
-
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 using Large = Shape<256, 256, 2, 4, 2>;
@@ -604,19 +662,34 @@ void with_shape(int side, F&& f) {
 
 int64_t tiles_of(int64_t i, int64_t j, int side) { return ((i + side - 1) / side) * ((j + side - 1) / side); }
 
-// The tile of a product of i x j results: the largest that fills the card's 256 CUs.
-int choose_tile(int64_t i, int64_t j) {
-  for (int side : {256, 128})
-    if (tiles_of(i, j, side) >= 192) return side;
-  return 64;
+// Microseconds that a tile takes for a stage, on a card with little and with much to do, and for
+// its start and end; tiles that run at once.
+struct Cost {
+  int side;
+  double idle, busy, ends;
+  int slots;
+};
+constexpr Cost kCosts[] = {{256, 1.02, 1.58, 18, 256}, {128, 0.39, 0.57, 8, 256}, {64, 0.22, 0.67, 6, 512}};
+
+struct Work {                         // tiles of a product, each with so many stages
+  int64_t tiles, stages;
+};
+// Of one or two products in a launch: whole rounds of the longer tiles, and the work in all.
+double time_of(const Cost& c, Work a, Work b) {
+  const double fill = std::min(1.0, double(a.tiles + b.tiles) / c.slots), stage = c.idle + (c.busy - c.idle) * fill;
+  if (a.stages < b.stages) std::swap(a, b);
+  const double la = a.stages * stage + c.ends, lb = b.tiles ? b.stages * stage + c.ends : 0.0;
+  const double rounds = double((a.tiles + c.slots - 1) / c.slots) * la;
+  return std::max({rounds, (a.tiles * la + b.tiles * lb) / c.slots + 0.5 * lb, la});
 }
 
 struct Plan {
   int64_t piece, pieces, g_ld, xc_ld;
-  int logits, hidden, weight;         // tiles
-  int splits;                         // of dhidden's product over the vocabulary
+  int logits, grads;                  // sides of tiles
+  int splits, splits_w;               // of the contracted axis of dhidden's product and dweight's
+  bool weight_first;
   bool copy;
-  int64_t count, map, target, xc, wc, row_loss, g, stats, right, part, acc, bytes;   // workspace offsets
+  int64_t count, map, target, xc, wc, row_loss, g, stats, right, part, part_w, acc, bytes;   // workspace offsets
 };
 
 Plan make_plan(const fsdp_linear_cross_entropy_args& n) {
@@ -630,11 +703,35 @@ Plan make_plan(const fsdp_linear_cross_entropy_args& n) {
   // loads of 16 bytes at 32-bit offsets within a tile
   p.copy = n.rows > 0 && (n.dim % 8 || n.weight_pitch % 8 || n.weight_pitch > (int64_t(1) << 20) ||
                           reinterpret_cast<uintptr_t>(n.weight) % 16);
-  p.logits = choose_tile(n.vocab, p.piece);
-  p.weight = choose_tile(n.dim, n.vocab);
-  p.hidden = choose_tile(n.dim, p.piece);
-  const int64_t tiles = tiles_of(n.dim, p.piece, p.hidden), stages = (n.vocab + 63) / 64;
-  p.splits = int(std::max<int64_t>(1, std::min<int64_t>({256 / tiles, stages / 8, 16})));
+  const int64_t in_dim = (n.dim + 63) / 64, in_vocab = (n.vocab + 63) / 64, in_rows = (p.piece + 63) / 64;
+  double least = 0;
+  for (const Cost& c : kCosts) {
+    const double t = time_of(c, {tiles_of(n.vocab, p.piece, c.side), in_dim}, {0, 0});
+    if (!p.logits || t < least) {
+      p.logits = c.side;
+      least = t;
+    }
+  }
+  p.splits = p.splits_w = 1;
+  for (const Cost& c : kCosts) {
+    const int64_t th = n.dhidden ? tiles_of(n.dim, p.piece, c.side) : 0, tw = n.dweight ? tiles_of(n.dim, n.vocab, c.side) : 0;
+    for (int sh : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      if (sh > 1 && (!th || in_vocab < 4 * sh)) break;
+      for (int sw : {1, 2, 4, 8, 16}) {
+        if (sw > 1 && (!tw || in_rows < 4 * sw || p.pieces > 1)) break;
+        // parts are written and read in fp32 at 4 TB/s
+        const double parts = ((sh > 1 ? double(sh) * p.piece : 0.0) + (sw > 1 ? double(sw) * n.vocab : 0.0)) * n.dim * 8;
+        const double t = time_of(c, {th * sh, (in_vocab + sh - 1) / sh}, {tw * sw, (in_rows + sw - 1) / sw}) +
+                         (parts > 0 ? 5 + parts / 4e6 : 0.0);
+        if (parts > 4e9 || (p.grads && t >= least)) continue;
+        p.grads = c.side;
+        p.splits = sh;
+        p.splits_w = sw;
+        p.weight_first = in_rows * sh > in_vocab * sw;
+        least = t;
+      }
+    }
+  }
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -651,7 +748,8 @@ Plan make_plan(const fsdp_linear_cross_entropy_args& n) {
   p.wc = take(p.copy ? n.vocab * p.xc_ld * 2 : 0);
   p.g = take(grads ? p.piece * p.g_ld * 2 : 0);
   p.part = take(n.dhidden && p.splits > 1 ? p.splits * p.piece * p.xc_ld * 4 : 0);
-  p.acc = take(n.dweight && p.pieces > 1 ? round_up(n.vocab, p.weight) * round_up(n.dim, p.weight) * 4 : 0);
+  p.part_w = take(n.dweight && p.splits_w > 1 ? p.splits_w * n.vocab * p.xc_ld * 4 : 0);
+  p.acc = take(n.dweight && p.pieces > 1 ? round_up(n.vocab, p.grads) * round_up(n.dim, p.grads) * 4 : 0);
   p.bytes = at;
   return p;
 }
@@ -717,6 +815,7 @@ fsdp_status run(const fsdp_linear_cross_entropy_args* n, hipStream_t stream) {
   a.stats = reinterpret_cast<f32x2*>(ws + p.stats);
   a.right = reinterpret_cast<float*>(ws + p.right);
   a.part = reinterpret_cast<float*>(ws + p.part);
+  a.part_w = reinterpret_cast<float*>(ws + p.part_w);
   a.acc = n->dweight && p.pieces > 1 ? reinterpret_cast<float*>(ws + p.acc) : nullptr;
   a.rows = n->rows;
   a.vocab = n->vocab;
@@ -731,37 +830,34 @@ fsdp_status run(const fsdp_linear_cross_entropy_args* n, hipStream_t stream) {
   a.grads = a.dx || a.dw;
   a.scale = static_cast<float>(n->grad_scale);
 
-  k_loss_gather<<<unsigned(std::max<int64_t>(1, (n->rows + kGatherRows - 1) / kGatherRows)), 256, 0, stream>>>(a);
-  if (p.copy)
-    k_loss_copy<<<unsigned(n->vocab), 256, 0, stream>>>(static_cast<const uint16_t*>(n->weight), n->weight_pitch,
-                                                         reinterpret_cast<uint16_t*>(ws + p.wc), p.xc_ld, n->dim);
-  auto blocks = [](int64_t i, int64_t j, int side, int splits) { return unsigned((tiles_of(i, j, side) * splits + 7) / 8 * 8); };
+  const int gathers = int(std::max<int64_t>(1, (n->rows + kGatherRows - 1) / kGatherRows));
+  k_loss_gather<<<unsigned(gathers + (p.copy ? n->vocab : 0)), 256, 0, stream>>>(
+      a, gathers, static_cast<const uint16_t*>(n->weight), n->weight_pitch, reinterpret_cast<uint16_t*>(ws + p.wc));
   for (int64_t i = 0; i < p.pieces; ++i) {
     const int64_t row0 = i * p.piece, rows = std::min(p.piece, n->rows - row0);
+    a.last = i + 1 == p.pieces;
     if (rows > 0) {
       with_shape(p.logits, [&](auto sh) {
         using SH = decltype(sh);
         a.chunk_bits = __builtin_ctz(SH::TI / SH::WI);
         a.chunks = int32_t((n->vocab - 1) >> a.chunk_bits) + 1;
-        k_loss_product<kLogits, SH><<<blocks(n->vocab, rows, SH::TI, 1), SH::kThreads, 0, stream>>>(a, row0, 1);
+        k_loss_logits<SH><<<unsigned(round_up(tiles_of(n->vocab, rows, SH::TI), 8)), SH::kThreads, 0, stream>>>(a, row0);
       });
       k_loss_rows<<<unsigned(rows), 256, 0, stream>>>(a, row0);
-      if (a.dx) {
-        with_shape(p.hidden, [&](auto sh) {
-          using SH = decltype(sh);
-          k_loss_product<kHidden, SH><<<blocks(n->dim, rows, SH::TI, p.splits), SH::kThreads, 0, stream>>>(a, row0, p.splits);
-        });
-        if (p.splits > 1) k_loss_join<<<unsigned(rows), 256, 0, stream>>>(a, row0, p.splits);
-      }
     }
-    if (a.dw)
-      with_shape(p.weight, [&](auto sh) {
+    if (a.grads) {
+      with_shape(p.grads, [&](auto sh) {
         using SH = decltype(sh);
-        k_loss_product<kWeight, SH><<<blocks(n->dim, n->vocab, SH::TI, 1), SH::kThreads, 0, stream>>>(a, row0, 1);
+        const int64_t hidden = a.dx ? round_up(tiles_of(n->dim, rows, SH::TI) * p.splits, 8) : 0;
+        const int64_t weight = a.dw ? round_up(tiles_of(n->dim, n->vocab, SH::TI) * p.splits_w, 8) : 0;
+        k_loss_grads<SH><<<unsigned(hidden + weight + 1), SH::kThreads, 0, stream>>>(a, row0, p.splits, p.splits_w, p.weight_first);
       });
+      const int64_t joins = a.dx && p.splits > 1 ? rows : 0, joins_w = a.dw && p.splits_w > 1 ? n->vocab : 0;
+      if (joins + joins_w) k_loss_join<<<unsigned(joins + joins_w), 256, 0, stream>>>(a, row0, joins, p.splits, p.splits_w);
+    }
     if (fsdp_status st = fsdp::after_launch("fsdp_linear_cross_entropy")) return st;
   }
-  k_loss_mean<<<1, 1024, 0, stream>>>(a);
+  if (!a.grads) k_loss_mean<<<1, 1024, 0, stream>>>(a);
   return fsdp::after_launch("fsdp_linear_cross_entropy");
 }
 
