@@ -597,79 +597,149 @@ __global__ __launch_bounds__(256) void k_loss_join(Loss a, int64_t row0, int64_t
   }
 }
 
-// A row's loss from its chunks' m and S, and its row of G from P.
-__global__ __launch_bounds__(256) void k_loss_rows(Loss a, int64_t row0) {
-  __shared__ float part[8];
-  const int64_t r = blockIdx.x;
-  if (row0 + r >= *a.count) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// e^x for x <= 0: the argument's rounding, 2^-24 of it, and a unit or two in the last place.
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+// What sums are taken from: -infinity stands for a chunk with nothing in it, whose sum is 0.
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+// A row's loss from its chunks' m and S, by `lanes` lanes; every lane gets it.
+template <int LANES>
+__device__ __forceinline__ float row_loss(const Loss& a, int64_t r, int lane, float right, f32x2* joined) {
   const f32x2* stats = a.stats + r;
   float m = -INFINITY, s = 0.f;
-  for (int t = threadIdx.x; t < a.chunks; t += 256) m = fmaxf(m, stats[t * a.piece].x);
+  for (int t = lane; t < a.chunks; t += 4 * LANES) {
+    f32x2 q[4];
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-  if (lane == 0) part[wave] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-  const float from = m == -INFINITY ? 0.f : m;
-  for (int t = threadIdx.x; t < a.chunks; t += 256) {
-    const f32x2 q = stats[t * a.piece];
-    s += q.y * expf((q.x == -INFINITY ? from : q.x) - from);
+    for (int u = 0; u < 4; ++u) q[u] = t + u * LANES < a.chunks ? stats[(t + u * LANES) * a.piece] : f32x2{-INFINITY, 0.f};
+    const float top = fmaxf(fmaxf(fmaxf(q[0].x, q[1].x), fmaxf(q[2].x, q[3].x)), m), base = base_of(top);
+    s *= exp_of(m - base);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) s += q[u].y * exp_of(q[u].x - base);
+    m = top;
   }
-  s = wave_sum(s);
-  if (lane == 0) part[4 + wave] = s;
+  float top = m;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  s = wave_sum(s * exp_of(m - base_of(top)));
+  if constexpr (LANES > 64) {
+    if ((lane & 63) == 0) joined[lane / 64] = f32x2{top, s};
+    __syncthreads();
+    float all = joined[0].x;
+#pragma unroll
+    for (int w = 1; w < LANES / 64; ++w) all = fmaxf(all, joined[w].x);
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < LANES / 64; ++w) s += joined[w].y * exp_of(joined[w].x - base_of(all));
+    top = all;
+  }
+  const float ahead = top - right;
+  return ahead > 0.f ? ahead + logf(s + expf(-ahead)) : log1pf(s * expf(ahead));
+}
+
+// Losses only, of few rows: a wave a row, and the mean, in one workgroup.
+constexpr int kFewRows = 32;
+__global__ __launch_bounds__(1024) void k_loss_few(Loss a) {
+  __shared__ double part[16];
+  const int n = *a.count, lane = threadIdx.x & 63;
+  for (int r = threadIdx.x >> 6; r < n; r += 16) {
+    const float loss = row_loss<64>(a, r, lane, a.right[r], nullptr);
+    if (lane == 0) {
+      a.row_loss[r] = loss;
+      if (a.losses) a.losses[a.map[r]] = loss;
+    }
+  }
   __syncthreads();
-  s = (part[4] + part[5]) + (part[6] + part[7]);
-  const float right = a.right[r], ahead = m - right;
-  const float loss = ahead > 0.f ? ahead + logf(s + expf(-ahead)) : log1pf(s * expf(ahead));
-  if (threadIdx.x == 0) {
+  mean_of_rows(a, part);
+}
+
+// A row's loss and its row of G from P. `slices` workgroups share a row, each with a part of the
+// vocabulary, where there are few rows; each of them joins m and S.
+//
+// Bound by HBM: 8192 rows of 32000 are read and written in 210 us (5 TB/s), four loads under way a
+// lane, the first four before the loss is known. (Streamed stores took as long.)
+__global__ __launch_bounds__(256) void k_loss_rows(Loss a, int64_t row0, int slices) {
+  __shared__ f32x2 joined[4];
+  const int64_t r = slices == 1 ? blockIdx.x : blockIdx.x / uint32_t(slices);
+  const int slice = slices == 1 ? 0 : int(blockIdx.x - r * slices);
+  if (row0 + r >= *a.count) return;
+  const int target = a.target[row0 + r], vocab = int(a.vocab);
+  const float right = a.right[r];
+  uint16_t* g = a.g + r * a.g_ld;
+  const int end = a.grads ? int(a.vocab * (slice + 1) / slices + 7) & ~7 : 0;
+  constexpr int kDeep = 4, kStep = 256 * 8;
+  f16x8 p[kDeep];
+  float mt[kDeep];
+  auto fetch = [&](int c0) {
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int c = c0 + u * kStep;
+      if (c >= end) continue;
+      p[u] = *reinterpret_cast<const f16x8*>(g + c);
+      mt[u] = a.stats[(c < vocab ? c >> a.chunk_bits : 0) * a.piece + r].x;
+    }
+  };
+  int c0 = (int(a.vocab * slice / slices + 7) & ~7) + threadIdx.x * 8;
+  fetch(c0);
+  const float loss = row_loss<256>(a, r, threadIdx.x, right, joined);
+  if (threadIdx.x == 0 && slice == 0) {
     a.row_loss[row0 + r] = loss;
     if (a.losses) a.losses[a.map[row0 + r]] = loss;
   }
-  if (!a.grads) return;
-  const int target = a.target[row0 + r];
-  uint16_t* g = a.g + r * a.g_ld;
-  for (int c = threadIdx.x * 8; c < a.vocab; c += 256 * 8) {
-    const float mt = stats[(c >> a.chunk_bits) * a.piece].x;
-    const float f = mt == -INFINITY ? 0.f : expf(mt - right - loss);
-    const f16x8 p = *reinterpret_cast<const f16x8*>(g + c);
-    float v[8];
+  while (c0 < end) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = float(p[e]) * f;
-    if (uint32_t(target - c) < 8) {
+    for (int u = 0; u < kDeep; ++u) {
+      const int c = c0 + u * kStep;
+      if (c >= end) continue;
+      const float f = mt[u] == -INFINITY ? 0.f : exp_of(mt[u] - right - loss);
+      float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e == target) v[e] = expm1f(-loss);
+      for (int e = 0; e < 8; ++e) v[e] = float(p[u][e]) * f;
+      if (uint32_t(target - c) < 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e == target) v[e] = expm1f(-loss);
+      }
+      *reinterpret_cast<u32x4*>(g + c) = u32x4{round_bf16(v[0], v[1]), round_bf16(v[2], v[3]), round_bf16(v[4], v[5]),
+                                               round_bf16(v[6], v[7])};
     }
-    *reinterpret_cast<u32x4*>(g + c) = u32x4{round_bf16(v[0], v[1]), round_bf16(v[2], v[3]), round_bf16(v[4], v[5]),
-                                             round_bf16(v[6], v[7])};
+    c0 += kDeep * kStep;
+    fetch(c0);
   }
 }
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
+// The tiles: 256, one workgroup a CU; 128 with four stages in LDS, one a CU, for few tiles; 128 with
+// two stages, two a CU, and 64, two a CU, for many.
 using Large = Shape<256, 256, 2, 4, 2>;
-using Middle = Shape<128, 128, 2, 2, 4>;
+using Deep = Shape<128, 128, 2, 4, 4>;
+using Twin = Shape<128, 128, 2, 4, 2>;
 using Small = Shape<64, 64, 2, 2, 4>;
 
-// f(a tile's shape) for a tile of `side`.
-template <typename F>
-void with_shape(int side, F&& f) {
-  if (side == 256) f(Large{});
-  else if (side == 128) f(Middle{});
-  else f(Small{});
-}
-
-int64_t tiles_of(int64_t i, int64_t j, int side) { return ((i + side - 1) / side) * ((j + side - 1) / side); }
-
-// Microseconds that a tile takes for a stage, on a card with little and with much to do, and for
-// its start and end; tiles that run at once.
+// What a tile costs, in microseconds: a stage on a card with little and with much to do, its start
+// and end; tiles that run at once.
 struct Cost {
   int side;
   double idle, busy, ends;
   int slots;
 };
-constexpr Cost kCosts[] = {{256, 1.02, 1.58, 18, 256}, {128, 0.39, 0.57, 8, 256}, {64, 0.22, 0.67, 6, 512}};
+constexpr Cost kCosts[] = {
+    {256, 1.02, 1.45, 16, 256}, {128, 0.36, 0.56, 5, 256}, {128, 0.57, 1.08, 6, 512}, {64, 0.22, 0.46, 2.4, 512}};
+
+constexpr int kShapes = sizeof(kCosts) / sizeof(kCosts[0]);
+
+// f(the shape that kCosts[which] is of).
+template <typename F>
+void with_shape(int which, F&& f) {
+  switch (which) {
+    case 0: return f(Large{});
+    case 1: return f(Deep{});
+    case 2: return f(Twin{});
+    default: return f(Small{});
+  }
+}
+
+int64_t tiles_of(int64_t i, int64_t j, int side) { return ((i + side - 1) / side) * ((j + side - 1) / side); }
 
 struct Work {                         // tiles of a product, each with so many stages
   int64_t tiles, stages;
@@ -679,13 +749,13 @@ double time_of(const Cost& c, Work a, Work b) {
   const double fill = std::min(1.0, double(a.tiles + b.tiles) / c.slots), stage = c.idle + (c.busy - c.idle) * fill;
   if (a.stages < b.stages) std::swap(a, b);
   const double la = a.stages * stage + c.ends, lb = b.tiles ? b.stages * stage + c.ends : 0.0;
-  const double rounds = double((a.tiles + c.slots - 1) / c.slots) * la;
-  return std::max({rounds, (a.tiles * la + b.tiles * lb) / c.slots + 0.5 * lb, la});
+  if (a.tiles + b.tiles <= c.slots) return la;
+  return std::max(double((a.tiles + c.slots - 1) / c.slots) * la, (a.tiles * la + b.tiles * lb) / c.slots + 0.5 * lb);
 }
 
 struct Plan {
   int64_t piece, pieces, g_ld, xc_ld;
-  int logits, grads;                  // sides of tiles
+  int logits, grads;                  // tiles, by their places in kCosts
   int splits, splits_w;               // of the contracted axis of dhidden's product and dweight's
   bool weight_first;
   bool copy;
@@ -704,27 +774,29 @@ Plan make_plan(const fsdp_linear_cross_entropy_args& n) {
   p.copy = n.rows > 0 && (n.dim % 8 || n.weight_pitch % 8 || n.weight_pitch > (int64_t(1) << 20) ||
                           reinterpret_cast<uintptr_t>(n.weight) % 16);
   const int64_t in_dim = (n.dim + 63) / 64, in_vocab = (n.vocab + 63) / 64, in_rows = (p.piece + 63) / 64;
-  double least = 0;
-  for (const Cost& c : kCosts) {
-    const double t = time_of(c, {tiles_of(n.vocab, p.piece, c.side), in_dim}, {0, 0});
-    if (!p.logits || t < least) {
-      p.logits = c.side;
+  double least = HUGE_VAL;
+  for (int i = 0; i < kShapes; ++i) {
+    const double t = time_of(kCosts[i], {tiles_of(n.vocab, p.piece, kCosts[i].side), in_dim}, {0, 0});
+    if (t < least) {
+      p.logits = i;
       least = t;
     }
   }
   p.splits = p.splits_w = 1;
-  for (const Cost& c : kCosts) {
-    const int64_t th = n.dhidden ? tiles_of(n.dim, p.piece, c.side) : 0, tw = n.dweight ? tiles_of(n.dim, n.vocab, c.side) : 0;
+  least = HUGE_VAL;
+  for (int i = 0; i < kShapes && grads; ++i) {
+    const int side = kCosts[i].side;
+    const int64_t th = n.dhidden ? tiles_of(n.dim, p.piece, side) : 0, tw = n.dweight ? tiles_of(n.dim, n.vocab, side) : 0;
     for (int sh : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
       if (sh > 1 && (!th || in_vocab < 4 * sh)) break;
       for (int sw : {1, 2, 4, 8, 16}) {
         if (sw > 1 && (!tw || in_rows < 4 * sw || p.pieces > 1)) break;
         // parts are written and read in fp32 at 4 TB/s
         const double parts = ((sh > 1 ? double(sh) * p.piece : 0.0) + (sw > 1 ? double(sw) * n.vocab : 0.0)) * n.dim * 8;
-        const double t = time_of(c, {th * sh, (in_vocab + sh - 1) / sh}, {tw * sw, (in_rows + sw - 1) / sw}) +
+        const double t = time_of(kCosts[i], {th * sh, (in_vocab + sh - 1) / sh}, {tw * sw, (in_rows + sw - 1) / sw}) +
                          (parts > 0 ? 5 + parts / 4e6 : 0.0);
-        if (parts > 4e9 || (p.grads && t >= least)) continue;
-        p.grads = c.side;
+        if (parts > 4e9 || t >= least) continue;
+        p.grads = i;
         p.splits = sh;
         p.splits_w = sw;
         p.weight_first = in_rows * sh > in_vocab * sw;
@@ -743,13 +815,14 @@ Plan make_plan(const fsdp_linear_cross_entropy_args& n) {
   p.target = take(n.rows * 4);
   p.row_loss = take(n.rows * 4);
   p.right = take(p.piece * 4);
-  p.stats = take(p.piece * ((n.vocab + p.logits / 2 - 1) / (p.logits / 2)) * 8);
+  p.stats = take(p.piece * (n.vocab * 2 / kCosts[p.logits].side + 1) * 8);     // a chunk is half a tile
   p.xc = take(n.rows * p.xc_ld * 2);
   p.wc = take(p.copy ? n.vocab * p.xc_ld * 2 : 0);
   p.g = take(grads ? p.piece * p.g_ld * 2 : 0);
   p.part = take(n.dhidden && p.splits > 1 ? p.splits * p.piece * p.xc_ld * 4 : 0);
   p.part_w = take(n.dweight && p.splits_w > 1 ? p.splits_w * n.vocab * p.xc_ld * 4 : 0);
-  p.acc = take(n.dweight && p.pieces > 1 ? round_up(n.vocab, p.grads) * round_up(n.dim, p.grads) * 4 : 0);
+  const int side = kCosts[p.grads].side;
+  p.acc = take(n.dweight && p.pieces > 1 ? round_up(n.vocab, side) * round_up(n.dim, side) * 4 : 0);
   p.bytes = at;
   return p;
 }
@@ -843,7 +916,12 @@ fsdp_status run(const fsdp_linear_cross_entropy_args* n, hipStream_t stream) {
         a.chunks = int32_t((n->vocab - 1) >> a.chunk_bits) + 1;
         k_loss_logits<SH><<<unsigned(round_up(tiles_of(n->vocab, rows, SH::TI), 8)), SH::kThreads, 0, stream>>>(a, row0);
       });
-      k_loss_rows<<<unsigned(rows), 256, 0, stream>>>(a, row0);
+      if (!a.grads && n->rows <= kFewRows) {
+        k_loss_few<<<1, 1024, 0, stream>>>(a);
+        return fsdp::after_launch("fsdp_linear_cross_entropy");
+      }
+      const int slices = a.grads ? int(std::max<int64_t>(1, std::min<int64_t>(2048 / rows, n->vocab / 4096))) : 1;
+      k_loss_rows<<<unsigned(rows * slices), 256, 0, stream>>>(a, row0, slices);
     }
     if (a.grads) {
       with_shape(p.grads, [&](auto sh) {
