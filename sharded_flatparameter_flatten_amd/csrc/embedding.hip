@@ -73,7 +73,7 @@ struct Zeros {
 };
 
 // The positions of all tokens, sorted by token and, for equal ones, by position: `order`; the
-// list of row v is order[start[v]] to order[start[v + 1] - 1].
+// list of row v is order[start[v]] to order[start[v + 1] - 1]; `sorted` has the tokens themselves.
 //
 // Workgroup g sorts what falls into its `range` rows of the vocabulary, on its own: every
 // workgroup reads all tokens, so it also counts how many fall before its range, which is where
@@ -87,7 +87,7 @@ constexpr int kTokenLoads = 8;
 template <typename T, Rows HOW>
 __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const int64_t* tokens, int64_t n, int64_t vocab,
                                                                 int64_t padding, int range, int32_t* start,
-                                                                int32_t* order, Zeros<T> zeros) {
+                                                                int32_t* order, int32_t* sorted, Zeros<T> zeros) {
   const int sorting = int((vocab + range - 1) / range);
   if (int(blockIdx.x) >= sorting) {
     zeros.template write<HOW>((blockIdx.x - sorting) * (64 * kSortWaves / 256) + threadIdx.x / 256, [](int64_t) { return true; });
@@ -126,23 +126,25 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const int64_t* t
 #pragma unroll
   for (int w = 0; w < kSortWaves; ++w) base += before[w];
   const int v = threadIdx.x;
+  int32_t own[kSortWaves] = {};
   if (v < here) {
     int32_t sum = 0;
-    for (int w = 0; w < kSortWaves; ++w) sum += at[w][v];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) sum += own[w] = at[w][v];
     total[v] = sum;
   }
   __syncthreads();
   if (wave == 0) {                    // sums become places: an exclusive scan, 64 rows at a time
     int32_t carry = base;
     for (int v0 = 0; v0 < here; v0 += 64) {
-      const int32_t own = v0 + lane < here ? total[v0 + lane] : 0;
-      int32_t x = own;
+      const int32_t sum = v0 + lane < here ? total[v0 + lane] : 0;
+      int32_t x = sum;
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
         const int32_t y = __shfl_up(x, d);
         if (lane >= d) x += y;
       }
-      if (v0 + lane < here) total[v0 + lane] = carry + x - own;
+      if (v0 + lane < here) total[v0 + lane] = carry + x - sum;
       carry += __shfl(x, 63);
     }
     if (lane == 0 && lo + here == vocab) start[vocab] = carry;
@@ -151,10 +153,10 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const int64_t* t
   if (v < here) {
     int32_t place = total[v];
     start[lo + v] = place;
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const int32_t own = at[w][v];
       at[w][v] = place;
-      place += own;
+      place += own[w];
     }
   }
   __syncthreads();
@@ -172,6 +174,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const int64_t* t
     if (mine) {
       place = at[wave][row];
       order[place + earlier] = i;
+      sorted[place + earlier] = int32_t(lo) + row;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // every lane has read
     if (mine && earlier == 0) at[wave][row] = place + __builtin_popcountll(same);
@@ -194,11 +197,11 @@ constexpr int64_t kBesideSort = int64_t(48) << 20, kBesideJoin = int64_t(24) << 
 
 template <typename T>
 struct EmbedBackArgs {
-  const int64_t* tokens;
   const T* dy;
   T* dw;
   const int32_t* start;
   const int32_t* order;
+  const int32_t* sorted;
   float* part;
   int64_t vocab, dim, dy_ld, dw_ld, part_ld;
   int64_t dense;                      // absent rows from here on are written elsewhere
@@ -207,33 +210,40 @@ struct EmbedBackArgs {
   float scale;
 };
 
-// sum of dy's rows order[begin] to order[end - 1], columns from c on; 8 rows under way
-template <typename T>
+// sum of dy's rows order[begin] to order[end - 1], kWindow at most, columns from c on; 8 rows under
+// way. Where the list is the same for all of a wave, its lanes fetch all of it at once.
+template <Rows HOW, typename T>
 __device__ __forceinline__ void sum_rows(const EmbedBackArgs<T>& a, int32_t begin, int32_t end, int c,
                                          float (&sum)[kElems<T>]) {
   constexpr int N = kElems<T>;
 #pragma unroll
   for (int e = 0; e < N; ++e) sum[e] = 0.f;
-  auto add = [&](u32x4 q) {
-    float x[N];
-    unpack(q, x);
-#pragma unroll
-    for (int e = 0; e < N; ++e) sum[e] += x[e];
-  };
-  int32_t i = begin;
+  static_assert(kWindow <= 64, "a lane an entry");
+  const int32_t lane = threadIdx.x & 63, n = end - begin;
+  int32_t entry = 0;
+  if (HOW != kShared && lane < n) entry = a.order[begin + lane];
+  int32_t i = 0;
   auto batch = [&](auto many) {
     constexpr int M = many.value;
     u32x4 q[M];
 #pragma unroll
-    for (int u = 0; u < M; ++u) q[u] = load_piece(a.dy + a.order[i + u] * a.dy_ld, c, int(a.dim));
+    for (int u = 0; u < M; ++u) {
+      const int32_t row = HOW != kShared ? __builtin_amdgcn_readlane(entry, i + u) : a.order[begin + i + u];
+      q[u] = load_piece(a.dy + row * a.dy_ld, c, int(a.dim));
+    }
 #pragma unroll
-    for (int u = 0; u < M; ++u) add(q[u]);
+    for (int u = 0; u < M; ++u) {
+      float x[N];
+      unpack(q[u], x);
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum[e] += x[e];
+    }
     i += M;
   };
-  while (i + 8 <= end) batch(std::integral_constant<int, 8>{});
-  if (i + 4 <= end) batch(std::integral_constant<int, 4>{});
-  if (i + 2 <= end) batch(std::integral_constant<int, 2>{});
-  if (i < end) batch(std::integral_constant<int, 1>{});
+  while (i + 8 <= n) batch(std::integral_constant<int, 8>{});
+  if (i + 4 <= n) batch(std::integral_constant<int, 4>{});
+  if (i + 2 <= n) batch(std::integral_constant<int, 2>{});
+  if (i < n) batch(std::integral_constant<int, 1>{});
 }
 
 template <bool ADD, bool STREAM, typename T>
@@ -248,7 +258,8 @@ __device__ __forceinline__ void write_row(const EmbedBackArgs<T>& a, int64_t v, 
 }
 
 template <int N>
-__device__ __forceinline__ void keep(float* p, const float (&x)[N]) {
+__device__ __forceinline__ void keep(bool inside, float* p, const float (&x)[N]) {
+  if (!inside) return;
 #pragma unroll
   for (int h = 0; h < N; h += 4) *reinterpret_cast<f32x4*>(p + h) = f32x4{x[h], x[h + 1], x[h + 2], x[h + 3]};
 }
@@ -264,22 +275,23 @@ __global__ __launch_bounds__(256) void k_embed_back(EmbedBackArgs<T> a, fsdp::Ro
   int64_t v;
   int c;
   own_piece<T, HOW>(g, blockIdx.x < parts ? blockIdx.x : blockIdx.x - parts, v, c);
-  if (c >= a.dim) return;
+  // lanes past the row's end stay where a wave is in one row: they hold entries of its list
+  if (HOW == kShared && c >= a.dim) return;
   float sum[N];
   if (blockIdx.x < parts) {
     if (threadIdx.x >> g.bits) return;
     const int w = blockIdx.x / uint32_t(g.chunks), first = w * kWindow, last = (first + kWindow < all ? first + kWindow : all) - 1;
     if (first > last) return;
-    const int64_t u = a.tokens[a.order[last]];
-    v = a.tokens[a.order[first]];
+    const int64_t u = a.sorted[last];
+    v = a.sorted[first];
     const int32_t end = a.start[v + 1], begin = a.start[u];
     if (end - a.start[v] > kWindow) {
-      sum_rows(a, first, end <= last ? end : last + 1, c, sum);
-      keep(a.part + int64_t(2 * w) * a.part_ld + c, sum);
+      sum_rows<HOW>(a, first, end <= last ? end : last + 1, c, sum);
+      keep(c < a.dim, a.part + int64_t(2 * w) * a.part_ld + c, sum);
     }
     if (u != v && a.start[u + 1] - begin > kWindow) {
-      sum_rows(a, begin, last + 1, c, sum);
-      keep(a.part + int64_t(2 * w + 1) * a.part_ld + c, sum);
+      sum_rows<HOW>(a, begin, last + 1, c, sum);
+      keep(c < a.dim, a.part + int64_t(2 * w + 1) * a.part_ld + c, sum);
     }
     return;
   }
@@ -296,7 +308,7 @@ __global__ __launch_bounds__(256) void k_embed_back(EmbedBackArgs<T> a, fsdp::Ro
     if (ADD) {
       if (at[u] >= all) continue;
       const int64_t place = at[u];
-      at[u] = a.tokens[a.order[place]];
+      at[u] = a.sorted[place];
       begin[u] = a.start[at[u]];
       end[u] = begin[u] == place ? a.start[at[u] + 1] : begin[u];
     } else if (at[u] < a.vocab) {
@@ -308,7 +320,7 @@ __global__ __launch_bounds__(256) void k_embed_back(EmbedBackArgs<T> a, fsdp::Ro
   for (int u = 0; u < kLists; ++u) {
     const int32_t n = end[u] - begin[u];
     if (n > kWindow || (n == 0 && (ADD || at[u] >= a.dense))) continue;
-    sum_rows(a, begin[u], end[u], c, sum);
+    sum_rows<HOW>(a, begin[u], end[u], c, sum);
     write_row<ADD, HOW == kStreamed>(a, at[u], c, sum);
   }
 }
@@ -327,7 +339,7 @@ __global__ __launch_bounds__(256) void k_embed_join(EmbedBackArgs<T> a, fsdp::Ro
   const int w = blockIdx.x / uint32_t(g.chunks);
   const int32_t all = a.start[a.vocab], first = w * kWindow, last = (first + kWindow < all ? first + kWindow : all) - 1;
   if (first > last || c >= a.dim || threadIdx.x >> g.bits) return;
-  const int64_t v = a.tokens[a.order[last]];
+  const int64_t v = a.sorted[last];
   const int32_t begin = a.start[v], end = a.start[v + 1];
   if (begin < first || end - begin <= kWindow) return;       // begins elsewhere, or is no long list
   float sum[N] = {};
@@ -356,7 +368,7 @@ int range_of_rows(int64_t vocab) {
 }
 
 int64_t windows_of(int64_t rows) { return rows > kWindow ? (rows + kWindow - 1) / kWindow : 0; }
-int64_t lists_bytes(int64_t rows, int64_t vocab) { return ((vocab + 1 + rows) * 4 + 15) / 16 * 16; }
+int64_t lists_bytes(int64_t rows, int64_t vocab) { return ((vocab + 1 + 2 * rows) * 4 + 15) / 16 * 16; }
 int64_t part_pitch(int64_t dim) { return (dim + 7) / 8 * 8; }
 
 int64_t back_workspace(int64_t rows, int64_t vocab, int64_t dim) {
@@ -421,11 +433,11 @@ fsdp_status launch_back(const fsdp_embedding_backward_args& n, hipStream_t strea
   int32_t* order = start + n.vocab + 1;
   const int range = range_of_rows(n.vocab);
   EmbedBackArgs<T> a{};
-  a.tokens = n.tokens;
   a.dy = static_cast<const T*>(n.dy);
   a.dw = static_cast<T*>(n.dweight);
   a.start = start;
   a.order = order;
+  a.sorted = order + n.rows;
   a.part = reinterpret_cast<float*>(static_cast<char*>(n.workspace) + lists_bytes(n.rows, n.vocab));
   a.vocab = n.vocab;
   a.dim = n.dim;
@@ -446,7 +458,7 @@ fsdp_status launch_back(const fsdp_embedding_backward_args& n, hipStream_t strea
     a.dense = join.begin = join.end - beside_join;
     const int64_t sorting = (n.vocab + range - 1) / range + (fsdp::row_blocks(g, beside_sort) + 3) / 4;
     k_embed_sort<T, HOW><<<unsigned(sorting), 64 * kSortWaves, 0, stream>>>(n.tokens, n.rows, n.vocab, n.padding_idx, range,
-                                                                          start, order, sort);
+                                                                          start, order, order + n.rows, sort);
     const int per_lane = n.accumulate ? kListsOf<true> : kListsOf<false>;
     const int64_t bands = (fsdp::row_blocks(g, lists) / g.chunks + per_lane - 1) / per_lane;
     a.stride = bands << (8 - g.bits);

@@ -750,7 +750,9 @@ double time_of(const Cost& c, Work a, Work b) {
   if (a.stages < b.stages) std::swap(a, b);
   const double la = a.stages * stage + c.ends, lb = b.tiles ? b.stages * stage + c.ends : 0.0;
   if (a.tiles + b.tiles <= c.slots) return la;
-  return std::max(double((a.tiles + c.slots - 1) / c.slots) * la, (a.tiles * la + b.tiles * lb) / c.slots + 0.5 * lb);
+  // the longer tiles go first; fewer than one round of them have the card to themselves at the end
+  const double rounds = a.tiles < c.slots ? a.stages * (c.idle + c.busy) / 2 + c.ends : double((a.tiles + c.slots - 1) / c.slots) * la;
+  return std::max(rounds, (a.tiles * la + b.tiles * lb) / c.slots + 0.5 * lb);
 }
 
 struct Plan {
