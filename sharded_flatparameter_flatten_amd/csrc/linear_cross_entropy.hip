@@ -79,20 +79,12 @@ __device__ __forceinline__ float factor(const Loss& a) {
   return a.mean ? a.scale / float(*a.count > 1 ? *a.count : 1) : a.scale;
 }
 
-// Every workgroup counts the rows that count before its own, so it knows where they go. The
-// workgroups past `gathers`, if weight is to be copied, give it rows that the products' loads can
-// take: 16-byte pieces, zeros past dim.
-__global__ __launch_bounds__(256) void k_loss_gather(Loss a, int gathers, const uint16_t* w, int64_t w_ld, uint16_t* wc) {
-  if (int(blockIdx.x) >= gathers) {
-    const int64_t row = blockIdx.x - gathers;
-    for (int64_t k = threadIdx.x * 8; k < a.xc_ld - 64; k += 256 * 8)
-      *reinterpret_cast<u32x4*>(wc + row * a.xc_ld + k) = load_piece(w + row * w_ld, k, a.dim);
-    return;
-  }
-  __shared__ int32_t part[4];
-  __shared__ int32_t to[kGatherRows];
+// The rows that count end to end, with their targets and places: kGatherRows of the caller's rows a
+// workgroup of 256. Each counts the rows that count before its own, so it knows where they go.
+__device__ __forceinline__ void gather(const Loss& a, int64_t block, int32_t* shared) {
+  int32_t *part = shared, *to = shared + 4;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row0 = int64_t(blockIdx.x) * kGatherRows;
+  const int64_t row0 = block * kGatherRows;
   int32_t before = 0;
   for (int64_t i = threadIdx.x; i < row0; i += 4 * 256) {
     int64_t t[4];
@@ -142,6 +134,15 @@ __global__ __launch_bounds__(256) void k_loss_gather(Loss a, int gathers, const 
     }
   }
 }
+// The workgroups past `gathers`, if weight is to be copied, give it rows that the products' loads
+// can take: 16-byte pieces, zeros past dim.
+__global__ __launch_bounds__(256) void k_loss_gather(Loss a, int gathers, const uint16_t* w, int64_t w_ld, uint16_t* wc) {
+  __shared__ int32_t shared[4 + kGatherRows];
+  if (int(blockIdx.x) < gathers) return gather(a, blockIdx.x, shared);
+  const int64_t row = blockIdx.x - gathers;
+  for (int64_t k = threadIdx.x * 8; k < a.xc_ld - 64; k += 256 * 8)
+    *reinterpret_cast<u32x4*>(wc + row * a.xc_ld + k) = load_piece(w + row * w_ld, k, a.dim);
+}
 
 // ---------------------------------------------------------------------------
 // the products
@@ -164,7 +165,9 @@ enum Kind { kLogits, kHidden, kWeight };
 // transposing reads of LDS, where 16 lanes take 4 rows x 16 columns and each gets a column's 4
 // values. 32 lanes read 64 bytes of each of 4 rows: the 64-byte blocks of row r are moved by
 // r % 4 (T = 64, whose rows are half as long: by r / 2 % 2), so that they touch each bank once.
-template <bool ACROSS, int T, int PER>
+//
+// LIST: along, and row r of the tile is row list[r] of memory (negative: zeros).
+template <bool ACROSS, int T, int PER, bool LIST = false>
 struct Operand {
   static constexpr int kRowBytes = ACROSS ? 2 * T : 128, kRows = 1024 / kRowBytes;   // rows a load fills
   const char* base;
@@ -176,7 +179,8 @@ struct Operand {
   static constexpr int32_t kMaxBytes = 0x7FFFFF00;   // a descriptor's, past every offset within a stage
 
   // PER loads a wave, an even number where T = 256 or the operand is along.
-  __device__ __forceinline__ void init(const uint16_t* p, int64_t pitch, int64_t elements, int wave, int lane) {
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t pitch, int64_t elements, int wave, int lane,
+                                       const int32_t* list = nullptr) {
     base = reinterpret_cast<const char*>(p);
     ld = pitch * 2;
     bytes = elements * 2;
@@ -187,6 +191,11 @@ struct Operand {
       const int r = odd * kRows + row;
       const int moved = !ACROSS ? c ^ (r >> 1 & 7) : T == 64 ? c ^ (r >> 1 & 1) << 2 : c ^ (r & 3) << 2;
       v[odd] = row * int32_t(ld) + moved * 16;
+      if constexpr (LIST) {
+        static_assert(!ACROSS && PER == 2, "an offset for each of the loads");
+        const int32_t at = list[first * kRows + r];
+        v[odd] = at < 0 ? kMaxBytes : at * int32_t(ld) + moved * 16;
+      }
     }
     last = columns = 0x7FFFFFFF;
   }
@@ -199,7 +208,7 @@ struct Operand {
     const int64_t at = ACROSS ? int64_t(k) * 64 * ld : int64_t(k) * 128;
     const int64_t left = bytes - at;
     const __amdgpu_buffer_rsrc_t r = rsrc(base + at, left < 0 ? 0 : left < kMaxBytes ? left : kMaxBytes);
-    int32_t offset = v[q & 1] + (first + q) * kRows * int32_t(ld);
+    int32_t offset = LIST ? v[q & 1] : v[q & 1] + (first + q) * kRows * int32_t(ld);
     if constexpr (!ACROSS) {
       // chunks at or past `columns` of the last stage: out of bounds, which loads zeros
       const int32_t c = (threadIdx.x & 7) ^ ((((q & 1) * 8 + (threadIdx.x & 63) / 8) >> 1) & 7);
@@ -257,6 +266,13 @@ struct Shape {
   static constexpr int kLds = std::max(S * (TI + TJ) * 128, TJ * kRowJ);
 };
 
+// The tiles: 256, one workgroup a CU; 128 with four stages in LDS, one a CU, for few tiles; 128 with
+// two stages, two a CU, and 64, two a CU, for many.
+using Large = Shape<256, 256, 2, 4, 2>;
+using Deep = Shape<128, 128, 2, 4, 4>;
+using Twin = Shape<128, 128, 2, 4, 2>;
+using Small = Shape<64, 64, 2, 2, 4>;
+
 // Rows of a piece that count. They are known on the device only: grids are for all rows.
 __device__ __forceinline__ int rows_here(const Loss& a, int64_t row0) {
   const int64_t left = *a.count - row0;
@@ -271,11 +287,19 @@ __device__ __forceinline__ int tiles_j_of(const Loss& a, int n) {
   return ((KIND == kWeight ? int(a.vocab) : n) + SH::TJ - 1) / SH::TJ;
 }
 
+// Up to 64 rows, gathered by the workgroup that reads them.
+constexpr int kFew = 64;
+struct Few {
+  int32_t n;                          // rows that count
+  int32_t row[kFew];                  // their places; past them -1
+  int32_t target[kFew];
+};
+
 // Workgroup b runs on XCD b % 8, and tiles that share operands should share its L2: each XCD takes
 // one run of a product's tiles, in bands of 8; `slot` is the place in it. Past the run's end there
 // is nothing to do.
-template <Kind KIND, typename SH>
-__device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits, int slot, char* lds) {
+template <Kind KIND, typename SH, bool FEW = false>
+__device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits, int slot, char* lds, const Few* few = nullptr) {
   constexpr int TI = SH::TI, TJ = SH::TJ, WI = SH::WI, WJ = SH::WJ, S = SH::S, kWaves = WI * WJ;
   constexpr bool kAcrossA = KIND != kLogits, kAcrossB = KIND == kWeight;
   constexpr int MI = TI / WI / 32, NI = TJ / WJ / 32;
@@ -284,8 +308,8 @@ __device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits,
   static_assert(S >= 2 && (S & (S - 1)) == 0 && (S - 1) * kPer < 64, "stages");
   constexpr int kStageA = TI * 128, kStage = (TI + TJ) * 128, kRowJ = SH::kRowJ;
 
-  const int n = rows_here(a, row0);
-  const bool more = *a.count - row0 > a.piece;   // pieces follow
+  const int n = FEW ? few->n : rows_here(a, row0);
+  const bool more = KIND == kWeight && *a.count - row0 > a.piece;   // pieces follow
   const int side_i = int(KIND == kLogits ? a.vocab : a.dim), side_j = KIND == kWeight ? int(a.vocab) : n;
   const int depth = KIND == kLogits ? int(a.dim) : KIND == kHidden ? int(a.vocab) : n;
   const int tiles_i = tiles_i_of<KIND, SH>(a), tiles_j = tiles_j_of<KIND, SH>(a, n);
@@ -306,12 +330,17 @@ __device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits,
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave / WJ, wj = wave % WJ;
   Operand<kAcrossA, TI, kPerA> oa;
-  Operand<kAcrossB, TJ, kPerB> ob;
+  Operand<kAcrossB, TJ, kPerB, FEW> ob;
   const uint16_t* xc = a.xc + row0 * a.xc_ld;
   if constexpr (KIND == kLogits) {
     oa.init(a.wt + int64_t(i0) * a.wt_ld, a.wt_ld, (a.vocab - 1 - i0) * a.wt_ld + a.wt_dim, wave, lane);
     oa.end_at(a.wt_dim, kt);
-    ob.init(xc + int64_t(j0) * a.xc_ld, a.xc_ld, int64_t(n - j0) * a.xc_ld, wave, lane);
+    if constexpr (FEW) {
+      ob.init(a.x, a.x_ld, (a.rows - 1) * a.x_ld + a.dim, wave, lane, few->row);
+      ob.end_at(a.dim, kt);
+    } else {
+      ob.init(xc + int64_t(j0) * a.xc_ld, a.xc_ld, int64_t(n - j0) * a.xc_ld, wave, lane);
+    }
   } else if constexpr (KIND == kHidden) {
     oa.init(a.wt + int64_t(k0) * 64 * a.wt_ld + i0, a.wt_ld, (a.vocab - 1 - int64_t(k0) * 64) * a.wt_ld + a.wt_dim - i0, wave, lane);
     ob.init(a.g + int64_t(j0) * a.g_ld + k0 * 64, a.g_ld, int64_t(n - j0) * a.g_ld - k0 * 64, wave, lane);
@@ -439,7 +468,7 @@ __device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits,
 #pragma unroll
     for (int y = 0; y < NI; ++y) {
       const int j = j0 + jl + 32 * y;
-      const int t = j < n ? a.target[row0 + j] - i0 - il : -1;
+      const int t = j < n ? (FEW ? few->target[j] : a.target[row0 + j]) - i0 - il : -1;
       if (__builtin_amdgcn_ballot_w64(t >= 0 && t < TI / WI) != 0 || i0 + TI > side_i) {
         float right = 0.f;
 #pragma unroll
@@ -533,6 +562,31 @@ template <typename SH>
 __global__ __launch_bounds__(SH::kThreads) void k_loss_logits(Loss a, int64_t row0) {
   __shared__ __attribute__((aligned(1024))) char lds[SH::kLds];
   product<kLogits, SH>(a, row0, 1, blockIdx.x / 8, lds);
+}
+
+// The same for up to 64 rows that the products' loads can take as they are: a tile's workgroup
+// finds the rows that count itself, and what later launches need is gathered beside the tiles, by
+// the workgroups past `tiles` (one token under the 7B head: 59 us with a launch for it, 54 so).
+__global__ __launch_bounds__(Small::kThreads) void k_loss_logits_few(Loss a, int tiles) {
+  static_assert(Small::kThreads == 256 && Small::TJ == kFew, "a gathering workgroup, one column of tiles");
+  // one array: with more of them the compiler waits for the loads into LDS before each read of it
+  __shared__ __attribute__((aligned(1024))) char lds[Small::kLds + sizeof(Few)];
+  if (int(blockIdx.x) >= tiles) return gather(a, blockIdx.x - tiles, reinterpret_cast<int32_t*>(lds));
+  Few& few = *reinterpret_cast<Few*>(lds + Small::kLds);
+  if (threadIdx.x < kFew) {
+    const int lane = threadIdx.x;
+    const int64_t t = lane < a.rows ? a.targets[lane] : -1;
+    const uint64_t have = __builtin_amdgcn_ballot_w64(counts(a, t));
+    const int n = __builtin_popcountll(have), c = __builtin_popcountll(have & ((uint64_t(1) << lane) - 1));
+    if (lane >= n) few.row[lane] = -1;
+    if (counts(a, t)) {
+      few.row[c] = lane;
+      few.target[c] = int32_t(t);
+    }
+    if (lane == 0) few.n = n;
+  }
+  __syncthreads();
+  product<kLogits, Small, true>(a, 0, 1, blockIdx.x / 8, lds, &few);
 }
 
 // The mean, or sum, of the rows' losses, in the order that the workgroup's lanes make; 64 bits.
@@ -636,14 +690,17 @@ __device__ __forceinline__ float row_loss(const Loss& a, int64_t r, int lane, fl
   return ahead > 0.f ? ahead + logf(s + expf(-ahead)) : log1pf(s * expf(ahead));
 }
 
-// Losses only, of few rows: a wave a row, and the mean, in one workgroup.
+// Losses only, of few rows, and the mean, in one workgroup: a wave a row, or all of it for each of
+// up to 4 (whose chunks one wave would read in several rounds).
 constexpr int kFewRows = 32;
 __global__ __launch_bounds__(1024) void k_loss_few(Loss a) {
   __shared__ double part[16];
+  __shared__ f32x2 joined[4][16];
   const int n = *a.count, lane = threadIdx.x & 63;
-  for (int r = threadIdx.x >> 6; r < n; r += 16) {
-    const float loss = row_loss<64>(a, r, lane, a.right[r], nullptr);
-    if (lane == 0) {
+  const bool all = n <= 4;
+  for (int r = all ? 0 : threadIdx.x >> 6; r < n; r += all ? 1 : 16) {
+    const float loss = all ? row_loss<1024>(a, r, threadIdx.x, a.right[r], joined[r & 3]) : row_loss<64>(a, r, lane, a.right[r], nullptr);
+    if ((all ? int(threadIdx.x) : lane) == 0) {
       a.row_loss[r] = loss;
       if (a.losses) a.losses[a.map[r]] = loss;
     }
@@ -709,13 +766,6 @@ __global__ __launch_bounds__(256) void k_loss_rows(Loss a, int64_t row0, int sli
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// The tiles: 256, one workgroup a CU; 128 with four stages in LDS, one a CU, for few tiles; 128 with
-// two stages, two a CU, and 64, two a CU, for many.
-using Large = Shape<256, 256, 2, 4, 2>;
-using Deep = Shape<128, 128, 2, 4, 4>;
-using Twin = Shape<128, 128, 2, 4, 2>;
-using Small = Shape<64, 64, 2, 2, 4>;
-
 // What a tile costs, in microseconds: a stage on a card with little and with much to do, its start
 // and end; tiles that run at once.
 struct Cost {
@@ -760,7 +810,8 @@ struct Plan {
   int logits, grads;                  // tiles, by their places in kCosts
   int splits, splits_w;               // of the contracted axis of dhidden's product and dweight's
   bool weight_first;
-  bool copy;
+  bool copy;                          // weight is copied
+  bool few;                           // the logits' tiles gather their rows themselves
   int64_t count, map, target, xc, wc, row_loss, g, stats, right, part, part_w, acc, bytes;   // workspace offsets
 };
 
@@ -775,11 +826,13 @@ Plan make_plan(const fsdp_linear_cross_entropy_args& n) {
   // loads of 16 bytes at 32-bit offsets within a tile
   p.copy = n.rows > 0 && (n.dim % 8 || n.weight_pitch % 8 || n.weight_pitch > (int64_t(1) << 20) ||
                           reinterpret_cast<uintptr_t>(n.weight) % 16);
+  p.few = n.rows > 0 && n.rows <= kFew && p.pieces == 1 && !p.copy && n.hidden_pitch % 8 == 0 &&
+          n.hidden_pitch <= (int64_t(1) << 20) && reinterpret_cast<uintptr_t>(n.hidden) % 16 == 0;
   const int64_t in_dim = (n.dim + 63) / 64, in_vocab = (n.vocab + 63) / 64, in_rows = (p.piece + 63) / 64;
   double least = HUGE_VAL;
   for (int i = 0; i < kShapes; ++i) {
     const double t = time_of(kCosts[i], {tiles_of(n.vocab, p.piece, kCosts[i].side), in_dim}, {0, 0});
-    if (t < least) {
+    if (p.few ? kCosts[i].side == Small::TI : t < least) {
       p.logits = i;
       least = t;
     }
@@ -906,8 +959,9 @@ fsdp_status run(const fsdp_linear_cross_entropy_args* n, hipStream_t stream) {
   a.scale = static_cast<float>(n->grad_scale);
 
   const int gathers = int(std::max<int64_t>(1, (n->rows + kGatherRows - 1) / kGatherRows));
-  k_loss_gather<<<unsigned(gathers + (p.copy ? n->vocab : 0)), 256, 0, stream>>>(
-      a, gathers, static_cast<const uint16_t*>(n->weight), n->weight_pitch, reinterpret_cast<uint16_t*>(ws + p.wc));
+  if (!p.few)
+    k_loss_gather<<<unsigned(gathers + (p.copy ? n->vocab : 0)), 256, 0, stream>>>(
+        a, gathers, static_cast<const uint16_t*>(n->weight), n->weight_pitch, reinterpret_cast<uint16_t*>(ws + p.wc));
   for (int64_t i = 0; i < p.pieces; ++i) {
     const int64_t row0 = i * p.piece, rows = std::min(p.piece, n->rows - row0);
     a.last = i + 1 == p.pieces;
@@ -916,7 +970,9 @@ fsdp_status run(const fsdp_linear_cross_entropy_args* n, hipStream_t stream) {
         using SH = decltype(sh);
         a.chunk_bits = __builtin_ctz(SH::TI / SH::WI);
         a.chunks = int32_t((n->vocab - 1) >> a.chunk_bits) + 1;
-        k_loss_logits<SH><<<unsigned(round_up(tiles_of(n->vocab, rows, SH::TI), 8)), SH::kThreads, 0, stream>>>(a, row0);
+        const unsigned tiles = unsigned(round_up(tiles_of(n->vocab, rows, SH::TI), 8));
+        if (p.few) k_loss_logits_few<<<tiles + gathers, SH::kThreads, 0, stream>>>(a, int(tiles));
+        else k_loss_logits<SH><<<tiles, SH::kThreads, 0, stream>>>(a, row0);
       });
       if (!a.grads && n->rows <= kFewRows) {
         k_loss_few<<<1, 1024, 0, stream>>>(a);
