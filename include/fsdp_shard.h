@@ -503,8 +503,9 @@ fsdp_status fsdp_dropout(const fsdp_dropout_args* args, hipStream_t stream);
  * operands with fp32 sums, for which softmax(z) - onehot is rounded to bf16 (2^-8 of each value,
  * the target's from a difference that does not cancel). A row with a NaN logit gives NaN, one
  * with an infinite logit NaN or its limit. dhidden or dweight may be NULL; what is not asked for is not computed.
- * Rows are worked off in pieces of `piece` (0: as many as a scratch of 1 GiB holds); with
- * more than one piece dweight's sums are kept in fp32 in the workspace between them.
+ * Rows are worked off in pieces of `piece` (0: chosen for a scratch of 2 bytes a logit of 1 GiB,
+ * or of 1 GiB and what dweight's sums would take); with more than one piece dweight's sums are kept
+ * in fp32 in the workspace between them.
  * `workspace`: device memory, 256-byte aligned, of as many bytes as
  * fsdp_linear_cross_entropy_workspace says for the same arguments (of pointers only alignment
  * counts, and whether dhidden and dweight are NULL); its contents need not be kept from call to call. The same

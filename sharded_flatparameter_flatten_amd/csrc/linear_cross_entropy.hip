@@ -40,7 +40,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kGatherRows = 8;        // rows a workgroup gathers
-constexpr int64_t kScratch = int64_t(1) << 30;
+constexpr int64_t kScratch = int64_t(1) << 30;       // bytes of P and G, if dweight's sums take no more
 constexpr int64_t kMaxProduct = int64_t(1) << 35;   // elements of an operand or a result: grids stay below 2^32 lanes
 
 // What the kernels of one call share.
@@ -135,13 +135,20 @@ __device__ __forceinline__ void gather(const Loss& a, int64_t block, int32_t* sh
   }
 }
 // The workgroups past `gathers`, if weight is to be copied, give it rows that the products' loads
-// can take: 16-byte pieces, zeros past dim.
+// can take: 16-byte pieces, zeros past dim. A wave a row.
 __global__ __launch_bounds__(256) void k_loss_gather(Loss a, int gathers, const uint16_t* w, int64_t w_ld, uint16_t* wc) {
   __shared__ int32_t shared[4 + kGatherRows];
   if (int(blockIdx.x) < gathers) return gather(a, blockIdx.x, shared);
-  const int64_t row = blockIdx.x - gathers;
-  for (int64_t k = threadIdx.x * 8; k < a.xc_ld - 64; k += 256 * 8)
-    *reinterpret_cast<u32x4*>(wc + row * a.xc_ld + k) = load_piece(w + row * w_ld, k, a.dim);
+  const int64_t row = int64_t(blockIdx.x - gathers) * 4 + threadIdx.x / 64, end = a.xc_ld - 64;
+  if (row >= a.vocab) return;
+  for (int64_t k = (threadIdx.x & 63) * 8; k < end; k += 4 * 512) {
+    u32x4 q[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) q[u] = load_piece(w + row * w_ld, k + u * 512, a.dim);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (k + u * 512 < end) *reinterpret_cast<u32x4*>(wc + row * a.xc_ld + k + u * 512) = q[u];
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -820,9 +827,12 @@ Plan make_plan(const fsdp_linear_cross_entropy_args& n) {
   const bool grads = n.dhidden || n.dweight;
   p.g_ld = round_up(n.vocab, 256) + 64;
   p.xc_ld = round_up(n.dim, 64) + 64;
-  p.piece = n.piece > 0 ? n.piece : std::max<int64_t>(256, kScratch / (2 * p.g_ld) / 256 * 256);
+  // A second piece needs dweight's sums in fp32: as much scratch may be used before there is one.
+  const int64_t scratch = kScratch + (n.dweight ? n.vocab * n.dim * 4 : 0);
+  const int64_t most = n.piece > 0 ? n.piece : std::max<int64_t>(256, scratch / (2 * p.g_ld) / 256 * 256);
+  p.pieces = std::max<int64_t>(1, (n.rows + most - 1) / most);
+  p.piece = n.piece > 0 ? n.piece : round_up((n.rows + p.pieces - 1) / p.pieces, 256);   // pieces of a size
   p.piece = std::max<int64_t>(1, std::min(p.piece, n.rows));
-  p.pieces = std::max<int64_t>(1, (n.rows + p.piece - 1) / p.piece);
   // loads of 16 bytes at 32-bit offsets within a tile
   p.copy = n.rows > 0 && (n.dim % 8 || n.weight_pitch % 8 || n.weight_pitch > (int64_t(1) << 20) ||
                           reinterpret_cast<uintptr_t>(n.weight) % 16);
@@ -960,7 +970,7 @@ fsdp_status run(const fsdp_linear_cross_entropy_args* n, hipStream_t stream) {
 
   const int gathers = int(std::max<int64_t>(1, (n->rows + kGatherRows - 1) / kGatherRows));
   if (!p.few)
-    k_loss_gather<<<unsigned(gathers + (p.copy ? n->vocab : 0)), 256, 0, stream>>>(
+    k_loss_gather<<<unsigned(gathers + (p.copy ? (n->vocab + 3) / 4 : 0)), 256, 0, stream>>>(
         a, gathers, static_cast<const uint16_t*>(n->weight), n->weight_pitch, reinterpret_cast<uint16_t*>(ws + p.wc));
   for (int64_t i = 0; i < p.pieces; ++i) {
     const int64_t row0 = i * p.piece, rows = std::min(p.piece, n->rows - row0);
