@@ -28,6 +28,20 @@ def test_dropout(lib, rows, dim, extra, shift, dtype, residual):
         assert out.intact()
 
 
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("rows,dim,extra", [(9000, 2056, 0), (3000, 8200, 8), (1100, 20001, 7)])
+def test_large(lib, rows, dim, extra, dtype, residual):
+    """Outputs that go past L2, and ones of that size that cannot."""
+    x = E.rows_of(rows, dim, dim + extra, 0, dtype, 1.0, 1)
+    res = E.rows_of(rows, dim, dim + extra, 0, dtype, 2.0, 2) if residual else None
+    out = E.Guarded(rows, dim, dim + extra, 0, dtype)
+    lib.dropout(x, out.t, 0.1, 7, 8, residual=res)
+    torch.cuda.synchronize()
+    assert E.same_bits(out.t, E.dropout(x, 0.1, 7, 8, res))
+    assert out.intact()
+
+
 @pytest.mark.parametrize("dtype", [BF, F])
 def test_in_place(lib, dtype):
     x, res = torch.randn(37, 200).to(dtype), torch.randn(37, 200).to(dtype)

@@ -115,6 +115,38 @@ def test_backward_of_frequent_tokens(lib, dtype):
                 assert E.near(dw, want, off, E.HALF[dtype]), (vocab, dim, add)
 
 
+@pytest.mark.parametrize("dtype,n,vocab,dim", [(BF, 3000, 12000, 2056), (F, 2500, 30001, 1028), (BF, 9000, 7000, 4096), (F, 40, 9000, 1500),
+                                               (BF, 100, 40000, 2048), (BF, 2048, 5000, 1024), (BF, 2049, 5000, 1024)])
+def test_backward_large(lib, dtype, n, vocab, dim):
+    """Outputs that go past L2, whose zeros are written by every launch; frequent tokens at both
+    ends of the vocabulary."""
+    gen = torch.Generator().manual_seed(n)
+    t = torch.randint(0, vocab, (n,), generator=gen)
+    t[::3] = torch.tensor([0, 1, vocab - 1, vocab - 2, vocab // 2])[torch.randint(0, 5, (len(t[::3]),), generator=gen)]
+    t = t.cuda()
+    dy = E.rows_of(n, dim, dim, 0, dtype, 1e-2, 3)
+    for add in (False, True):
+        dw = torch.full((vocab, dim), 0.25 if add else float("nan"), dtype=dtype, device="cuda")
+        back(lib, t, dy, dw, scale=2.0, accumulate=add)
+        torch.cuda.synchronize()
+        want, off, _ = E.embedding_backward(t, dy, vocab, 2.0, torch.full_like(dw, 0.25) if add else None)
+        assert E.near(dw, want, off, E.HALF[dtype])
+        del want, off
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("n,dim,extra", [(9000, 2056, 0), (3000, 8200, 8), (40000, 520, 0), (1200, 20001, 0)])
+def test_forward_large(lib, dtype, n, dim, extra):
+    w = E.rows_of(500, dim, dim, 0, dtype, 1.0, 1)
+    t = tokens_of(n, 500, "outside")
+    out = E.Guarded(n, dim, dim + extra, 0, dtype)
+    lib.embedding(t, w, out.t)
+    torch.cuda.synchronize()
+    ok = (t >= 0) & (t < 500)
+    assert torch.equal(out.t, torch.where(ok[:, None], w[t.clamp(0, 499)], torch.zeros((), dtype=dtype, device="cuda")))
+    assert out.intact()
+
+
 def test_backward_order(lib):
     """Equal tokens are summed so that the same inputs give the same bits, and values that are not
     numbers reach only their own row."""

@@ -67,6 +67,43 @@ def test_loss(lib, rows, vocab, dim, extra, shift, skip):
     check(lib, x, w, t, extra, shift)
 
 
+# enough for every tile: many rows and tokens, long rows, few rows and a long vocabulary, unaligned ones
+@pytest.mark.parametrize("rows,vocab,dim,extra,shift,piece", [
+    (4100, 4200, 136, 0, 0, 0), (2100, 2100, 4104, 0, 0, 0), (2100, 2100, 4104, 8, 0, 1100), (1500, 5003, 1027, 9, 1, 0),
+    (5000, 300, 2056, 0, 0, 0), (300, 9001, 2050, 0, 0, 0), (64, 20000, 320, 0, 0, 0), (1300, 3000, 600, 0, 0, 0),
+    (9000, 520, 72, 0, 0, 4000), (513, 30000, 520, 0, 8, 0)])
+def test_larger(lib, rows, vocab, dim, extra, shift, piece):
+    x, w, t = inputs(rows, vocab, dim, extra, shift, 0.1, seed=rows)
+    check(lib, x, w, t, extra, shift, piece=piece)
+
+
+def test_every_row_once(lib):
+    """Values that no product rounds, so that every element has to be right: each row's softmax is
+    one or zero, the gradients' sums are small whole numbers."""
+    for rows, vocab, dim in ((700, 600, 512), (5000, 5100, 264), (2600, 640, 4096)):
+        x, w = torch.zeros(rows, dim, dtype=BF, device="cuda"), torch.zeros(vocab, dim, dtype=BF, device="cuda")
+        r, v = torch.arange(rows, device="cuda"), torch.arange(vocab, device="cuda")
+        w[v, v % dim] = 256.0                       # logits of 0 and 65536
+        x[r, (7 * r) % min(dim, vocab)] = 256.0
+        best = (7 * r) % min(dim, vocab)
+        t = torch.where(r % 3 == 0, -100, (best + 1 + r) % min(dim, vocab))
+        if vocab > dim:                             # several of the vocabulary alike: the first only
+            w[dim:] = 0.0
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        losses = torch.empty(rows, device="cuda")
+        call(lib, x, w, t, dx, dw, losses, reduction="sum")
+        miss = (t >= 0) & (t != best)
+        assert torch.equal(losses, miss * 65536.0)
+        want = torch.zeros(rows, dim, device="cuda")
+        want[r[miss], best[miss]] = 256.0
+        want[r[miss], t[miss]] = -256.0
+        assert torch.equal(dx.float(), want)
+        sums = torch.zeros(vocab, dim, device="cuda")
+        sums.index_put_((best[miss], best[miss]), torch.tensor(256.0, device="cuda"), accumulate=True)
+        sums.index_put_((t[miss], best[miss]), torch.tensor(-256.0, device="cuda"), accumulate=True)
+        assert torch.equal(dw, sums.to(BF))
+
+
 @pytest.mark.parametrize("grads", ["none", "dhidden", "dweight"])
 @pytest.mark.parametrize("rows,vocab,dim", [(1, 700, 64), (19, 300, 100), (70, 129, 65), (300, 600, 264)])
 def test_what_is_asked_for(lib, rows, vocab, dim, grads):
@@ -239,6 +276,20 @@ def test_offsets_past_32_bits(lib):
     a = call(lib, wide[:, :dim], far[:, :dim], t, dx, dw)
     b = call(lib, x, w, t, ref_x, ref_w)
     assert E.same_bits(a, b) and E.same_bits(dx, ref_x) and E.same_bits(dw, ref_w)
+
+
+def test_wide_pitches(lib):
+    """Rows of weight further apart than a tile's 32-bit offsets reach."""
+    rows, vocab, dim, pitch = 70, 150, 72, (1 << 20) + 64
+    x, w, t = inputs(rows, vocab, dim, seed=17)
+    far = torch.empty(vocab, pitch, dtype=BF, device="cuda")
+    far[:, :dim] = w
+    dx, dw, ref_x, ref_w = (torch.empty_like(a) for a in (x, w, x, w))
+    a, b = call(lib, x, far[:, :dim], t, dx, dw), call(lib, x, w, t, ref_x, ref_w)
+    assert E.same_bits(a, b) and E.same_bits(dx, ref_x) and E.same_bits(dw, ref_w)
+    few = far[:40, :dim]                            # rows of hidden too
+    a, b = call(lib, few, w, t[:40], dx[:40]), call(lib, few.contiguous(), w, t[:40], ref_x[:40])
+    assert E.same_bits(a, b) and E.same_bits(dx[:40], ref_x[:40])
 
 
 def test_refuses(lib):
