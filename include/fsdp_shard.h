@@ -449,7 +449,8 @@ fsdp_status fsdp_embedding(const fsdp_embedding_args* args, hipStream_t stream);
  * the rows of absent tokens are neither read nor written: the gradient of an embedding
  * that is also the head is the head's with this one added. The same inputs give the same bits.
  * `workspace`: device memory, 16-byte aligned, of fsdp_embedding_backward_workspace bytes; its
- * contents need not be kept from call to call. rows == 0 writes zeros (with accumulate: nothing).
+ * contents need not be kept from call to call; calls that may run at once (two streams, two
+ * graphs) take one each. rows == 0 writes zeros (with accumulate: nothing).
  * If the runtime refuses a launch, those before it stay. */
 typedef struct {
   const int64_t* tokens;      /* rows */
@@ -508,7 +509,8 @@ fsdp_status fsdp_dropout(const fsdp_dropout_args* args, hipStream_t stream);
  * in fp32 in the workspace between them.
  * `workspace`: device memory, 256-byte aligned, of as many bytes as
  * fsdp_linear_cross_entropy_workspace says for the same arguments (of pointers only alignment
- * counts, and whether dhidden and dweight are NULL); its contents need not be kept from call to call. The same
+ * counts, and whether dhidden and dweight are NULL); its contents need not be kept from call to call, and calls
+ * that may run at once take one each. The same
  * inputs give the same bits. rows, vocab < 2^22, dim <= 2^20, and the product of any two (of the rows:
  * those of a piece) at most 2^35. If the runtime refuses a launch,
  * those before it stay. */
