@@ -47,7 +47,8 @@ __device__ __forceinline__ u32x4 philox(uint32_t group, uint32_t row, uint64_t o
   return c;
 }
 
-// One piece a lane: with loops over a row, two or four pieces a lane, every size was slower (8192 rows
+// Bound by HBM: with 2 rounds of the generator instead of 10 the same times (8192 rows of 11008, 60 us,
+// 6.0 TB/s). One piece a lane: with loops over a row, two or four pieces a lane, every size was slower (8192 rows
 // of 4096 with a residual: 35 us, 37 and 38). An fp32 piece is half of a block's 8 columns: two lanes
 // then make the same block, on twice the bytes a column.
 template <typename T, bool RES, Rows HOW>

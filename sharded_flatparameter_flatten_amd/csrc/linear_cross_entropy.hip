@@ -51,7 +51,7 @@ struct Loss {
   int32_t* count;                     // rows that count
   int32_t* map;                       // their places among the caller's
   int32_t* target;                    // and targets
-  uint16_t* xc;                       // and values, dim_pad + 64 apart, zeros past dim
+  uint16_t* xc;                       // and values, dim_pad + 64 apart, zeros past dim (NULL: not needed)
   float* row_loss;
   float* loss;
   float* losses;                      // or NULL
@@ -80,23 +80,27 @@ __device__ __forceinline__ float factor(const Loss& a) {
 }
 
 // The rows that count end to end, with their targets and places: kGatherRows of the caller's rows a
-// workgroup of 256. Each counts the rows that count before its own, so it knows where they go.
+// workgroup. Each counts the rows that count before its own, so it knows where they go.
+template <int WAVES>
 __device__ __forceinline__ void gather(const Loss& a, int64_t block, int32_t* shared) {
-  int32_t *part = shared, *to = shared + 4;
+  constexpr int kLanes = 64 * WAVES;
+  int32_t *part = shared, *to = shared + WAVES;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row0 = block * kGatherRows;
   int32_t before = 0;
-  for (int64_t i = threadIdx.x; i < row0; i += 4 * 256) {
+  for (int64_t i = threadIdx.x; i < row0; i += 4 * kLanes) {
     int64_t t[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) t[u] = i + u * 256 < row0 ? a.targets[i + u * 256] : -1;
+    for (int u = 0; u < 4; ++u) t[u] = i + u * kLanes < row0 ? a.targets[i + u * kLanes] : -1;
 #pragma unroll
     for (int u = 0; u < 4; ++u) before += counts(a, t[u]);
   }
   before = wave_sum(before);
   if (lane == 0) part[wave] = before;
   __syncthreads();
-  const int32_t base = part[0] + part[1] + part[2] + part[3];
+  int32_t base = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) base += part[w];
   if (wave == 0) {
     const int64_t row = row0 + lane;
     const int64_t t = lane < kGatherRows && row < a.rows ? a.targets[row] : -1;
@@ -110,7 +114,7 @@ __device__ __forceinline__ void gather(const Loss& a, int64_t block, int32_t* sh
     if (lane == 0 && row0 + kGatherRows >= a.rows) *a.count = base + __builtin_popcountll(have);
   }
   __syncthreads();
-  for (int r = wave; r < kGatherRows; r += 4) {
+  for (int r = wave; r < kGatherRows; r += WAVES) {
     const int64_t row = row0 + r;
     if (row >= a.rows) return;
     const int32_t c = to[r];
@@ -121,6 +125,7 @@ __device__ __forceinline__ void gather(const Loss& a, int64_t block, int32_t* sh
       for (int64_t k = lane * 8; k < a.dim; k += 512) store_piece(a.dx + row * a.dx_ld, k, a.dim, zero);
       continue;
     }
+    if (!a.xc) continue;
     const uint16_t* x = a.x + row * a.x_ld;
     uint16_t* xc = a.xc + c * a.xc_ld;
     const int64_t end = a.xc_ld - 64;
@@ -138,7 +143,7 @@ __device__ __forceinline__ void gather(const Loss& a, int64_t block, int32_t* sh
 // can take: 16-byte pieces, zeros past dim. A wave a row.
 __global__ __launch_bounds__(256) void k_loss_gather(Loss a, int gathers, const uint16_t* w, int64_t w_ld, uint16_t* wc) {
   __shared__ int32_t shared[4 + kGatherRows];
-  if (int(blockIdx.x) < gathers) return gather(a, blockIdx.x, shared);
+  if (int(blockIdx.x) < gathers) return gather<4>(a, blockIdx.x, shared);
   const int64_t row = int64_t(blockIdx.x - gathers) * 4 + threadIdx.x / 64, end = a.xc_ld - 64;
   if (row >= a.vocab) return;
   for (int64_t k = (threadIdx.x & 63) * 8; k < end; k += 4 * 512) {
@@ -299,19 +304,69 @@ __device__ __forceinline__ int tiles_j_of(const Loss& a, int n) {
   return ((KIND == kWeight ? int(a.vocab) : n) + SH::TJ - 1) / SH::TJ;
 }
 
-// Up to 64 rows, gathered by the workgroup that reads them.
-constexpr int kFew = 64;
+// Up to kFewMax rows, found by the workgroup that reads them: it counts all that count, and lists
+// those of its tile.
+constexpr int kFewMax = 2048;
+template <typename SH>
 struct Few {
-  int32_t n;                          // rows that count
-  int32_t row[kFew];                  // their places; past them -1
-  int32_t target[kFew];
+  static constexpr int kWaves = SH::WI * SH::WJ, kLoads = kFewMax / 64 / kWaves;
+  int32_t counted[kWaves];            // by each wave, in its stretch of the rows
+  int32_t row[SH::TJ];                // the places of the tile's rows; past them -1
+  int32_t target[SH::TJ];
+};
+template <typename SH>
+struct Finder {
+  using List = Few<SH>;
+  int32_t t[List::kLoads];            // this lane's targets; -1: does not count
+  int32_t begin, before, n;           // of the wave's stretch; rows that count before it; of all
+  List* list;
+
+  __device__ __forceinline__ void count(const Loss& a, List* to) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    list = to;
+    const int rows = int(a.rows), stretch = (rows + 64 * List::kWaves - 1) / (64 * List::kWaves) * 64;
+    begin = wave * stretch;
+    int32_t own = 0;
+#pragma unroll
+    for (int u = 0; u < List::kLoads; ++u) {
+      const int i = begin + u * 64 + lane;
+      const int64_t target = u * 64 < stretch && i < rows ? a.targets[i] : -1;
+      t[u] = counts(a, target) ? int32_t(target) : -1;
+      own += __builtin_popcountll(__builtin_amdgcn_ballot_w64(t[u] >= 0));
+    }
+    if (lane == 0) list->counted[wave] = own;
+    for (int j = threadIdx.x; j < SH::TJ; j += SH::kThreads) list->row[j] = -1;
+    __syncthreads();
+    before = n = 0;
+#pragma unroll
+    for (int w = 0; w < List::kWaves; ++w) {
+      before += w < wave ? list->counted[w] : 0;
+      n += list->counted[w];
+    }
+  }
+  __device__ __forceinline__ void find(int j0) const {
+    const int lane = threadIdx.x & 63;
+    int32_t at = before - j0;
+#pragma unroll
+    for (int u = 0; u < List::kLoads; ++u) {
+      const uint64_t have = __builtin_amdgcn_ballot_w64(t[u] >= 0);
+      const int32_t j = at + __builtin_popcountll(have & ((uint64_t(1) << lane) - 1));
+      if (t[u] >= 0 && j >= 0 && j < SH::TJ) {
+        list->row[j] = begin + u * 64 + lane;
+        list->target[j] = t[u];
+      }
+      at += __builtin_popcountll(have);
+    }
+    __syncthreads();
+  }
 };
 
 // Workgroup b runs on XCD b % 8, and tiles that share operands should share its L2: each XCD takes
 // one run of a product's tiles, in bands of 8; `slot` is the place in it. Past the run's end there
 // is nothing to do.
 template <Kind KIND, typename SH, bool FEW = false>
-__device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits, int slot, char* lds, const Few* few = nullptr) {
+__device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits, int slot, char* lds,
+                                        const Finder<SH>* few = nullptr) {
   constexpr int TI = SH::TI, TJ = SH::TJ, WI = SH::WI, WJ = SH::WJ, S = SH::S, kWaves = WI * WJ;
   constexpr bool kAcrossA = KIND != kLogits, kAcrossB = KIND == kWeight;
   constexpr int MI = TI / WI / 32, NI = TJ / WJ / 32;
@@ -348,7 +403,8 @@ __device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits,
     oa.init(a.wt + int64_t(i0) * a.wt_ld, a.wt_ld, (a.vocab - 1 - i0) * a.wt_ld + a.wt_dim, wave, lane);
     oa.end_at(a.wt_dim, kt);
     if constexpr (FEW) {
-      ob.init(a.x, a.x_ld, (a.rows - 1) * a.x_ld + a.dim, wave, lane, few->row);
+      few->find(j0);
+      ob.init(a.x, a.x_ld, (a.rows - 1) * a.x_ld + a.dim, wave, lane, few->list->row);
       ob.end_at(a.dim, kt);
     } else {
       ob.init(xc + int64_t(j0) * a.xc_ld, a.xc_ld, int64_t(n - j0) * a.xc_ld, wave, lane);
@@ -480,7 +536,7 @@ __device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits,
 #pragma unroll
     for (int y = 0; y < NI; ++y) {
       const int j = j0 + jl + 32 * y;
-      const int t = j < n ? (FEW ? few->target[j] : a.target[row0 + j]) - i0 - il : -1;
+      const int t = j < n ? (FEW ? few->list->target[j - j0] : a.target[row0 + j]) - i0 - il : -1;
       if (__builtin_amdgcn_ballot_w64(t >= 0 && t < TI / WI) != 0 || i0 + TI > side_i) {
         float right = 0.f;
 #pragma unroll
@@ -576,29 +632,18 @@ __global__ __launch_bounds__(SH::kThreads) void k_loss_logits(Loss a, int64_t ro
   product<kLogits, SH>(a, row0, 1, blockIdx.x / 8, lds);
 }
 
-// The same for up to 64 rows that the products' loads can take as they are: a tile's workgroup
-// finds the rows that count itself, and what later launches need is gathered beside the tiles, by
-// the workgroups past `tiles` (one token under the 7B head: 59 us with a launch for it, 54 so).
-__global__ __launch_bounds__(Small::kThreads) void k_loss_logits_few(Loss a, int tiles) {
-  static_assert(Small::kThreads == 256 && Small::TJ == kFew, "a gathering workgroup, one column of tiles");
+// The same for up to kFewMax rows that the products' loads can take as they are: a tile's workgroup
+// finds its rows itself, and what later launches need is gathered beside the tiles, by the workgroups
+// past `tiles` (one token under the 7B head: 59 us with a launch for it, 55 so; 512 rows of 256, a
+// vocabulary of 1024, with gradients: 22.7 and 18.5).
+template <typename SH>
+__global__ __launch_bounds__(SH::kThreads) void k_loss_logits_few(Loss a, int tiles) {
   // one array: with more of them the compiler waits for the loads into LDS before each read of it
-  __shared__ __attribute__((aligned(1024))) char lds[Small::kLds + sizeof(Few)];
-  if (int(blockIdx.x) >= tiles) return gather(a, blockIdx.x - tiles, reinterpret_cast<int32_t*>(lds));
-  Few& few = *reinterpret_cast<Few*>(lds + Small::kLds);
-  if (threadIdx.x < kFew) {
-    const int lane = threadIdx.x;
-    const int64_t t = lane < a.rows ? a.targets[lane] : -1;
-    const uint64_t have = __builtin_amdgcn_ballot_w64(counts(a, t));
-    const int n = __builtin_popcountll(have), c = __builtin_popcountll(have & ((uint64_t(1) << lane) - 1));
-    if (lane >= n) few.row[lane] = -1;
-    if (counts(a, t)) {
-      few.row[c] = lane;
-      few.target[c] = int32_t(t);
-    }
-    if (lane == 0) few.n = n;
-  }
-  __syncthreads();
-  product<kLogits, Small, true>(a, 0, 1, blockIdx.x / 8, lds, &few);
+  __shared__ __attribute__((aligned(1024))) char lds[SH::kLds + sizeof(Few<SH>)];
+  if (int(blockIdx.x) >= tiles) return gather<SH::kThreads / 64>(a, blockIdx.x - tiles, reinterpret_cast<int32_t*>(lds));
+  Finder<SH> few;
+  few.count(a, reinterpret_cast<Few<SH>*>(lds + SH::kLds));
+  product<kLogits, SH, true>(a, 0, 1, blockIdx.x / 8, lds, &few);
 }
 
 // The mean, or sum, of the rows' losses, in the order that the workgroup's lanes make; 64 bits.
@@ -841,17 +886,17 @@ Plan make_plan(const fsdp_linear_cross_entropy_args& n) {
   // loads of 16 bytes at 32-bit offsets within a tile
   p.copy = n.rows > 0 && (n.dim % 8 || n.weight_pitch % 8 || n.weight_pitch > (int64_t(1) << 20) ||
                           reinterpret_cast<uintptr_t>(n.weight) % 16);
-  p.few = n.rows > 0 && n.rows <= kFew && p.pieces == 1 && !p.copy && n.hidden_pitch % 8 == 0 &&
-          n.hidden_pitch <= (int64_t(1) << 20) && reinterpret_cast<uintptr_t>(n.hidden) % 16 == 0;
   const int64_t in_dim = (n.dim + 63) / 64, in_vocab = (n.vocab + 63) / 64, in_rows = (p.piece + 63) / 64;
   double least = HUGE_VAL;
   for (int i = 0; i < kShapes; ++i) {
     const double t = time_of(kCosts[i], {tiles_of(n.vocab, p.piece, kCosts[i].side), in_dim}, {0, 0});
-    if (p.few ? kCosts[i].side == Small::TI : t < least) {
+    if (t < least) {
       p.logits = i;
       least = t;
     }
   }
+  p.few = p.logits > 0 && n.rows > 0 && n.rows <= kFewMax && p.pieces == 1 && !p.copy && n.hidden_pitch % 8 == 0 &&
+          n.rows * n.hidden_pitch < (int64_t(1) << 29) && reinterpret_cast<uintptr_t>(n.hidden) % 16 == 0;
   p.splits = p.splits_w = 1;
   least = HUGE_VAL;
   for (int i = 0; i < kShapes && grads; ++i) {
@@ -948,7 +993,7 @@ fsdp_status run(const fsdp_linear_cross_entropy_args* n, hipStream_t stream) {
   a.count = reinterpret_cast<int32_t*>(ws + p.count);
   a.map = reinterpret_cast<int32_t*>(ws + p.map);
   a.target = reinterpret_cast<int32_t*>(ws + p.target);
-  a.xc = reinterpret_cast<uint16_t*>(ws + p.xc);
+  a.xc = p.few && !n->dweight ? nullptr : reinterpret_cast<uint16_t*>(ws + p.xc);
   a.row_loss = reinterpret_cast<float*>(ws + p.row_loss);
   a.loss = n->loss;
   a.losses = n->losses;
@@ -986,8 +1031,10 @@ fsdp_status run(const fsdp_linear_cross_entropy_args* n, hipStream_t stream) {
         a.chunk_bits = __builtin_ctz(SH::TI / SH::WI);
         a.chunks = int32_t((n->vocab - 1) >> a.chunk_bits) + 1;
         const unsigned tiles = unsigned(round_up(tiles_of(n->vocab, rows, SH::TI), 8));
-        if (p.few) k_loss_logits_few<<<tiles + gathers, SH::kThreads, 0, stream>>>(a, int(tiles));
-        else k_loss_logits<SH><<<tiles, SH::kThreads, 0, stream>>>(a, row0);
+        if constexpr (SH::TI < 256) {             // the largest tile has enough to do for a launch more
+          if (p.few) return k_loss_logits_few<SH><<<tiles + gathers, SH::kThreads, 0, stream>>>(a, int(tiles));
+        }
+        k_loss_logits<SH><<<tiles, SH::kThreads, 0, stream>>>(a, row0);
       });
       if (!a.grads && n->rows <= kFewRows) {
         k_loss_few<<<1, 1024, 0, stream>>>(a);
