@@ -381,9 +381,9 @@ __device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits,
   const int depth = KIND == kLogits ? int(a.dim) : KIND == kHidden ? int(a.vocab) : n;
   const int tiles_i = tiles_i_of<KIND, SH>(a), tiles_j = tiles_j_of<KIND, SH>(a, n);
   if (KIND == kWeight && row0 > 0 && n == 0) return;
-  const int total = tiles_i * tiles_j * splits, run = (total + 7) / 8;
+  const int all = tiles_i * tiles_j * splits, run = (all + 7) / 8;
   int local = int(blockIdx.x % 8) * run + slot;
-  if (slot >= run || local >= total) return;
+  if (slot >= run || local >= all) return;
   int k0 = 0, kt = (depth + 63) / 64, z = 0, ti, tj;
   if (KIND != kLogits && splits > 1) {
     z = divide(local, tiles_i * tiles_j);
@@ -433,6 +433,25 @@ __device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits,
     for (int y = 0; y < NI; ++y)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.f;
+  // The logits' sums in two levels, where registers allow: 8 stages' sums are added to the total. A
+  // sum of 4096 products that grows to 15 takes 256 roundings of its last place otherwise, and what a
+  // sure row loses is off by that: 4e-6 of itself, 1e-7 to 1e-6 so. (With two stages in LDS the
+  // registers would cost one of the two workgroups on a CU: odd sizes 20 -> 31 us.)
+  constexpr bool kLevels = KIND == kLogits && TI < 256 && S > 2;
+  f32x16 total[kLevels ? MI : 1][kLevels ? NI : 1] = {};
+  auto add_level = [&] {
+    if constexpr (kLevels) {
+#pragma unroll
+      for (int x = 0; x < MI; ++x)
+#pragma unroll
+        for (int y = 0; y < NI; ++y)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            total[x][y][e] += acc[x][y][e];
+            acc[x][y][e] = 0.f;
+          }
+    }
+  };
   // dweight's sums go on from piece to piece: registers as they are, a tile's in one place.
   const __amdgpu_buffer_rsrc_t sums = rsrc(a.acc + int64_t(ti * tiles_j + tj) * (TI * TJ), TI * TJ * 4);
   const int own_sums = threadIdx.x * 16;
@@ -511,6 +530,7 @@ __device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits,
       wait_loads<(S - 2) * kPer>();
       meet();
       half(k, upper, true_type{}, true_type{});
+      if (kLevels && (k & 7) == 7) add_level();
     }
     for (; k + 1 < kt; ++k) {
       half(k, lower, false_type{}, true_type{});
@@ -522,6 +542,13 @@ __device__ __forceinline__ void product(const Loss& a, int64_t row0, int splits,
     wait_loads<0>();
     meet();
     half(k, upper, false_type{}, false_type{});
+  }
+  if constexpr (kLevels) {
+    add_level();
+#pragma unroll
+    for (int x = 0; x < MI; ++x)
+#pragma unroll
+      for (int y = 0; y < NI; ++y) acc[x][y] = total[x][y];
   }
 
   // A lane holds, of column j = jl + 32 y, the rows i = il + 32 x + 8 g + e in acc[x][y][4 g + e].
@@ -890,7 +917,8 @@ Plan make_plan(const fsdp_linear_cross_entropy_args& n) {
   double least = HUGE_VAL;
   for (int i = 0; i < kShapes; ++i) {
     const double t = time_of(kCosts[i], {tiles_of(n.vocab, p.piece, kCosts[i].side), in_dim}, {0, 0});
-    if (t < least) {
+    // up to 64 rows: the others would be half empty, and this one's sums are the most exact
+    if (p.piece <= Small::TJ ? kCosts[i].side == Small::TJ : t < least) {
       p.logits = i;
       least = t;
     }
