@@ -504,6 +504,8 @@ fsdp_status fsdp_dropout(const fsdp_dropout_args* args, hipStream_t stream);
  * operands with fp32 sums, for which softmax(z) - onehot is rounded to bf16 (2^-8 of each value,
  * the target's from a difference that does not cancel). A row with a NaN logit gives NaN, one
  * with an infinite logit NaN or its limit. dhidden or dweight may be NULL; what is not asked for is not computed.
+ * A weight whose rows are not a multiple of 8 long, do not begin on 16 bytes or are more than 2^20
+ * apart is copied into the workspace first.
  * Rows are worked off in pieces of `piece` (0: chosen for a scratch of 2 bytes a logit of 1 GiB,
  * or of 1 GiB and what dweight's sums would take); with more than one piece dweight's sums are kept
  * in fp32 in the workspace between them.
